@@ -1,0 +1,79 @@
+// Internal interface between the key/value cache's C-ABI host code (kvc.cpp)
+// and its gfx950 kernels (kv_append.hip, kv_attend.hip).
+#pragma once
+
+#include "agemm_internal.h"
+#include "kv_layout.h"
+
+namespace agemm {
+
+// Cases of the error word (ErrWord.code) of the cache's kernels; `tile` is the
+// index of the token or sequence, `seen` the value met, `target` its bound.
+enum KvErr : uint32_t {
+  kKvSlot = 1,      // slot past the last page
+  kKvPosition = 2,  // position outside the rotation table
+  kKvValue = 3,     // key or value not finite or beyond the limit
+  kKvPage = 4,      // page id outside the cache
+  kKvLength = 5,    // length negative or beyond the page table
+  kKvRows = 6,      // query rows beyond max_q or T, or not ascending
+};
+
+constexpr float kKvLimit = 20000.f;  // |x| held: (16 + n) s + b and b = -3.14 |x| at worst stay in binary16
+
+struct KvAppendArgs {
+  KvLayout L;
+  char* pages;
+  int64_t tokens;
+  const _Float16 *q, *k, *v;
+  _Float16* q_out;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, o_ts, o_hs;
+  const int64_t* slots;
+  const int64_t* positions;
+  const float* rope;
+  int64_t rope_len;
+  int32_t rope_dims, interleaved;
+  const _Float16 *q_norm, *k_norm;
+  float eps;
+  int32_t rows;  // heads of one token: Hq (with q) + 2 Hkv (with k)
+  ErrWord* err;
+};
+
+struct KvReadArgs {
+  KvLayout L;
+  const char* pages;
+  int64_t tokens;
+  const int64_t* slots;
+  _Float16 *k_out, *v_out;
+  ErrWord* err;
+};
+
+struct KvAttendArgs {
+  KvLayout L;
+  const char* pages;
+  int32_t batch, max_q;
+  int64_t tokens;
+  const _Float16* q;
+  int64_t q_ts, q_hs;
+  const int32_t *q_start, *kv_len, *q_off, *table;
+  int64_t table_stride;
+  int32_t table_width, causal;
+  float scale;
+  void* out;
+  float* lse;
+  ErrWord* err;
+};
+
+hipError_t launch_kv_append(const KvAppendArgs& a, int num_cus, hipStream_t s);
+hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t s);
+hipError_t launch_kv_attend(const KvAttendArgs& a, bool out_f32, hipStream_t s);
+
+#ifdef __HIPCC__
+__device__ inline void kv_report(ErrWord* err, uint32_t code, int64_t index, int64_t seen, int64_t bound) {
+  __hip_atomic_store(&err->tile, (uint32_t)index, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+  __hip_atomic_store(&err->target, (uint32_t)bound, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+  __hip_atomic_store(&err->seen, (uint32_t)seen, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
+  __hip_atomic_store(&err->code, code, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_SYSTEM);
+}
+#endif
+
+}  // namespace agemm

@@ -1,0 +1,40 @@
+// The key/value cache's argument checks and page layout as a CPU library: the
+// host library's and the kernels' own headers behind C entries, for
+// tests/test_kv_host.py. No GPU, no HIP.
+#include "kv_checks.h"
+
+using namespace agemm;
+
+extern "C" {
+
+int kvh_create(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages) {
+  return kv_check_create(Hq, Hkv, D, page_tokens, num_pages);
+}
+
+int kvh_append(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages, const void* pages, const kvc_append_args* p,
+               char* why) {
+  return kv_check_append(kv_layout(Hq, Hkv, D, page_tokens, num_pages), pages, p, why);
+}
+
+int kvh_attend(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages, const void* pages, const kvc_attend_args* p,
+               int64_t need, const void* workspace, int64_t workspace_bytes, char* why) {
+  return kv_check_attend(kv_layout(Hq, Hkv, D, page_tokens, num_pages), pages, p, need, workspace, workspace_bytes,
+                         why);
+}
+
+int kvh_read(const void* pages, int64_t tokens, const int64_t* slots, const void* k_out, const void* v_out, char* why) {
+  return kv_check_read(pages, tokens, slots, k_out, v_out, why);
+}
+
+// Byte of the block of `slot` and kv head h, and the token's places in it.
+int64_t kvh_block(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages, int64_t slot, int h, int* token,
+                  int* quarter, int* place) {
+  const KvLayout L = kv_layout(Hq, Hkv, D, page_tokens, num_pages);
+  const int off = (int)(slot & (L.page_tokens - 1));
+  *token = off & 31;
+  *quarter = kv_value_quarter(*token);
+  *place = kv_value_place(*token);
+  return kv_block_at(L, slot >> L.page_shift, h, off >> 5);
+}
+
+}  // extern "C"
