@@ -1,122 +1,755 @@
 // Attention over the 4-bit paged cache on gfx950.
 //
-// One workgroup per (query row, query head) walks the sequence's blocks of 32
-// tokens with a running maximum m, sum l and weighted values acc of the
-// softmax:
-//   m' = max(m, S_j), l' = l e^(m-m') + sum_j e^(S_j-m'), acc alike.
-// Eight threads share a key's product; then each thread owns a channel.
+// The products run on the matrix units in binary16 with binary32 sums, keys
+// and values as the binary16 numbers that their nibbles stand for, and
+// transposed: S^T = K Q^T has keys as rows and queries as columns, so that a
+// lane holds one query's scores for a few keys, and O^T = V^T P^T takes the
+// weights P^T from the very registers that the scores came in. The matrix
+// instructions ask for the operand of a product over keys with eight
+// consecutive inner indices a lane; as the order of the inner index is free
+// when both operands share it, the eight keys of a lane are those whose scores
+// it holds, and the cache stores values in that order (kvcache.h). No lane
+// exchanges data for the products.
+//
+// A nibble n becomes (16 + n) by an OR: n in bits 6..9 of a binary16 number
+// with exponent 4. One packed multiply-add with (s, b) makes two channels'
+// values: 3 operations for two.
+//
+// The running maximum m of the softmax is replaced only when a score passes it
+// by 2^3: weights are kept as 2^(x - m + 12) (x the score in units of log 2),
+// at most 2^15, so the usual block needs no maximum across lanes and no
+// rescaling. Below 2^(m - 26) weights lose bits to binary16's subnormals.
+// With binary32 outputs a weight enters the product as two binary16 numbers,
+// its value cut to binary16 and the rest.
 #include "kv_internal.h"
 
 namespace agemm {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr float kLowest = -3.402823466e+38f;  // lse of a row that sees nothing
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef _Float16 half8v __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+typedef float float16v __attribute__((ext_vector_type(16)));
+typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
 
-__device__ inline float held(uint32_t n, _Float16 s, _Float16 b) {
-  return (float)__builtin_fmaf16((_Float16)(float)(16 + n), s, b);
+constexpr float kLowest = -3.402823466e+38f;  // lse of a row that sees nothing
+constexpr float kLog2e = 1.44269504088896f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kNoMax = -3.0e38f;  // exponent base before the first score
+constexpr float kShift = 12.f;      // weights are 2^(x - m + kShift)
+constexpr float kTop = 15.f;        // and at most 2^kTop
+
+__device__ inline float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Two of a word's nibbles, j and j + 4, as (16 + n).
+template <int j>
+__device__ inline half2v sixteen_plus(uint32_t w) {
+  uint32_t x;
+  if constexpr (j == 0) x = w << 6;
+  else if constexpr (j == 1) x = w << 2;
+  else if constexpr (j == 2) x = w >> 2;
+  else x = w >> 6;
+  return __builtin_bit_cast(half2v, (x & 0x03C003C0u) | 0x4C004C00u);
+}
+
+// (Taken by value: of an element of a vector, __builtin_bit_cast reads a wrong one.)
+__device__ inline half2v halves(uint32_t w) { return __builtin_bit_cast(half2v, w); }
+
+__device__ inline half8v join4(half2v a, half2v b, half2v c, half2v d) {
+  return half8v{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// Eight channels of one key from a word of its row: channels 0 4 1 5 2 6 3 7.
+__device__ inline half8v key_operand(uint32_t w, half2v s, half2v b) {
+  return join4(__builtin_elementwise_fma(sixteen_plus<0>(w), s, b), __builtin_elementwise_fma(sixteen_plus<1>(w), s, b),
+               __builtin_elementwise_fma(sixteen_plus<2>(w), s, b), __builtin_elementwise_fma(sixteen_plus<3>(w), s, b));
+}
+
+// One channel (nibble j of the 16-bit words) of eight tokens; s and b of the tokens in pairs.
+template <int j>
+__device__ inline half8v value_operand(uint4v w, const half2v (&s)[4], const half2v (&b)[4]) {
+  return join4(__builtin_elementwise_fma(sixteen_plus<j>(w.x), s[0], b[0]),
+               __builtin_elementwise_fma(sixteen_plus<j>(w.y), s[1], b[1]),
+               __builtin_elementwise_fma(sixteen_plus<j>(w.z), s[2], b[2]),
+               __builtin_elementwise_fma(sixteen_plus<j>(w.w), s[3], b[3]));
+}
+
+// A query's eight channels in the order of key_operand.
+__device__ inline half8v query_operand(const _Float16* q) {
+  const half8v v = *reinterpret_cast<const half8v*>(q);
+  return half8v{v[0], v[4], v[1], v[5], v[2], v[6], v[3], v[7]};
+}
+
+// A sequence's rows and lengths, checked against what the call gave.
+struct Sequence {
+  int64_t row0;  // its first row of q
+  int n;         // its queries, 0 if they cannot be used
+  int len;       // cached tokens
+  int64_t off;   // the first query sees off + 1 tokens
+
+  __device__ int seen(int i) const {
+    const int64_t v = off + i + 1;
+    return v < 0 ? 0 : v > len ? len : (int)v;
+  }
+};
+
+__device__ inline Sequence sequence(const KvAttendArgs& a, int b, bool tell) {
+  Sequence s;
+  int64_t end;
+  if (a.q_start) {
+    s.row0 = a.q_start[b];
+    end = a.q_start[b + 1];
+  } else {
+    s.row0 = b;
+    end = b + 1;
+  }
+  const int64_t n = end - s.row0;
+  const bool usable = n >= 0 && n <= a.max_q && s.row0 >= 0 && end <= a.tokens;
+  if (!usable && tell) kv_report(a.err, kKvRows, b, n, a.max_q);
+  s.n = usable ? (int)n : 0;
+  const int64_t most = (int64_t)a.table_width << a.L.page_shift;
+  s.len = a.kv_len[b];
+  if (s.len < 0 || s.len > most) {
+    if (tell) kv_report(a.err, kKvLength, b, s.len, most);
+    s.len = s.len < 0 ? 0 : (int)most;
+  }
+  s.off = !a.causal ? (int64_t)s.len : a.q_off ? (int64_t)a.q_off[b] : (int64_t)s.len - n;
+  return s;
+}
+
+// Block j of a sequence: its bytes, or nullptr if its page is not in the cache.
+__device__ inline const char* block_at(const KvAttendArgs& a, int b, int h, int j, bool tell) {
+  const int in_page = a.L.page_shift - 5;
+  const int64_t page = a.table[(int64_t)b * a.table_stride + (j >> in_page)];
+  if (page < 0 || page >= a.L.num_pages) {
+    if (tell) kv_report(a.err, kKvPage, b, page, a.L.num_pages);
+    return nullptr;
+  }
+  return a.pages + kv_block_at(a.L, page, h, j & ((1 << in_page) - 1));
+}
+
+// Writes one row's channels d0 .. d0 + N - 1 of a finished output.
+template <bool F32, int N>
+__device__ inline void store_out(void* out, int64_t at, const float (&v)[N]) {
+  if constexpr (F32) {
+    float4v* p = reinterpret_cast<float4v*>(static_cast<float*>(out) + at);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) p[i] = float4v{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+  } else {
+    struct alignas(N * 2) H {
+      _Float16 x[N];
+    } h;
+#pragma unroll
+    for (int i = 0; i < N; ++i) h.x[i] = (_Float16)v[i];
+    *reinterpret_cast<H*>(static_cast<_Float16*>(out) + at) = h;
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+
+// For at most 16 NT rows a kv head (single tokens, drafts): HBM-bound, each
+// cached byte read once. A workgroup takes a run of an item's blocks; its waves
+// take every kWaves-th block each, with loads one block ahead and no barrier,
+// and join their sums at the end. A wave holds all rows of the item as the 16
+// columns of its products (NT times), and a block of 32 keys as two tiles of 16.
+constexpr int kWaves = 8;
+
+template <int D>
+struct Raw {  // one block as a lane reads it
+  uint32_t k[2][D / 32];
+  half2v kp[2];
+  uint4v v[D / 64];
+  uint4v vs, vb;
+};
+
+template <int D>
+__device__ inline void load_block(Raw<D>& r, const char* blk, int col, int quarter) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const char* row = blk + (t * 16 + col) * (D / 2) + quarter * (D / 8);
+    if constexpr (D == 64) {
+      const uint2v w = *reinterpret_cast<const uint2v*>(row);
+      r.k[t][0] = w.x;
+      r.k[t][1] = w.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 128; ++i) {
+        const uint4v w = *reinterpret_cast<const uint4v*>(row + 16 * i);
+        r.k[t][4 * i] = w.x;
+        r.k[t][4 * i + 1] = w.y;
+        r.k[t][4 * i + 2] = w.z;
+        r.k[t][4 * i + 3] = w.w;
+      }
+    }
+    r.kp[t] = *reinterpret_cast<const half2v*>(blk + 32 * D + 4 * (t * 16 + col));
+  }
+#pragma unroll
+  for (int g = 0; g < D / 64; ++g)
+    r.v[g] = *reinterpret_cast<const uint4v*>(blk + 16 * D + ((g * 4 + quarter) * 16 + col) * 16);
+  r.vs = *reinterpret_cast<const uint4v*>(blk + 32 * D + 128 + quarter * 16);
+  r.vb = *reinterpret_cast<const uint4v*>(blk + 32 * D + 192 + quarter * 16);
+}
+
+template <int D, int NT, bool F32>
+struct FewState {
+  half8v q[NT][D / 32];
+  float4v o[NT][D / 16];  // O^T: row 4 quarter + i of tile m is channel (4 quarter + i) D / 16 + m
+  float base[NT];         // m - kShift
+  float sum[NT];          // of this lane's weights
+  int seen[NT];           // keys that the column's row sees
+};
+
+// Folds one block in. MASK: some row does not see all of it, or it is the sequence's last.
+template <int D, int NT, bool F32, bool MASK>
+__device__ inline void take_block(FewState<D, NT, F32>& st, const Raw<D>& r, int j, int len, int quarter, float factor) {
+  float4v s[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const half2v sc = {r.kp[t].x, r.kp[t].x}, of = {r.kp[t].y, r.kp[t].y};
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const half8v k = key_operand(r.k[t][i], sc, of);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, st.q[n][i], s[n][t], 0, 0, 0);
+    }
+  }
+
+  half8v hi[NT], lo[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float e[8];
+    float top = -__builtin_inff();
+    const int left = st.seen[n] - (j * 32 + quarter * 4);
+    auto exponents = [&](float base) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float x = __builtin_fmaf(s[n][t][i], factor, -base);
+          if (MASK && t * 16 + i >= left) x = -__builtin_inff();
+          e[4 * t + i] = x;
+        }
+      top = fmaxf(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])), fmaxf(fmaxf(e[4], e[5]), fmaxf(e[6], e[7])));
+    };
+    exponents(st.base[n]);
+    if (__any(top > kTop)) {  // a new maximum, for some column
+      exponents(0.f);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float base = fmaxf(st.base[n], top - kShift);
+      const float f = exp2_hw(st.base[n] - base);
+      st.sum[n] *= f;
+#pragma unroll
+      for (int m = 0; m < D / 16; ++m) st.o[n][m] *= f;
+      st.base[n] = base;
+      exponents(base);
+    }
+    float p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p[i] = exp2_hw(e[i]);
+      st.sum[n] += p[i];
+    }
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const auto c = __builtin_amdgcn_cvt_pkrtz(p[i], p[i + 1]);
+        hi[n][i] = (_Float16)c[0];
+        hi[n][i + 1] = (_Float16)c[1];
+        const auto d = __builtin_amdgcn_cvt_pkrtz(p[i] - (float)hi[n][i], p[i + 1] - (float)hi[n][i + 1]);
+        lo[n][i] = (_Float16)d[0];
+        lo[n][i + 1] = (_Float16)d[1];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) hi[n][i] = (_Float16)p[i];
+    }
+  }
+
+  half2v vs[4], vb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    vs[i] = halves(r.vs[i]);
+    vb[i] = halves(r.vb[i]);
+    if constexpr (MASK) {  // what lies behind the sequence's end may be anything
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int e = 2 * i + x;
+        if (j * 32 + (e >> 2) * 16 + quarter * 4 + (e & 3) >= len) vs[i][x] = vb[i][x] = (_Float16)0.f;
+      }
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < D / 64; ++g) {
+    const half8v v[4] = {value_operand<0>(r.v[g], vs, vb), value_operand<1>(r.v[g], vs, vb),
+                         value_operand<2>(r.v[g], vs, vb), value_operand<3>(r.v[g], vs, vb)};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float4v& o = st.o[n][4 * g + x];
+        o = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[x], hi[n], o, 0, 0, 0);
+        if constexpr (F32) o = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[x], lo[n], o, 0, 0, 0);
+      }
+  }
+}
+
+template <int D, int NT, bool F32>
+__global__ __launch_bounds__(kWaves * 64, NT * D > 64 ? 2 : 4) void kv_attend_few_kernel(KvAttendArgs a) {
+  constexpr int MT = D / 16;
+  __shared__ float4v merge[kWaves / 2 * NT * MT * 64];
+  __shared__ float heads[2][kWaves][NT * 16];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, quarter = lane >> 4;
+  const int item = blockIdx.x, run = blockIdx.y;
+  const int b = item / a.L.Hkv, h = item - b * a.L.Hkv;
+  const int G = a.L.Hq / a.L.Hkv;
+  const Sequence seq = sequence(a, b, run == 0 && h == 0 && threadIdx.x == 0);
+  const int rows = seq.n * G;
+  if (rows == 0) return;
+  const int nblk = (seq.seen(seq.n - 1) + 31) >> 5;
+  const int runs = kv_runs(a.plan.chunk, a.plan.splits, nblk);
+  if (run >= runs) return;
+  const int chunk = kv_run_blocks(a.plan.chunk, a.plan.splits, nblk);
+  const int j1 = nblk < (run + 1) * chunk ? nblk : (run + 1) * chunk;
+  int j = run * chunk + wave;
+
+  FewState<D, NT, F32> st;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = n * 16 + col;
+    const bool live = r < rows;
+    const int i = r / G;
+    const _Float16* q = a.q + (seq.row0 + i) * a.q_ts + (int64_t)(h * G + r - i * G) * a.q_hs + quarter * (D / 4);
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) st.q[n][x] = live ? query_operand(q + 8 * x) : half8v{};
+    st.seen[n] = live ? seq.seen(i) : seq.len;
+    st.base[n] = kNoMax;
+    st.sum[n] = 0.f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) st.o[n][m] = float4v{0.f, 0.f, 0.f, 0.f};
+  }
+  const int whole = seq.seen(0) >> 5;  // blocks that every row sees whole
+  const float factor = a.scale * kLog2e;
+  const bool tell = lane == 0;
+
+  auto take = [&](const Raw<D>& r, int at) {
+    if (at < whole) take_block<D, NT, F32, false>(st, r, at, seq.len, quarter, factor);
+    else take_block<D, NT, F32, true>(st, r, at, seq.len, quarter, factor);
+  };
+  Raw<D> x, y;
+  const char *bx = nullptr, *by = nullptr;
+  if (j < j1 && (bx = block_at(a, b, h, j, tell))) load_block<D>(x, bx, col, quarter);
+  while (j < j1) {
+    if (j + kWaves < j1 && (by = block_at(a, b, h, j + kWaves, tell))) load_block<D>(y, by, col, quarter);
+    if (bx) take(x, j);
+    j += kWaves;
+    if (j >= j1) break;
+    if (j + kWaves < j1 && (bx = block_at(a, b, h, j + kWaves, tell))) load_block<D>(x, bx, col, quarter);
+    if (by) take(y, j);
+    j += kWaves;
+  }
+
+  // Join the waves: a common base, then sums by halves, in a fixed order.
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    st.sum[n] += __shfl_xor(st.sum[n], 16);
+    st.sum[n] += __shfl_xor(st.sum[n], 32);
+    if (quarter == 0) {
+      heads[0][wave][n * 16 + col] = st.base[n];
+      heads[1][wave][n * 16 + col] = st.sum[n];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float top = kNoMax, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, heads[0][w][n * 16 + col]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += heads[1][w][n * 16 + col] * exp2_hw(heads[0][w][n * 16 + col] - top);
+    const float f = exp2_hw(st.base[n] - top);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) st.o[n][m] *= f;
+    st.base[n] = top;
+    st.sum[n] = sum;
+  }
+#pragma unroll
+  for (int half = kWaves / 2; half > 0; half >>= 1) {
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) merge[((wave - half) * NT * MT + n * MT + m) * 64 + lane] = st.o[n][m];
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) st.o[n][m] += merge[(wave * NT * MT + n * MT + m) * 64 + lane];
+    }
+    __syncthreads();
+  }
+  if (wave != 0) return;
+
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = n * 16 + col;
+    if (r >= rows) continue;
+    const int i = r / G;
+    const int64_t o = (seq.row0 + i) * a.L.Hq + h * G + r - i * G;
+    const bool last = runs == 1;
+    float* slot = last ? nullptr : a.ws + ((int64_t)item * a.plan.splits + run) * a.plan.slot_floats;
+    const float inv = !last ? 1.f : st.sum[n] != 0.f ? 1.f / st.sum[n] : 0.f;
+#pragma unroll
+    for (int y4 = 0; y4 < 4; ++y4) {
+      float v[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) v[m] = st.o[n][m][y4] * inv;
+      const int d0 = (quarter * 4 + y4) * MT;
+      if (last) store_out<F32>(a.out, o * D + d0, v);
+      else store_out<true>(slot, (int64_t)r * D + d0, v);
+    }
+    if (quarter == 0) {
+      if (last) {
+        if (a.lse) a.lse[o] = st.sum[n] != 0.f ? (st.base[n] + log2f(st.sum[n])) * kLn2 : kLowest;
+      } else {
+        slot[a.plan.rows * D + 2 * r] = st.base[n];
+        slot[a.plan.rows * D + 2 * r + 1] = st.sum[n];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+
+// For more rows (prompts): MFMA-bound. A workgroup of four waves takes 128
+// rows of an item, 32 a wave, the columns of 32 x 32 products. The workgroup
+// turns a tile of 256 / D blocks into binary16 operands in LDS,
+// each thread one 16-byte piece of the keys and one of the values, while the
+// waves multiply the tile before it; one barrier a tile.
+constexpr int kManyThreads = 256;
+
+template <int D, bool F32>
+__global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_kernel(KvAttendArgs a) {
+  constexpr int KB = 256 / D;      // blocks of a tile
+  constexpr int KS = D / 16;       // inner steps of the scores
+  constexpr int MT = D / 32;       // channel tiles of the output
+  constexpr int RN = D / 32;       // 16-byte pieces of a key row
+  constexpr int KFRAG = KB * KS * 64, VFRAG = KB * 2 * MT * 64;  // 16-byte operands of a tile: 1024 each
+  __shared__ half8v kl[2][KFRAG];
+  __shared__ half8v vl[2][VFRAG];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, hh = lane >> 5;
+  const int G = a.L.Hq / a.L.Hkv;
+  // Heads innermost: workgroups of one head go to one XCD and share its cache;
+  // later tiles, which see more keys, first.
+  const int item = blockIdx.x, run = blockIdx.y;
+  const int h = item % a.L.Hkv, rest = item / a.L.Hkv;
+  const int b = rest % a.batch, tile = a.plan.tiles - 1 - rest / a.batch;
+  const Sequence seq = sequence(a, b, run == 0 && h == 0 && tile == 0 && tid == 0);
+  const int rows = seq.n * G;
+  const int r0 = tile * 128;
+  if (r0 >= rows) return;
+  const int r_last = (r0 + 127 < rows ? r0 + 127 : rows - 1);
+  const int nblk = (seq.seen(r_last / G) + 31) >> 5;
+  const int runs = kv_runs(a.plan.chunk, a.plan.splits, nblk);
+  if (run >= runs) return;
+  const int chunk = kv_run_blocks(a.plan.chunk, a.plan.splits, nblk);
+  const int j0 = run * chunk;
+  const int j1 = nblk < j0 + chunk ? nblk : j0 + chunk;
+
+  const int r = r0 + wave * 32 + col;
+  const bool live = r < rows;
+  const int qi = live ? r / G : 0;
+  const int64_t orow = (seq.row0 + qi) * a.L.Hq + h * G + (r - qi * G);
+  half8v q[KS];
+  {
+    const _Float16* src = a.q + (seq.row0 + qi) * a.q_ts + (int64_t)(h * G + r - qi * G) * a.q_hs + hh * 8;
+#pragma unroll
+    for (int u = 0; u < KS; ++u) q[u] = live ? query_operand(src + 16 * u) : half8v{};
+  }
+  const int seen = live ? seq.seen(qi) : seq.len;
+  // Wave-uniform: blocks below `whole` are seen whole by every row of the wave, none at or past `none`.
+  const int w0 = r0 + wave * 32, w1 = (w0 + 31 < rows ? w0 + 31 : rows - 1);
+  const int whole = w0 < rows ? seq.seen(w0 / G) >> 5 : 0;
+  const int none = w0 < rows ? (seq.seen(w1 / G) + 31) >> 5 : 0;
+  const float factor = a.scale * kLog2e;
+
+  float16v o[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[m][i] = 0.f;
+  float base = kNoMax, sum = 0.f;
+
+  // This thread's piece of a tile: block, and within it the key row's piece and the value piece.
+  const int piece = tid & (D - 1), pb = tid / D;
+  const int ktok = piece / RN, krun = piece % RN;
+  const int vq = (piece >> 4) & 3, vc = piece & 15, vg = piece >> 6;
+  uint4v kr, vr, vsr, vbr;
+  half2v kpr;
+  int have = 0;  // 1: this thread's block is there
+  auto fetch = [&](int jt) {
+    const int j = jt + pb;
+    const char* blk = j < j1 ? block_at(a, b, h, j, piece == 0) : nullptr;
+    have = blk != nullptr;
+    if (!blk) return;
+    kr = *reinterpret_cast<const uint4v*>(blk + piece * 16);
+    kpr = *reinterpret_cast<const half2v*>(blk + 32 * D + 4 * ktok);
+    vr = *reinterpret_cast<const uint4v*>(blk + 16 * D + piece * 16);
+    vsr = *reinterpret_cast<const uint4v*>(blk + 32 * D + 128 + vq * 16);
+    vbr = *reinterpret_cast<const uint4v*>(blk + 32 * D + 192 + vq * 16);
+  };
+  __shared__ int there[2][KB];
+  auto spread = [&](int jt, int buf) {
+    const int j = jt + pb;
+    half2v ks = kpr, vs[4], vb[4];
+    // Nothing may come of tokens behind the sequence's end or without a page.
+    const bool kok = have && j * 32 + ktok < seq.len;
+    if (!kok) {
+      ks = half2v{(_Float16)0.f, (_Float16)0.f};
+      kr = uint4v{0, 0, 0, 0};
+    }
+    const half2v s2 = {ks.x, ks.x}, b2 = {ks.y, ks.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int w = krun * 4 + i;  // word of the row: step w / 2, half w & 1
+      kl[buf][(pb * KS + (w >> 1)) * 64 + (((w & 1) * 32 + ktok) ^ (krun * (8 / RN)))] = key_operand(kr[i], s2, b2);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      vs[i] = halves(vsr[i]);
+      vb[i] = halves(vbr[i]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int e = 2 * i + x;
+        if (!have || j * 32 + (e >> 2) * 16 + vq * 4 + (e & 3) >= seq.len) vs[i][x] = vb[i][x] = (_Float16)0.f;
+      }
+    }
+    const half8v v[4] = {value_operand<0>(vr, vs, vb), value_operand<1>(vr, vs, vb), value_operand<2>(vr, vs, vb),
+                         value_operand<3>(vr, vs, vb)};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      vl[buf][((pb * 2 + (vq >> 1)) * MT + 2 * vg + (x >> 1)) * 64 + (vq & 1) * 32 + (x & 1) * 16 + vc] = v[x];
+    if (piece == 0) there[buf][pb] = have;
+  };
+
+  auto take = [&](int j, int buf, int kb, bool mask) {
+    float16v s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+    for (int u = 0; u < KS; ++u) {
+      const half8v k = kl[buf][(kb * KS + u) * 64 + (lane ^ ((u >> 1) * (8 / RN)))];
+      s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[u], s, 0, 0, 0);
+    }
+    float e[16];
+    float top;
+    const int left = seen - (j * 32 + hh * 4);
+    auto exponents = [&](float bs) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        e[i] = __builtin_fmaf(s[i], factor, -bs);
+        if (mask && 8 * (i >> 2) + (i & 3) >= left) e[i] = -__builtin_inff();
+      }
+      top = e[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, e[i]);
+    };
+    exponents(base);
+    if (__any(top > kTop)) {
+      exponents(0.f);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float nb = fmaxf(base, top - kShift);
+      const float f = exp2_hw(base - nb);
+      sum *= f;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) o[m] *= f;
+      base = nb;
+      exponents(nb);
+    }
+    half8v hi[2], lo[2];
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float p0 = exp2_hw(e[i]), p1 = exp2_hw(e[i + 1]);
+      sum += p0;
+      sum += p1;
+      // group i / 4 of four keys: elements 0..3 of product 0 and 1, then 4..7
+      const int u = (i >> 2) & 1, x = (i >> 3) * 4 + (i & 3);
+      if constexpr (F32) {
+        const auto c = __builtin_amdgcn_cvt_pkrtz(p0, p1);
+        hi[u][x] = (_Float16)c[0];
+        hi[u][x + 1] = (_Float16)c[1];
+        const auto d = __builtin_amdgcn_cvt_pkrtz(p0 - (float)hi[u][x], p1 - (float)hi[u][x + 1]);
+        lo[u][x] = (_Float16)d[0];
+        lo[u][x + 1] = (_Float16)d[1];
+      } else {
+        hi[u][x] = (_Float16)p0;
+        hi[u][x + 1] = (_Float16)p1;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const half8v v = vl[buf][((kb * 2 + u) * MT + m) * 64 + lane];
+        o[m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, hi[u], o[m], 0, 0, 0);
+        if constexpr (F32) o[m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, lo[u], o[m], 0, 0, 0);
+      }
+  };
+
+  if (j0 < j1) {
+    fetch(j0);
+    spread(j0, 0);
+    if (j0 + KB < j1) fetch(j0 + KB);
+    __syncthreads();
+    int buf = 0;
+    for (int jt = j0; jt < j1; jt += KB, buf ^= 1) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const int j = jt + kb;
+        if (j >= j1 || j >= none || !there[buf][kb]) continue;
+        if (j < whole) take(j, buf, kb, false);
+        else take(j, buf, kb, true);
+      }
+      if (jt + KB < j1) {
+        spread(jt + KB, buf ^ 1);
+        if (jt + 2 * KB < j1) fetch(jt + 2 * KB);
+      }
+      __syncthreads();
+    }
+  }
+
+  sum += __shfl_xor(sum, 32);
+  if (!live) return;
+  // O^T: register i of tile m is row R = 8 (i / 4) + 4 hh + i % 4, channel (R % 16) D / 16 + 2 m + R / 16.
+  const bool last = runs == 1;
+  float* slot = last ? nullptr : a.ws + ((int64_t)item * a.plan.splits + run) * a.plan.slot_floats;
+  const int lr = r - r0;
+  const float inv = !last ? 1.f : sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int y = 0; y < 8; ++y) {
+    float v[2 * MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      v[2 * m] = o[m][y] * inv;
+      v[2 * m + 1] = o[m][8 + y] * inv;
+    }
+    const int d0 = (8 * (y >> 2) + 4 * hh + (y & 3)) * (2 * MT);
+    if (last) store_out<F32>(a.out, orow * D + d0, v);
+    else store_out<true>(slot, (int64_t)lr * D + d0, v);
+  }
+  if (hh == 0) {
+    if (last) {
+      if (a.lse) a.lse[orow] = sum != 0.f ? (base + log2f(sum)) * kLn2 : kLowest;
+    } else {
+      slot[a.plan.rows * D + 2 * lr] = base;
+      slot[a.plan.rows * D + 2 * lr + 1] = sum;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- join
+
+// Joins the partials of the runs of an item, one workgroup a row: its four
+// waves take every fourth run, in order, and their sums meet in LDS.
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void kv_attend_join_kernel(KvAttendArgs a) {
+  constexpr int E = D / 64;
+  __shared__ float acc[3][D], sums[3];
+  const int rpi = a.plan.rows;
+  const int item = blockIdx.x / rpi, lr = blockIdx.x - item * rpi;
+  const int G = a.L.Hq / a.L.Hkv;
+  int b, h, r0;
+  if (a.plan.many) {
+    h = item % a.L.Hkv;
+    const int rest = item / a.L.Hkv;
+    b = rest % a.batch;
+    r0 = (a.plan.tiles - 1 - rest / a.batch) * rpi;
+  } else {
+    b = item / a.L.Hkv;
+    h = item - b * a.L.Hkv;
+    r0 = 0;
+  }
+  const Sequence seq = sequence(a, b, false);
+  const int rows = seq.n * G, r = r0 + lr;
+  if (r >= rows) return;
+  const int r_last = r0 + rpi - 1 < rows ? r0 + rpi - 1 : rows - 1;
+  const int nblk = (seq.seen(r_last / G) + 31) >> 5;
+  const int runs = kv_runs(a.plan.chunk, a.plan.splits, nblk);
+  if (runs == 1) return;  // written by its only run
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float* slot = a.ws + (int64_t)item * a.plan.splits * a.plan.slot_floats;
+  float top = kNoMax;
+  for (int s = lane; s < runs; s += 64) top = fmaxf(top, slot[s * a.plan.slot_floats + rpi * D + 2 * lr]);
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
+  float v[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.f;
+#pragma unroll 4
+  for (int s = wave; s < runs; s += 4) {
+    const float* p = slot + s * a.plan.slot_floats;
+    const float f = exp2_hw(p[rpi * D + 2 * lr] - top);
+    sum += f * p[rpi * D + 2 * lr + 1];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] += f * p[lr * D + lane * E + e];
+  }
+  if (wave > 0) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[wave - 1][lane * E + e] = v[e];
+    if (lane == 0) sums[wave - 1] = sum;
+  }
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) {
+    sum += sums[w];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] += acc[w][lane * E + e];
+  }
+  const int i = r / G;
+  const int64_t o = (seq.row0 + i) * a.L.Hq + h * G + r - i * G;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if constexpr (F32) static_cast<float*>(a.out)[o * D + lane * E + e] = v[e] * inv;
+    else static_cast<_Float16*>(a.out)[o * D + lane * E + e] = (_Float16)(v[e] * inv);
+  }
+  if (a.lse && lane == 0) a.lse[o] = sum != 0.f ? (top + log2f(sum)) * kLn2 : kLowest;
 }
 
 template <int D, bool F32>
-__global__ __launch_bounds__(kThreads) void kv_attend_rows_kernel(KvAttendArgs a) {
-  __shared__ float qs[D], sc[32];
-  const int64_t row = blockIdx.x / a.L.Hq;
-  const int hq = (int)(blockIdx.x - row * a.L.Hq);
-  const int h = hq / (a.L.Hq / a.L.Hkv);
-  const int tid = threadIdx.x;
-  int b = (int)row, i = 0, n = 1;
-  if (a.q_start) {  // the sequence whose rows hold this one (block-uniform search)
-    for (b = 0; b < a.batch; ++b) {
-      if (a.q_start[b + 1] < a.q_start[b] && tid == 0) kv_report(a.err, kKvRows, b, a.q_start[b + 1] - a.q_start[b], a.max_q);
-      if (row >= a.q_start[b] && row < a.q_start[b + 1]) break;
-    }
-    if (b == a.batch) return;
-    i = (int)(row - a.q_start[b]);
-    n = a.q_start[b + 1] - a.q_start[b];
-    if (n > a.max_q || a.q_start[b] < 0 || a.q_start[b + 1] > a.tokens) {
-      if (tid == 0) kv_report(a.err, kKvRows, b, n, a.max_q);
-      return;
-    }
-  }
-  if (b >= a.batch) return;
-  int64_t len = a.kv_len[b];
-  const int64_t most = (int64_t)a.table_width << a.L.page_shift;
-  if (len < 0 || len > most) {
-    if (tid == 0) kv_report(a.err, kKvLength, b, len, most);
-    len = len < 0 ? 0 : most;
-  }
-  if (a.causal) {
-    const int64_t seen = (a.q_off ? (int64_t)a.q_off[b] : len - n) + i + 1;
-    if (seen < len) len = seen < 0 ? 0 : seen;
-  }
-  for (int d = tid; d < D; d += kThreads) qs[d] = (float)a.q[row * a.q_ts + hq * a.q_hs + d];
-  __syncthreads();
-
-  float m = -__builtin_inff(), l = 0.f, acc = 0.f;
-  for (int64_t at = 0; at < len; at += 32) {
-    const int64_t page = a.table[b * a.table_stride + (at >> a.L.page_shift)];
-    if (page < 0 || page >= a.L.num_pages) {
-      if (tid == 0) kv_report(a.err, kKvPage, b, page, a.L.num_pages);
-      continue;
-    }
-    const char* blk = a.pages + kv_block_at(a.L, page, h, (int)(at & (a.L.page_tokens - 1)) >> 5);
-    const _Float16* par = reinterpret_cast<const _Float16*>(blk + 32 * D);
-    const int key = tid >> 3, part = tid & 7;
-    float s = 0.f;
-    const uint8_t* kr = reinterpret_cast<const uint8_t*>(blk) + key * (D / 2) + part * (D / 16);
-    for (int c = 0; c < D / 16; ++c) {
-      const uint32_t w = kr[c];
-      s += qs[part * (D / 8) + 2 * c] * held(w & 15, par[2 * key], par[2 * key + 1]);
-      s += qs[part * (D / 8) + 2 * c + 1] * held(w >> 4, par[2 * key], par[2 * key + 1]);
-    }
-    for (int x = 1; x < 8; x <<= 1) s += __shfl_xor(s, x, 8);
-    if (part == 0) sc[key] = at + key < len ? s * a.scale : -__builtin_inff();
-    __syncthreads();
-    float mn = m;
-    for (int j = 0; j < 32; ++j) mn = fmaxf(mn, sc[j]);
-    const float keep = mn == -__builtin_inff() ? 0.f : expf(m - mn);
-    l *= keep;
-    acc *= keep;
-    const int c = tid / (D / 16), g = (tid % (D / 16)) >> 2, jn = tid & 3;
-    const int top = (int)(len - at < 32 ? len - at : 32);
-    for (int j = 0; j < top; ++j) {
-      const float p = mn == -__builtin_inff() ? 0.f : expf(sc[j] - mn);
-      l += p;
-      if (tid < D) {
-        const int qr = kv_value_quarter(j), e8 = kv_value_place(j);
-        const uint32_t w = reinterpret_cast<const uint16_t*>(blk + 16 * D)[((g * 4 + qr) * 16 + c) * 8 + e8];
-        acc += p * held((w >> (4 * jn)) & 15, par[64 + qr * 8 + e8], par[96 + qr * 8 + e8]);
-      }
-    }
-    m = mn;
-    __syncthreads();
-  }
-  const int64_t o = row * a.L.Hq + hq;
-  if (tid < D) {
-    const float v = l != 0.f ? acc / l : 0.f;
-    if constexpr (F32) static_cast<float*>(a.out)[o * D + tid] = v;
-    else static_cast<_Float16*>(a.out)[o * D + tid] = (_Float16)v;
-  }
-  if (a.lse && tid == 0) a.lse[o] = l != 0.f ? m + logf(l) : kLowest;
-}
-
-template <int D>
-void launch_d(const KvAttendArgs& a, bool out_f32, hipStream_t s) {
-  const dim3 grid((unsigned)(a.tokens * a.L.Hq)), block(kThreads);
-  if (out_f32) hipLaunchKernelGGL((kv_attend_rows_kernel<D, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((kv_attend_rows_kernel<D, false>), grid, block, 0, s, a);
+hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.plan.items, (unsigned)a.plan.splits);
+  if (a.plan.many) hipLaunchKernelGGL((kv_attend_many_kernel<D, F32>), grid, dim3(kManyThreads), 0, s, a);
+  else if (a.plan.rows == 16) hipLaunchKernelGGL((kv_attend_few_kernel<D, 1, F32>), grid, dim3(kWaves * 64), 0, s, a);
+  else if constexpr (D <= 128)
+    hipLaunchKernelGGL((kv_attend_few_kernel<D, 2, F32>), grid, dim3(kWaves * 64), 0, s, a);
+  if (a.plan.splits > 1)
+    hipLaunchKernelGGL((kv_attend_join_kernel<D, F32>), dim3((unsigned)(a.plan.items * a.plan.rows)), dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_kv_attend(const KvAttendArgs& a, bool out_f32, hipStream_t s) {
   switch (a.L.D) {
-    case 64: launch_d<64>(a, out_f32, s); break;
-    case 128: launch_d<128>(a, out_f32, s); break;
-    case 256: launch_d<256>(a, out_f32, s); break;
+    case 64: return out_f32 ? launch_d<64, true>(a, s) : launch_d<64, false>(a, s);
+    case 128: return out_f32 ? launch_d<128, true>(a, s) : launch_d<128, false>(a, s);
+    case 256: return out_f32 ? launch_d<256, true>(a, s) : launch_d<256, false>(a, s);
     default: return hipErrorInvalidValue;
   }
-  return hipGetLastError();
 }
 
 }  // namespace agemm

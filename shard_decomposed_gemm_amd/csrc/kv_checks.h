@@ -18,6 +18,7 @@ constexpr size_t kKvWhy = 256;  // bytes of a reason
 constexpr int kKvNothing = -1;  // nothing to refuse and nothing to do
 
 constexpr int64_t kKvMaxTokens = int64_t{1} << 23;  // rows of one call: grids stay below 2^32 threads
+constexpr int64_t kKvMaxItems = (int64_t{1} << 23) - 1;  // of an attention call, for the same reason
 constexpr int64_t kKvMaxStride = int64_t{1} << 40;
 
 inline int kv_refuse(char* why, int code, const char* fmt, ...) __attribute__((format(printf, 3, 4)));
@@ -100,7 +101,7 @@ inline int kv_check_append(const KvLayout& L, const void* pages, const kvc_appen
   return AGEMM_OK;
 }
 
-inline int kv_check_attend(const KvLayout& L, const void* pages, const kvc_attend_args* p, int64_t need,
+inline int kv_check_attend(const KvLayout& L, const void* pages, const kvc_attend_args* p, const KvPlan& plan,
                            const void* workspace, int64_t workspace_bytes, char* why) {
   if (!p) return kv_refuse(why, AGEMM_EINVAL, "args must be non-NULL");
   if (p->batch < 0 || p->tokens < 0) return kv_refuse(why, AGEMM_EINVAL, "batch and tokens must not be negative");
@@ -108,6 +109,7 @@ inline int kv_check_attend(const KvLayout& L, const void* pages, const kvc_atten
   if (p->tokens > kKvMaxTokens || p->max_q > kKvMaxTokens || p->batch > kKvMaxTokens)
     return kv_refuse(why, AGEMM_ESHAPE, "more than %lld rows in a call", (long long)kKvMaxTokens);
   if (p->batch == 0 || p->tokens == 0) return kKvNothing;
+  if (plan.items > kKvMaxItems) return kv_refuse(why, AGEMM_ESHAPE, "batch and max_q too large for one call");
   if (p->causal != 0 && p->causal != 1) return kv_refuse(why, AGEMM_EINVAL, "causal must be 0 or 1");
   if (p->out_f32 != 0 && p->out_f32 != 1) return kv_refuse(why, AGEMM_EINVAL, "out_f32 must be 0 or 1");
   if (!isfinite(p->scale)) return kv_refuse(why, AGEMM_EINVAL, "scale must be finite");
@@ -122,8 +124,8 @@ inline int kv_check_attend(const KvLayout& L, const void* pages, const kvc_atten
   if (!p->kv_len || !p->page_table) return kv_refuse(why, AGEMM_EINVAL, "kv_len and page_table must be non-NULL");
   if (!kv_natural(p->q_start) || !kv_natural(p->kv_len) || !kv_natural(p->q_off) || !kv_natural(p->page_table) || !kv_natural(p->lse))
     return kv_refuse(why, AGEMM_EINVAL, "q_start, kv_len, q_off, page_table and lse must be aligned to their elements");
-  if (need > 0 && (!kv_aligned16(workspace) || workspace_bytes < need))
-    return kv_refuse(why, AGEMM_EINVAL, "workspace must be 16-byte aligned and hold %lld bytes", (long long)need);
+  if (plan.ws_bytes > 0 && (!kv_aligned16(workspace) || workspace_bytes < plan.ws_bytes))
+    return kv_refuse(why, AGEMM_EINVAL, "workspace must be 16-byte aligned and hold %lld bytes", (long long)plan.ws_bytes);
 
   return AGEMM_OK;
 }

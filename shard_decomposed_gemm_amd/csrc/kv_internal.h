@@ -60,6 +60,8 @@ struct KvAttendArgs {
   float scale;
   void* out;
   float* lse;
+  KvPlan plan;
+  float* ws;  // plan.ws_bytes of partials
   ErrWord* err;
 };
 

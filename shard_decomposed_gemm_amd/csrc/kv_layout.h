@@ -30,4 +30,55 @@ KV_HD inline int64_t kv_block_at(const KvLayout& L, int64_t page, int h, int i) 
 KV_HD inline int kv_value_quarter(int t) { return (t >> 2) & 3; }
 KV_HD inline int kv_value_place(int t) { return ((t >> 4) << 2) | (t & 3); }
 
+// How one attention call's work is laid out. Rows of a kv head's item are its
+// query heads of all queries, r = query * G + head. Each item's blocks of 32
+// tokens go in runs of `chunk` to `splits` workgroups at most (longer runs
+// where a sequence has more blocks than that); the partials of an item with
+// several runs meet in the workspace, one slot per (item, run).
+struct KvPlan {
+  int32_t many;    // 0: the kernel for few rows, 1: for many
+  int32_t rows;    // rows of one item
+  int32_t tiles;   // items of one sequence and kv head
+  int32_t splits;
+  int32_t chunk;   // blocks of a run
+  int64_t items;
+  int64_t slot_floats;  // of one partial: rows x D, then rows x (exponent, sum)
+  int64_t ws_bytes;
+};
+
+constexpr int kKvMaxSplits = 256;
+
+// Blocks that a run of an item with nblk blocks has, and the runs.
+KV_HD inline int kv_run_blocks(int chunk, int splits, int nblk) {
+  const int need = (nblk + splits - 1) / splits;
+  return need > chunk ? need : chunk;
+}
+KV_HD inline int kv_runs(int chunk, int splits, int nblk) {
+  const int c = kv_run_blocks(chunk, splits, nblk);
+  return nblk <= c ? 1 : (nblk + c - 1) / c;
+}
+
+inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
+  KvPlan p;
+  const int64_t rows = max_q * (L.Hq / L.Hkv);
+  p.many = rows > (L.D == 256 ? 16 : 32);
+  p.rows = p.many ? 128 : rows > 16 ? 32 : 16;
+  p.tiles = (int32_t)(p.many ? (rows + p.rows - 1) / p.rows : 1);
+  p.items = batch * L.Hkv * p.tiles;
+  const int64_t nblk = (max_kv + 31) / 32;
+  // Runs of equal length keep ragged batches even: several for each place on
+  // the chip there, one where a single sequence makes them equal anyway.
+  const int64_t places = (int64_t)num_cus * (p.many ? 4 : batch > 1 ? 6 : 2);
+  int64_t chunk = (p.items * nblk + places - 1) / places;
+  if (chunk < 32) chunk = 32;
+  int64_t splits = (nblk + chunk - 1) / chunk;
+  if (splits < 1) splits = 1;
+  if (splits > kKvMaxSplits) splits = kKvMaxSplits;
+  p.chunk = (int32_t)(chunk < (int64_t{1} << 26) ? chunk : int64_t{1} << 26);
+  p.splits = (int32_t)splits;
+  p.slot_floats = (int64_t)p.rows * (L.D + 2);
+  p.ws_bytes = p.splits > 1 ? p.items * p.splits * p.slot_floats * 4 : 0;
+  return p;
+}
+
 }  // namespace agemm

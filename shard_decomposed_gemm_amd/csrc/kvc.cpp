@@ -146,17 +146,21 @@ int kvc_append(kvc_ctx* ctx, void* pages, const kvc_append_args* p, void* stream
 
 int kvc_attend_workspace(const kvc_ctx* ctx, int32_t batch, int32_t max_q, int64_t max_kv, int64_t* bytes) {
   if (!ctx || !bytes || batch < 0 || max_q < 1 || max_kv < 1) return AGEMM_EINVAL;
-  *bytes = 0;
+  if (batch > kKvMaxTokens || max_q > kKvMaxTokens) return AGEMM_ESHAPE;
+  const KvPlan plan = kv_attend_plan(ctx->L, batch, max_q, max_kv, ctx->num_cus);
+  if (plan.items > kKvMaxItems) return AGEMM_ESHAPE;
+  *bytes = plan.ws_bytes;
   return AGEMM_OK;
 }
 
 int kvc_attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, void* workspace, int64_t workspace_bytes,
                void* stream) {
   if (!ctx) return AGEMM_EINVAL;
-  int64_t need = 0;
-  if (p) (void)kvc_attend_workspace(ctx, p->batch, p->max_q, p->max_kv, &need);
+  KvPlan plan{};
+  if (p && p->batch >= 0 && p->max_q >= 1 && p->max_kv >= 1)  // refused below otherwise
+    plan = kv_attend_plan(ctx->L, p->batch, p->max_q, p->max_kv, ctx->num_cus);
   char why[kKvWhy];
-  const int rc = kv_check_attend(ctx->L, pages, p, need, workspace, workspace_bytes, why);
+  const int rc = kv_check_attend(ctx->L, pages, p, plan, workspace, workspace_bytes, why);
   if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);
 
   KvAttendArgs a{};
@@ -178,6 +182,8 @@ int kvc_attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, void* 
   a.scale = p->scale;
   a.out = p->out;
   a.lse = p->lse;
+  a.plan = plan;
+  a.ws = static_cast<float*>(workspace);
   a.err = ctx->err_dev;
   OnDevice on(ctx->device);
   if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");

@@ -18,8 +18,11 @@ int kvh_append(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages, const
 
 int kvh_attend(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages, const void* pages, const kvc_attend_args* p,
                int64_t need, const void* workspace, int64_t workspace_bytes, char* why) {
-  return kv_check_attend(kv_layout(Hq, Hkv, D, page_tokens, num_pages), pages, p, need, workspace, workspace_bytes,
-                         why);
+  const KvLayout L = kv_layout(Hq, Hkv, D, page_tokens, num_pages);
+  KvPlan plan{};
+  if (p && p->batch >= 0 && p->max_q >= 1 && p->max_kv >= 1) plan = kv_attend_plan(L, p->batch, p->max_q, p->max_kv, 256);
+  plan.ws_bytes = need;
+  return kv_check_attend(L, pages, p, plan, workspace, workspace_bytes, why);
 }
 
 int kvh_read(const void* pages, int64_t tokens, const int64_t* slots, const void* k_out, const void* v_out, char* why) {
@@ -36,5 +39,16 @@ int64_t kvh_block(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages, in
   *place = kv_value_place(*token);
   return kv_block_at(L, slot >> L.page_shift, h, off >> 5);
 }
+
+// The work plan: many, rows, tiles, splits, chunk, items, slot_floats, ws_bytes.
+void kvh_plan(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages, int64_t batch, int64_t max_q, int64_t max_kv,
+              int num_cus, int64_t* out) {
+  const KvPlan p = kv_attend_plan(kv_layout(Hq, Hkv, D, page_tokens, num_pages), batch, max_q, max_kv, num_cus);
+  const int64_t v[8] = {p.many, p.rows, p.tiles, p.splits, p.chunk, p.items, p.slot_floats, p.ws_bytes};
+  for (int i = 0; i < 8; ++i) out[i] = v[i];
+}
+
+int kvh_run_blocks(int chunk, int splits, int nblk) { return kv_run_blocks(chunk, splits, nblk); }
+int kvh_runs(int chunk, int splits, int nblk) { return kv_runs(chunk, splits, nblk); }
 
 }  // extern "C"

@@ -37,6 +37,8 @@ def host(tmp_path_factory):
     lib.kvh_read.argtypes = [vp, i64, vp, vp, vp, ctypes.c_char_p]
     lib.kvh_block.argtypes = shape + [i64, ctypes.c_int] + [ctypes.POINTER(ctypes.c_int)] * 3
     lib.kvh_block.restype = i64
+    lib.kvh_plan.argtypes = shape + [i64, i64, i64, ctypes.c_int, ctypes.POINTER(i64)]
+    lib.kvh_plan.restype = None
     return lib
 
 
@@ -144,6 +146,29 @@ def test_layout_functions_agree_with_the_oracle(host, D, page_tokens, Hkv):
                 assert 32 * D + 128 + 2 * (8 * c[1].value + c[2].value) == at[off % 32]
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(64, 8, 128), (96, 96, 128), (12, 1, 128), (16, 2, 256), (32, 4, 64), (72, 1, 64)])
+def test_plan_covers_every_block_once_within_its_workspace(host, Hq, Hkv, D):
+    """Runs of blocks partition every length, the longest that fits 32 bits among them, in no more runs than the grid
+    and the workspace have; a longer sequence than max_kv is covered too."""
+    v = (ctypes.c_int64 * 8)()
+    for batch in (1, 2, 7, 64, 500, 8192):
+        for max_q in (1, 2, 5, 33, 700):
+            for max_kv in (1, 33, 777, 4099, 65536, 262144, (1 << 31) - 1):
+                host.kvh_plan(Hq, Hkv, D, 64, 1000, batch, max_q, max_kv, 256, v)
+                many, rows, tiles, splits, chunk, items, slot, ws = v
+                assert 1 <= splits <= 256 and chunk >= 1 and items == batch * Hkv * tiles
+                assert tiles * rows >= max_q * (Hq // Hkv) and (many or tiles == 1)
+                assert slot == rows * (D + 2) and ws == (items * splits * slot * 4 if splits > 1 else 0)
+                assert splits == 1 or items * rows < 1 << 24  # the join's grid
+                for n in (0, 1, 2, 31, 32, 33, 64, 1000, (max_kv + 31) // 32, (max_kv + 31) // 32 * 3, 1 << 26):
+                    if n > 1 << 26:
+                        continue
+                    c, r = host.kvh_run_blocks(chunk, splits, n), host.kvh_runs(chunk, splits, n)
+                    assert 1 <= r <= splits and c >= 1
+                    assert (r - 1) * c < max(n, 1) <= r * c < 1 << 31
+                    assert n > 0 or r == 1
+
+
 # ---------------------------------------------------------------- refusals
 
 SHAPE = (16, 4, 128, 64, 10)
@@ -239,7 +264,7 @@ def test_attend_accepts(host):
 @pytest.mark.parametrize("change,code", [
     (dict(batch=-1), agemm.EINVAL), (dict(tokens=-1), agemm.EINVAL), (dict(max_q=0), agemm.EINVAL),
     (dict(max_kv=0), agemm.EINVAL), (dict(tokens=(1 << 23) + 1), agemm.ESHAPE), (dict(max_q=(1 << 23) + 1), agemm.ESHAPE),
-    (dict(batch=(1 << 23) + 1), agemm.ESHAPE), (dict(causal=2), agemm.EINVAL), (dict(out_f32=2), agemm.EINVAL),
+    (dict(batch=(1 << 23) + 1), agemm.ESHAPE), (dict(batch=1 << 22, max_q=1 << 8), agemm.ESHAPE), (dict(causal=2), agemm.EINVAL), (dict(out_f32=2), agemm.EINVAL),
     (dict(scale=float("nan")), agemm.EINVAL), (dict(scale=float("inf")), agemm.EINVAL),
     (dict(table_width=0), agemm.EINVAL), (dict(table_stride=7), agemm.EINVAL), (dict(table_stride=-8), agemm.EINVAL),
     (dict(q_start=None), agemm.EINVAL), (dict(q_start=None, max_q=1, batch=13), agemm.EINVAL),
