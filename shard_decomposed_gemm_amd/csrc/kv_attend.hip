@@ -81,6 +81,23 @@ __device__ inline half8v query_operand(const _Float16* q) {
   return half8v{v[0], v[4], v[1], v[5], v[2], v[6], v[3], v[7]};
 }
 
+// Weights p0 and p1 as elements i and i + 1 of the binary16 operand hi, with
+// what the cut loses in lo (F32), or rounded (without lo).
+template <bool F32>
+__device__ inline void split_weight(float p0, float p1, half8v& hi, half8v& lo, int i) {
+  if constexpr (F32) {
+    const auto c = __builtin_amdgcn_cvt_pkrtz(p0, p1);
+    hi[i] = (_Float16)c[0];
+    hi[i + 1] = (_Float16)c[1];
+    const auto d = __builtin_amdgcn_cvt_pkrtz(p0 - (float)hi[i], p1 - (float)hi[i + 1]);
+    lo[i] = (_Float16)d[0];
+    lo[i + 1] = (_Float16)d[1];
+  } else {
+    hi[i] = (_Float16)p0;
+    hi[i + 1] = (_Float16)p1;
+  }
+}
+
 // A sequence's rows and lengths, checked against what the call gave.
 struct Sequence {
   int64_t row0;  // its first row of q
@@ -94,34 +111,35 @@ struct Sequence {
   }
 };
 
+// A value that is the same in all lanes, kept in a scalar register.
+__device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 __device__ inline Sequence sequence(const KvAttendArgs& a, int b, bool tell) {
   Sequence s;
-  int64_t end;
+  int start = b, end = b + 1;
   if (a.q_start) {
-    s.row0 = a.q_start[b];
-    end = a.q_start[b + 1];
-  } else {
-    s.row0 = b;
-    end = b + 1;
+    start = uniform(a.q_start[b]);
+    end = uniform(a.q_start[b + 1]);
   }
-  const int64_t n = end - s.row0;
-  const bool usable = n >= 0 && n <= a.max_q && s.row0 >= 0 && end <= a.tokens;
+  const int len = uniform(a.kv_len[b]);
+  const int64_t n = (int64_t)end - start;
+  s.off = !a.causal ? (int64_t)1 << 32 : a.q_off ? (int64_t)uniform(a.q_off[b]) : 0;
+  const bool usable = n >= 0 && n <= a.max_q && start >= 0 && end <= a.tokens;
   if (!usable && tell) kv_report(a.err, kKvRows, b, n, a.max_q);
   s.n = usable ? (int)n : 0;
+  s.row0 = start;
   const int64_t most = (int64_t)a.table_width << a.L.page_shift;
-  s.len = a.kv_len[b];
-  if (s.len < 0 || s.len > most) {
-    if (tell) kv_report(a.err, kKvLength, b, s.len, most);
-    s.len = s.len < 0 ? 0 : (int)most;
-  }
-  s.off = !a.causal ? (int64_t)s.len : a.q_off ? (int64_t)a.q_off[b] : (int64_t)s.len - n;
+  const bool fits = len >= 0 && len <= most;
+  if (!fits && tell) kv_report(a.err, kKvLength, b, len, most);
+  s.len = len < 0 ? 0 : len <= most ? len : (int)most;
+  if (a.causal && !a.q_off) s.off = (int64_t)s.len - n;
   return s;
 }
 
 // Block j of a sequence: its bytes, or nullptr if its page is not in the cache.
 __device__ inline const char* block_at(const KvAttendArgs& a, int b, int h, int j, bool tell) {
   const int in_page = a.L.page_shift - 5;
-  const int64_t page = a.table[(int64_t)b * a.table_stride + (j >> in_page)];
+  const int page = uniform(a.table[(int64_t)b * a.table_stride + (j >> in_page)]);
   if (page < 0 || page >= a.L.num_pages) {
     if (tell) kv_report(a.err, kKvPage, b, page, a.L.num_pages);
     return nullptr;
@@ -150,155 +168,56 @@ __device__ inline void store_out(void* out, int64_t at, const float (&v)[N]) {
 
 // For at most 16 NT rows a kv head (single tokens, drafts): HBM-bound, each
 // cached byte read once. A workgroup takes a run of an item's blocks; its waves
-// take every kWaves-th block each, with loads one block ahead and no barrier,
-// and join their sums at the end. A wave holds all rows of the item as the 16
-// columns of its products (NT times), and a block of 32 keys as two tiles of 16.
+// take every kWaves-th block each, with no barrier, and join their sums at the
+// end. A wave holds all rows of the item as the 16 columns of its products (NT
+// times), and a block of 32 keys as two tiles of 16. The next block's keys are
+// loaded when this block's are used up, its values likewise.
 constexpr int kWaves = 8;
 
 template <int D>
-struct Raw {  // one block as a lane reads it
-  uint32_t k[2][D / 32];
-  half2v kp[2];
-  uint4v v[D / 64];
-  uint4v vs, vb;
+struct RawKeys {  // a block's keys as a lane reads them
+  uint32_t w[2][D / 32];
+  half2v pair[2];
+};
+template <int D>
+struct RawValues {
+  uint4v w[D / 64];
+  uint4v s, b;
 };
 
 template <int D>
-__device__ inline void load_block(Raw<D>& r, const char* blk, int col, int quarter) {
+__device__ inline void load_keys(RawKeys<D>& r, const char* blk, int col, int quarter) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const char* row = blk + (t * 16 + col) * (D / 2) + quarter * (D / 8);
     if constexpr (D == 64) {
       const uint2v w = *reinterpret_cast<const uint2v*>(row);
-      r.k[t][0] = w.x;
-      r.k[t][1] = w.y;
+      r.w[t][0] = w.x;
+      r.w[t][1] = w.y;
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
         const uint4v w = *reinterpret_cast<const uint4v*>(row + 16 * i);
-        r.k[t][4 * i] = w.x;
-        r.k[t][4 * i + 1] = w.y;
-        r.k[t][4 * i + 2] = w.z;
-        r.k[t][4 * i + 3] = w.w;
+        r.w[t][4 * i] = w.x;
+        r.w[t][4 * i + 1] = w.y;
+        r.w[t][4 * i + 2] = w.z;
+        r.w[t][4 * i + 3] = w.w;
       }
     }
-    r.kp[t] = *reinterpret_cast<const half2v*>(blk + 32 * D + 4 * (t * 16 + col));
+    r.pair[t] = *reinterpret_cast<const half2v*>(blk + 32 * D + 4 * (t * 16 + col));
   }
+}
+template <int D>
+__device__ inline void load_values(RawValues<D>& r, const char* blk, int col, int quarter) {
 #pragma unroll
   for (int g = 0; g < D / 64; ++g)
-    r.v[g] = *reinterpret_cast<const uint4v*>(blk + 16 * D + ((g * 4 + quarter) * 16 + col) * 16);
-  r.vs = *reinterpret_cast<const uint4v*>(blk + 32 * D + 128 + quarter * 16);
-  r.vb = *reinterpret_cast<const uint4v*>(blk + 32 * D + 192 + quarter * 16);
+    r.w[g] = *reinterpret_cast<const uint4v*>(blk + 16 * D + ((g * 4 + quarter) * 16 + col) * 16);
+  r.s = *reinterpret_cast<const uint4v*>(blk + 32 * D + 128 + quarter * 16);
+  r.b = *reinterpret_cast<const uint4v*>(blk + 32 * D + 192 + quarter * 16);
 }
 
 template <int D, int NT, bool F32>
-struct FewState {
-  half8v q[NT][D / 32];
-  float4v o[NT][D / 16];  // O^T: row 4 quarter + i of tile m is channel (4 quarter + i) D / 16 + m
-  float base[NT];         // m - kShift
-  float sum[NT];          // of this lane's weights
-  int seen[NT];           // keys that the column's row sees
-};
-
-// Folds one block in. MASK: some row does not see all of it, or it is the sequence's last.
-template <int D, int NT, bool F32, bool MASK>
-__device__ inline void take_block(FewState<D, NT, F32>& st, const Raw<D>& r, int j, int len, int quarter, float factor) {
-  float4v s[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = float4v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const half2v sc = {r.kp[t].x, r.kp[t].x}, of = {r.kp[t].y, r.kp[t].y};
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const half8v k = key_operand(r.k[t][i], sc, of);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, st.q[n][i], s[n][t], 0, 0, 0);
-    }
-  }
-
-  half8v hi[NT], lo[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float e[8];
-    float top = -__builtin_inff();
-    const int left = st.seen[n] - (j * 32 + quarter * 4);
-    auto exponents = [&](float base) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x = __builtin_fmaf(s[n][t][i], factor, -base);
-          if (MASK && t * 16 + i >= left) x = -__builtin_inff();
-          e[4 * t + i] = x;
-        }
-      top = fmaxf(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])), fmaxf(fmaxf(e[4], e[5]), fmaxf(e[6], e[7])));
-    };
-    exponents(st.base[n]);
-    if (__any(top > kTop)) {  // a new maximum, for some column
-      exponents(0.f);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float base = fmaxf(st.base[n], top - kShift);
-      const float f = exp2_hw(st.base[n] - base);
-      st.sum[n] *= f;
-#pragma unroll
-      for (int m = 0; m < D / 16; ++m) st.o[n][m] *= f;
-      st.base[n] = base;
-      exponents(base);
-    }
-    float p[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[i] = exp2_hw(e[i]);
-      st.sum[n] += p[i];
-    }
-    if constexpr (F32) {
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const auto c = __builtin_amdgcn_cvt_pkrtz(p[i], p[i + 1]);
-        hi[n][i] = (_Float16)c[0];
-        hi[n][i + 1] = (_Float16)c[1];
-        const auto d = __builtin_amdgcn_cvt_pkrtz(p[i] - (float)hi[n][i], p[i + 1] - (float)hi[n][i + 1]);
-        lo[n][i] = (_Float16)d[0];
-        lo[n][i + 1] = (_Float16)d[1];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) hi[n][i] = (_Float16)p[i];
-    }
-  }
-
-  half2v vs[4], vb[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    vs[i] = halves(r.vs[i]);
-    vb[i] = halves(r.vb[i]);
-    if constexpr (MASK) {  // what lies behind the sequence's end may be anything
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int e = 2 * i + x;
-        if (j * 32 + (e >> 2) * 16 + quarter * 4 + (e & 3) >= len) vs[i][x] = vb[i][x] = (_Float16)0.f;
-      }
-    }
-  }
-#pragma unroll
-  for (int g = 0; g < D / 64; ++g) {
-    const half8v v[4] = {value_operand<0>(r.v[g], vs, vb), value_operand<1>(r.v[g], vs, vb),
-                         value_operand<2>(r.v[g], vs, vb), value_operand<3>(r.v[g], vs, vb)};
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float4v& o = st.o[n][4 * g + x];
-        o = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[x], hi[n], o, 0, 0, 0);
-        if constexpr (F32) o = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[x], lo[n], o, 0, 0, 0);
-      }
-  }
-}
-
-template <int D, int NT, bool F32>
-__global__ __launch_bounds__(kWaves * 64, NT * D > 64 ? 2 : 4) void kv_attend_few_kernel(KvAttendArgs a) {
+__global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void kv_attend_few_kernel(KvAttendArgs a) {
   constexpr int MT = D / 16;
   __shared__ float4v merge[kWaves / 2 * NT * MT * 64];
   __shared__ float heads[2][kWaves][NT * 16];
@@ -318,65 +237,156 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 64 ? 2 : 4) void kv_attend_fe
   const int j1 = nblk < (run + 1) * chunk ? nblk : (run + 1) * chunk;
   int j = run * chunk + wave;
 
-  FewState<D, NT, F32> st;
+  half8v q[NT][D / 32];
+  float4v o[NT][MT];  // O^T: row 4 quarter + i of tile m is channel (4 quarter + i) D / 16 + m
+  float base[NT];     // m - kShift
+  float sum[NT];      // of this lane's weights
+  int seen[NT];       // keys that the column's row sees
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = n * 16 + col;
     const bool live = r < rows;
     const int i = r / G;
-    const _Float16* q = a.q + (seq.row0 + i) * a.q_ts + (int64_t)(h * G + r - i * G) * a.q_hs + quarter * (D / 4);
+    const _Float16* src = a.q + (seq.row0 + i) * a.q_ts + (int64_t)(h * G + r - i * G) * a.q_hs + quarter * (D / 4);
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) st.q[n][x] = live ? query_operand(q + 8 * x) : half8v{};
-    st.seen[n] = live ? seq.seen(i) : seq.len;
-    st.base[n] = kNoMax;
-    st.sum[n] = 0.f;
+    for (int x = 0; x < D / 32; ++x) q[n][x] = live ? query_operand(src + 8 * x) : half8v{};
+    seen[n] = live ? seq.seen(i) : seq.len;
+    base[n] = kNoMax;
+    sum[n] = 0.f;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) st.o[n][m] = float4v{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < MT; ++m) o[n][m] = float4v{0.f, 0.f, 0.f, 0.f};
   }
   const int whole = seq.seen(0) >> 5;  // blocks that every row sees whole
   const float factor = a.scale * kLog2e;
-  const bool tell = lane == 0;
 
-  auto take = [&](const Raw<D>& r, int at) {
-    if (at < whole) take_block<D, NT, F32, false>(st, r, at, seq.len, quarter, factor);
-    else take_block<D, NT, F32, true>(st, r, at, seq.len, quarter, factor);
+  // A block without a page is read from the first page and hidden from every row.
+  RawKeys<D> k;
+  RawValues<D> v;
+  bool paged = false;
+  const char* blk = nullptr;
+  auto find = [&](int at) {
+    blk = block_at(a, b, h, at, lane == 0);
+    paged = blk != nullptr;
+    if (!paged) blk = a.pages;
   };
-  Raw<D> x, y;
-  const char *bx = nullptr, *by = nullptr;
-  if (j < j1 && (bx = block_at(a, b, h, j, tell))) load_block<D>(x, bx, col, quarter);
-  while (j < j1) {
-    if (j + kWaves < j1 && (by = block_at(a, b, h, j + kWaves, tell))) load_block<D>(y, by, col, quarter);
-    if (bx) take(x, j);
-    j += kWaves;
-    if (j >= j1) break;
-    if (j + kWaves < j1 && (bx = block_at(a, b, h, j + kWaves, tell))) load_block<D>(x, bx, col, quarter);
-    if (by) take(y, j);
-    j += kWaves;
+  if (j < j1) {
+    find(j);
+    load_keys<D>(k, blk, col, quarter);
+    load_values<D>(v, blk, col, quarter);
+  }
+  for (; j < j1; j += kWaves) {
+    const bool hide = j >= whole || !paged;
+    const int end = paged ? seq.len - j * 32 : 0;  // tokens of this block that hold anything
+    const bool more = j + kWaves < j1;
+    if (more) find(j + kWaves);
+
+    float4v s[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = float4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const half2v sc = {k.pair[t].x, k.pair[t].x}, of = {k.pair[t].y, k.pair[t].y};
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const half8v kk = key_operand(k.w[t][i], sc, of);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, q[n][i], s[n][t], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (more) load_keys<D>(k, blk, col, quarter);
+
+    half8v hi[NT], lo[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float e[8];
+      float top;
+      const int left = (end > 0 ? seen[n] - j * 32 : 0) - quarter * 4;
+      auto exponents = [&](float bs) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = __builtin_fmaf(s[n][i >> 2][i & 3], factor, -bs);
+        if (hide) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((i >> 2) * 16 + (i & 3) >= left) e[i] = -__builtin_inff();
+        }
+        top = fmaxf(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])), fmaxf(fmaxf(e[4], e[5]), fmaxf(e[6], e[7])));
+      };
+      exponents(base[n]);
+      if (__any(top > kTop)) {  // a new maximum, for some column
+        exponents(0.f);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float nb = fmaxf(base[n], top - kShift);
+        const float f = exp2_hw(base[n] - nb);
+        sum[n] *= f;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) o[n][m] *= f;
+        base[n] = nb;
+        exponents(nb);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float p0 = exp2_hw(e[i]), p1 = exp2_hw(e[i + 1]);
+        sum[n] += p0;
+        sum[n] += p1;
+        split_weight<F32>(p0, p1, hi[n], lo[n], i);
+      }
+    }
+
+    half2v vs[4], vb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      vs[i] = halves(v.s[i]);
+      vb[i] = halves(v.b[i]);
+    }
+    if (hide) {  // what lies behind the sequence's end may be anything
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if ((e >> 2) * 16 + quarter * 4 + (e & 3) >= end) vs[e >> 1][e & 1] = vb[e >> 1][e & 1] = (_Float16)0.f;
+    }
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g) {
+      auto multiply = [&](half8v vv, int m) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          o[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, hi[n], o[n][m], 0, 0, 0);
+          if constexpr (F32) o[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, lo[n], o[n][m], 0, 0, 0);
+        }
+      };
+      multiply(value_operand<0>(v.w[g], vs, vb), 4 * g);
+      multiply(value_operand<1>(v.w[g], vs, vb), 4 * g + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(value_operand<2>(v.w[g], vs, vb), 4 * g + 2);
+      multiply(value_operand<3>(v.w[g], vs, vb), 4 * g + 3);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (more) load_values<D>(v, blk, col, quarter);
   }
 
   // Join the waves: a common base, then sums by halves, in a fixed order.
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    st.sum[n] += __shfl_xor(st.sum[n], 16);
-    st.sum[n] += __shfl_xor(st.sum[n], 32);
+    sum[n] += __shfl_xor(sum[n], 16);
+    sum[n] += __shfl_xor(sum[n], 32);
     if (quarter == 0) {
-      heads[0][wave][n * 16 + col] = st.base[n];
-      heads[1][wave][n * 16 + col] = st.sum[n];
+      heads[0][wave][n * 16 + col] = base[n];
+      heads[1][wave][n * 16 + col] = sum[n];
     }
   }
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float top = kNoMax, sum = 0.f;
+    float top = kNoMax, all = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) top = fmaxf(top, heads[0][w][n * 16 + col]);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) sum += heads[1][w][n * 16 + col] * exp2_hw(heads[0][w][n * 16 + col] - top);
-    const float f = exp2_hw(st.base[n] - top);
+    for (int w = 0; w < kWaves; ++w) all += heads[1][w][n * 16 + col] * exp2_hw(heads[0][w][n * 16 + col] - top);
+    const float f = exp2_hw(base[n] - top);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) st.o[n][m] *= f;
-    st.base[n] = top;
-    st.sum[n] = sum;
+    for (int m = 0; m < MT; ++m) o[n][m] *= f;
+    base[n] = top;
+    sum[n] = all;
   }
 #pragma unroll
   for (int half = kWaves / 2; half > 0; half >>= 1) {
@@ -384,14 +394,14 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 64 ? 2 : 4) void kv_attend_fe
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) merge[((wave - half) * NT * MT + n * MT + m) * 64 + lane] = st.o[n][m];
+        for (int m = 0; m < MT; ++m) merge[((wave - half) * NT * MT + n * MT + m) * 64 + lane] = o[n][m];
     }
     __syncthreads();
     if (wave < half) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) st.o[n][m] += merge[(wave * NT * MT + n * MT + m) * 64 + lane];
+        for (int m = 0; m < MT; ++m) o[n][m] += merge[(wave * NT * MT + n * MT + m) * 64 + lane];
     }
     __syncthreads();
   }
@@ -402,25 +412,25 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 64 ? 2 : 4) void kv_attend_fe
     const int r = n * 16 + col;
     if (r >= rows) continue;
     const int i = r / G;
-    const int64_t o = (seq.row0 + i) * a.L.Hq + h * G + r - i * G;
+    const int64_t at = (seq.row0 + i) * a.L.Hq + h * G + r - i * G;
     const bool last = runs == 1;
     float* slot = last ? nullptr : a.ws + ((int64_t)item * a.plan.splits + run) * a.plan.slot_floats;
-    const float inv = !last ? 1.f : st.sum[n] != 0.f ? 1.f / st.sum[n] : 0.f;
+    const float inv = !last ? 1.f : sum[n] != 0.f ? 1.f / sum[n] : 0.f;
 #pragma unroll
     for (int y4 = 0; y4 < 4; ++y4) {
-      float v[MT];
+      float w[MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) v[m] = st.o[n][m][y4] * inv;
+      for (int m = 0; m < MT; ++m) w[m] = o[n][m][y4] * inv;
       const int d0 = (quarter * 4 + y4) * MT;
-      if (last) store_out<F32>(a.out, o * D + d0, v);
-      else store_out<true>(slot, (int64_t)r * D + d0, v);
+      if (last) store_out<F32>(a.out, at * D + d0, w);
+      else store_out<true>(slot, (int64_t)r * D + d0, w);
     }
     if (quarter == 0) {
       if (last) {
-        if (a.lse) a.lse[o] = st.sum[n] != 0.f ? (st.base[n] + log2f(st.sum[n])) * kLn2 : kLowest;
+        if (a.lse) a.lse[at] = sum[n] != 0.f ? (base[n] + log2f(sum[n])) * kLn2 : kLowest;
       } else {
-        slot[a.plan.rows * D + 2 * r] = st.base[n];
-        slot[a.plan.rows * D + 2 * r + 1] = st.sum[n];
+        slot[a.plan.rows * D + 2 * r] = base[n];
+        slot[a.plan.rows * D + 2 * r + 1] = sum[n];
       }
     }
   }
@@ -491,7 +501,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
   float base = kNoMax, sum = 0.f;
 
   // This thread's piece of a tile: block, and within it the key row's piece and the value piece.
-  const int piece = tid & (D - 1), pb = tid / D;
+  const int piece = tid & (D - 1), pb = uniform(tid / D);
   const int ktok = piece / RN, krun = piece % RN;
   const int vq = (piece >> 4) & 3, vc = piece & 15, vg = piece >> 6;
   uint4v kr, vr, vsr, vbr;
@@ -556,9 +566,11 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
     const int left = seen - (j * 32 + hh * 4);
     auto exponents = [&](float bs) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        e[i] = __builtin_fmaf(s[i], factor, -bs);
-        if (mask && 8 * (i >> 2) + (i & 3) >= left) e[i] = -__builtin_inff();
+      for (int i = 0; i < 16; ++i) e[i] = __builtin_fmaf(s[i], factor, -bs);
+      if (mask) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (8 * (i >> 2) + (i & 3) >= left) e[i] = -__builtin_inff();
       }
       top = e[0];
 #pragma unroll
@@ -583,18 +595,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
       sum += p0;
       sum += p1;
       // group i / 4 of four keys: elements 0..3 of product 0 and 1, then 4..7
-      const int u = (i >> 2) & 1, x = (i >> 3) * 4 + (i & 3);
-      if constexpr (F32) {
-        const auto c = __builtin_amdgcn_cvt_pkrtz(p0, p1);
-        hi[u][x] = (_Float16)c[0];
-        hi[u][x + 1] = (_Float16)c[1];
-        const auto d = __builtin_amdgcn_cvt_pkrtz(p0 - (float)hi[u][x], p1 - (float)hi[u][x + 1]);
-        lo[u][x] = (_Float16)d[0];
-        lo[u][x + 1] = (_Float16)d[1];
-      } else {
-        hi[u][x] = (_Float16)p0;
-        hi[u][x + 1] = (_Float16)p1;
-      }
+      split_weight<F32>(p0, p1, hi[(i >> 2) & 1], lo[(i >> 2) & 1], (i >> 3) * 4 + (i & 3));
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -613,12 +614,10 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
     __syncthreads();
     int buf = 0;
     for (int jt = j0; jt < j1; jt += KB, buf ^= 1) {
-#pragma unroll
+#pragma unroll 1
       for (int kb = 0; kb < KB; ++kb) {
         const int j = jt + kb;
-        if (j >= j1 || j >= none || !there[buf][kb]) continue;
-        if (j < whole) take(j, buf, kb, false);
-        else take(j, buf, kb, true);
+        if (j < j1 && j < none && uniform(there[buf][kb])) take(j, buf, kb, j >= whole);
       }
       if (jt + KB < j1) {
         spread(jt + KB, buf ^ 1);
@@ -666,7 +665,7 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(KvAttendArgs a) {
   constexpr int E = D / 64;
   __shared__ float acc[3][D], sums[3];
   const int rpi = a.plan.rows;
-  const int item = blockIdx.x / rpi, lr = blockIdx.x - item * rpi;
+  const int item = blockIdx.x / a.plan.join_rows, lr = blockIdx.x - item * a.plan.join_rows;
   const int G = a.L.Hq / a.L.Hkv;
   int b, h, r0;
   if (a.plan.many) {
@@ -737,7 +736,7 @@ hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
   else if constexpr (D <= 128)
     hipLaunchKernelGGL((kv_attend_few_kernel<D, 2, F32>), grid, dim3(kWaves * 64), 0, s, a);
   if (a.plan.splits > 1)
-    hipLaunchKernelGGL((kv_attend_join_kernel<D, F32>), dim3((unsigned)(a.plan.items * a.plan.rows)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((kv_attend_join_kernel<D, F32>), dim3((unsigned)(a.plan.items * a.plan.join_rows)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -38,6 +38,7 @@ KV_HD inline int kv_value_place(int t) { return ((t >> 4) << 2) | (t & 3); }
 struct KvPlan {
   int32_t many;    // 0: the kernel for few rows, 1: for many
   int32_t rows;    // rows of one item
+  int32_t join_rows;  // of them, those that a sequence of max_q queries can have
   int32_t tiles;   // items of one sequence and kv head
   int32_t splits;
   int32_t chunk;   // blocks of a run
@@ -63,12 +64,13 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
   const int64_t rows = max_q * (L.Hq / L.Hkv);
   p.many = rows > (L.D == 256 ? 16 : 32);
   p.rows = p.many ? 128 : rows > 16 ? 32 : 16;
+  p.join_rows = (int32_t)(rows < p.rows ? rows : p.rows);
   p.tiles = (int32_t)(p.many ? (rows + p.rows - 1) / p.rows : 1);
   p.items = batch * L.Hkv * p.tiles;
   const int64_t nblk = (max_kv + 31) / 32;
   // Runs of equal length keep ragged batches even: several for each place on
   // the chip there, one where a single sequence makes them equal anyway.
-  const int64_t places = (int64_t)num_cus * (p.many ? 4 : batch > 1 ? 6 : 2);
+  const int64_t places = (int64_t)num_cus * (p.many ? 4 : batch > 1 ? 16 : 2);
   int64_t chunk = (p.items * nblk + places - 1) / places;
   if (chunk < 32) chunk = 32;
   int64_t splits = (nblk + chunk - 1) / chunk;

@@ -6,6 +6,7 @@ binding raises when the library is missing.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from . import agemm
 from .agemm import OK, AgemmError, status_string
@@ -35,6 +36,12 @@ class AttendArgs(ctypes.Structure):
                 ("out_f32", _i32), ("out", _vp), ("lse", _vp)]
 
 
+# The same structs as bytes: packing them costs a third of filling a ctypes.Structure, and these calls are made for
+# every layer of a decode step. Null pointers are 0.
+_CODE = {_vp: "P", _i32: "i", _i64: "q", _f32: "f"}
+_pack_append, _pack_attend = (struct.Struct("@" + "".join(_CODE[t] for _, t in st._fields_)).pack
+                              for st in (AppendArgs, AttendArgs))
+
 _ready = False
 
 
@@ -46,8 +53,8 @@ def load() -> ctypes.CDLL:
         lib.kvc_create.argtypes = [ctypes.POINTER(_vp), ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, _i64]
         lib.kvc_destroy.argtypes = [_vp]
         lib.kvc_page_bytes.argtypes = [_vp, ctypes.POINTER(_i64)]
-        lib.kvc_append.argtypes = [_vp, _vp, ctypes.POINTER(AppendArgs), _vp]
-        lib.kvc_attend.argtypes = [_vp, _vp, ctypes.POINTER(AttendArgs), _vp, _i64, _vp]
+        lib.kvc_append.argtypes = [_vp, _vp, _vp, _vp]  # a packed AppendArgs
+        lib.kvc_attend.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp]  # a packed AttendArgs
         lib.kvc_attend_workspace.argtypes = [_vp, _i32, _i32, _i64, ctypes.POINTER(_i64)]
         lib.kvc_read.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp]
         lib.kvc_check.argtypes = [_vp]
@@ -78,13 +85,15 @@ class KvCache:
         if rc != OK:
             raise AgemmError(rc, f"kvc_create: {status_string(rc)}")
         self._h = h
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = torch.cuda.current_device()
+        self.device = torch.device("cuda", self._index)
         n = _i64()
         lib.kvc_page_bytes(h, ctypes.byref(n))
         self.page_bytes = n.value
         self._f16, self._f32 = torch.float16, torch.float32
         self._i32, self._i64, self._u8 = torch.int32, torch.int64, torch.uint8
-        self._current = torch.cuda.current_stream
+        self._pages_shape, self._D = (self.num_pages, self.page_bytes), (self.D,)
+        self._current = torch._C._cuda_getCurrentRawStream
 
     # -- helpers
     def _raise(self, rc: int, what: str):
@@ -93,11 +102,11 @@ class KvCache:
             raise AgemmError(rc, f"{what}: {msg or status_string(rc)}")
 
     def _stream(self, stream):
-        return (stream if stream is not None else self._current(self.device)).cuda_stream or None
+        return stream.cuda_stream if stream is not None else self._current(self._index)
 
     def _plain(self, t, what, dtype, shape):
         """Pointer of a contiguous tensor of this context's device."""
-        if t.dtype is not dtype or t.device != self.device:
+        if t.dtype is not dtype or t.get_device() != self._index:
             raise TypeError(f"{what} must be a {dtype} tensor on {self.device}")
         if t.shape != shape:
             raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -107,7 +116,7 @@ class KvCache:
 
     def _heads(self, t, what, T, H):
         """Pointer, token and head stride of a (T, H, D) float16 tensor with contiguous channels."""
-        if t.dtype is not self._f16 or t.device != self.device:
+        if t.dtype is not self._f16 or t.get_device() != self._index:
             raise TypeError(f"{what} must be a float16 tensor on {self.device}")
         if t.shape != (T, H, self.D):
             raise ValueError(f"{what} must have shape {(T, H, self.D)}, got {tuple(t.shape)}")
@@ -117,7 +126,7 @@ class KvCache:
         return t.data_ptr(), st if T > 1 else H * self.D, sh if H > 1 else self.D
 
     def _pages(self, pages):
-        return self._plain(pages, "pages", self._u8, (self.num_pages, self.page_bytes))
+        return self._plain(pages, "pages", self._u8, self._pages_shape)
 
     # -- memory of the caller
     def new_pages(self):
@@ -144,7 +153,8 @@ class KvCache:
         if q is None and k is None:
             raise ValueError("neither q nor k given")
         T = (q if q is not None else k).shape[0]
-        qp = op = kp = vp = None
+        plain = self._plain
+        qp = op = kp = vp = rp = sp = pp = qw = kw = 0
         qt = qh = ot = oh = kt = kh = vt = vh = rl = rd = 0
         if q is not None:
             qp, qt, qh = self._heads(q, "q", T, self.Hq)
@@ -154,18 +164,19 @@ class KvCache:
             kp, kt, kh = self._heads(k, "k", T, self.Hkv)
         if v is not None:
             vp, vt, vh = self._heads(v, "v", T, self.Hkv)
+        if slots is not None:
+            sp = plain(slots, "slots", self._i64, (T,))
         if rope is not None:
             rl, rd = rope.shape
-            rp = self._plain(rope, "rope", self._f32, (rl, rd))
-        else:
-            rp = None
-        D = (self.D,)
-        args = AppendArgs(T, qp, kp, vp, op, qt, qh, kt, kh, vt, vh, ot, oh,
-                          None if slots is None else self._plain(slots, "slots", self._i64, (T,)),
-                          None if positions is None else self._plain(positions, "positions", self._i64, (T,)),
-                          rp, rl, rd, 1 if interleaved else 0,
-                          None if q_norm is None else self._plain(q_norm, "q_norm", self._f16, D),
-                          None if k_norm is None else self._plain(k_norm, "k_norm", self._f16, D), eps)
+            rp = plain(rope, "rope", self._f32, (rl, rd))
+        if positions is not None:
+            pp = plain(positions, "positions", self._i64, (T,))
+        if q_norm is not None:
+            qw = plain(q_norm, "q_norm", self._f16, self._D)
+        if k_norm is not None:
+            kw = plain(k_norm, "k_norm", self._f16, self._D)
+        args = _pack_append(T, qp, kp, vp, op, qt, qh, kt, kh, vt, vh, ot, oh, sp, pp, rp, rl, rd, bool(interleaved),
+                            qw, kw, eps)
         rc = self._lib.kvc_append(self._h, self._pages(pages) if pages is not None else None, args, self._stream(stream))
         if rc != OK:
             self._raise(rc, "kvc_append")
@@ -180,14 +191,16 @@ class KvCache:
         allocated on the stream for this call."""
         T = q.shape[0]
         B = kv_len.shape[0]
+        plain = self._plain
         qp, qt, qh = self._heads(q, "q", T, self.Hq)
         f32 = out.dtype is self._f32
-        outp = self._plain(out, "out", self._f32 if f32 else self._f16, (T, self.Hq, self.D))
-        if page_table.dtype is not self._i32 or page_table.device != self.device or page_table.dim() != 2:
+        outp = plain(out, "out", self._f32 if f32 else self._f16, (T, self.Hq, self.D))
+        lsep = 0 if lse is None else plain(lse, "lse", self._f32, (T, self.Hq))
+        if page_table.dtype is not self._i32 or page_table.get_device() != self._index or page_table.dim() != 2:
             raise TypeError(f"page_table must be a two-dimensional int32 tensor on {self.device}")
-        if page_table.shape[0] != B:
-            raise ValueError(f"page_table must have {B} rows, got {page_table.shape[0]}")
-        W = page_table.shape[1]
+        rows, W = page_table.shape
+        if rows != B:
+            raise ValueError(f"page_table must have {B} rows, got {rows}")
         ts, ws = page_table.stride()
         if W > 1 and ws != 1:
             raise ValueError("page_table must have contiguous rows")
@@ -196,17 +209,16 @@ class KvCache:
         handle = self._stream(stream)
         if workspace is None:
             import torch
-            with torch.cuda.stream(stream if stream is not None else self._current(self.device)):
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
                 workspace = self.workspace(B, max_q, max_kv)
-        elif workspace.dtype is not self._u8 or workspace.device != self.device or not workspace.is_contiguous():
+        elif workspace.dtype is not self._u8 or workspace.get_device() != self._index or not workspace.is_contiguous():
             raise TypeError(f"workspace must be a contiguous uint8 tensor on {self.device}")
-        args = AttendArgs(B, max_q, T, qp, qt, qh,
-                          None if q_start is None else self._plain(q_start, "q_start", self._i32, (B + 1,)),
-                          self._plain(kv_len, "kv_len", self._i32, (B,)),
-                          None if q_off is None else self._plain(q_off, "q_off", self._i32, (B,)),
-                          page_table.data_ptr(), ts if B > 1 else W, W, 1 if causal else 0, max_kv,
-                          self.D ** -0.5 if scale is None else scale, 1 if f32 else 0, outp,
-                          None if lse is None else self._plain(lse, "lse", self._f32, (T, self.Hq)))
+        args = _pack_attend(B, max_q, T, qp, qt, qh,
+                            0 if q_start is None else plain(q_start, "q_start", self._i32, (B + 1,)),
+                            plain(kv_len, "kv_len", self._i32, (B,)),
+                            0 if q_off is None else plain(q_off, "q_off", self._i32, (B,)),
+                            page_table.data_ptr(), ts if B > 1 else W, W, bool(causal), max_kv,
+                            self.D ** -0.5 if scale is None else scale, f32, outp, lsep)
         rc = self._lib.kvc_attend(self._h, self._pages(pages), args, workspace.data_ptr(), workspace.numel(), handle)
         if rc != OK:
             self._raise(rc, "kvc_attend")

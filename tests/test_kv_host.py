@@ -72,6 +72,14 @@ def test_argument_structs_have_the_headers_size(tmp_path):
     assert [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()] == want
 
 
+def test_packed_arguments_are_the_structs():
+    for st, pack in ((kvc.AppendArgs, kvc._pack_append), (kvc.AttendArgs, kvc._pack_attend)):
+        values = [i + 1 if t is not ctypes.c_float else i + 0.5 for i, (_, t) in enumerate(st._fields_)]
+        assert len(pack(*values)) <= ctypes.sizeof(st)  # without the padding at the end
+        got = st.from_buffer_copy(pack(*values).ljust(ctypes.sizeof(st), b"\0"))
+        assert [getattr(got, name) for name, _ in st._fields_] == values
+
+
 # ---------------------------------------------------------------- oracle
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -304,8 +312,8 @@ def test_read_refuses(host, args, code):
 def test_calls_without_a_context_are_refused():
     lib = kvc.load()
     n = ctypes.c_int64()
-    assert lib.kvc_append(None, None, _append(), None) == agemm.EINVAL
-    assert lib.kvc_attend(None, None, _attend(), None, 0, None) == agemm.EINVAL
+    assert lib.kvc_append(None, None, ctypes.byref(_append()), None) == agemm.EINVAL
+    assert lib.kvc_attend(None, None, ctypes.byref(_attend()), None, 0, None) == agemm.EINVAL
     assert lib.kvc_read(None, None, 0, None, None, None, None) == agemm.EINVAL
     assert lib.kvc_check(None) == agemm.EINVAL
     assert lib.kvc_page_bytes(None, ctypes.byref(n)) == agemm.EINVAL
