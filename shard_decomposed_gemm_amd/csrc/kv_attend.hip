@@ -21,6 +21,8 @@
 // rescaling. Below 2^(m - 26) weights lose bits to binary16's subnormals.
 // With binary32 outputs a weight enters the product as two binary16 numbers,
 // its value cut to binary16 and the rest.
+#include <type_traits>
+
 #include "kv_internal.h"
 
 namespace agemm {
@@ -42,15 +44,35 @@ constexpr float kTop = 15.f;        // and at most 2^kTop
 
 __device__ inline float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The constants that make (16 + n) of a nibble, in registers: with both as
+// literals the compiler takes an AND and an OR, with registers one instruction.
+struct Bits {
+  uint32_t mask = 0x03C003C0u, exponent = 0x4C004C00u;
+  __device__ Bits() {
+    asm("" : "+s"(mask));
+    asm("" : "+v"(exponent));
+  }
+};
+
 // Two of a word's nibbles, j and j + 4, as (16 + n).
 template <int j>
-__device__ inline half2v sixteen_plus(uint32_t w) {
+__device__ inline half2v sixteen_plus(const Bits& c, uint32_t w) {
   uint32_t x;
   if constexpr (j == 0) x = w << 6;
   else if constexpr (j == 1) x = w << 2;
   else if constexpr (j == 2) x = w >> 2;
   else x = w >> 6;
-  return __builtin_bit_cast(half2v, (x & 0x03C003C0u) | 0x4C004C00u);
+  return __builtin_bit_cast(half2v, (x & c.mask) | c.exponent);
+}
+
+// The largest of eight (fmaxf would first quiet every operand).
+__device__ inline float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+__device__ inline float max8(const float* e) {
+  return max3(max3(max3(e[0], e[1], e[2]), e[3], e[4]), max3(e[5], e[6], e[7]), e[7]);
 }
 
 // (Taken by value: of an element of a vector, __builtin_bit_cast reads a wrong one.)
@@ -61,18 +83,18 @@ __device__ inline half8v join4(half2v a, half2v b, half2v c, half2v d) {
 }
 
 // Eight channels of one key from a word of its row: channels 0 4 1 5 2 6 3 7.
-__device__ inline half8v key_operand(uint32_t w, half2v s, half2v b) {
-  return join4(__builtin_elementwise_fma(sixteen_plus<0>(w), s, b), __builtin_elementwise_fma(sixteen_plus<1>(w), s, b),
-               __builtin_elementwise_fma(sixteen_plus<2>(w), s, b), __builtin_elementwise_fma(sixteen_plus<3>(w), s, b));
+__device__ inline half8v key_operand(const Bits& c, uint32_t w, half2v s, half2v b) {
+  return join4(__builtin_elementwise_fma(sixteen_plus<0>(c, w), s, b), __builtin_elementwise_fma(sixteen_plus<1>(c, w), s, b),
+               __builtin_elementwise_fma(sixteen_plus<2>(c, w), s, b), __builtin_elementwise_fma(sixteen_plus<3>(c, w), s, b));
 }
 
 // One channel (nibble j of the 16-bit words) of eight tokens; s and b of the tokens in pairs.
 template <int j>
-__device__ inline half8v value_operand(uint4v w, const half2v (&s)[4], const half2v (&b)[4]) {
-  return join4(__builtin_elementwise_fma(sixteen_plus<j>(w.x), s[0], b[0]),
-               __builtin_elementwise_fma(sixteen_plus<j>(w.y), s[1], b[1]),
-               __builtin_elementwise_fma(sixteen_plus<j>(w.z), s[2], b[2]),
-               __builtin_elementwise_fma(sixteen_plus<j>(w.w), s[3], b[3]));
+__device__ inline half8v value_operand(const Bits& c, uint4v w, const half2v (&s)[4], const half2v (&b)[4]) {
+  return join4(__builtin_elementwise_fma(sixteen_plus<j>(c, w.x), s[0], b[0]),
+               __builtin_elementwise_fma(sixteen_plus<j>(c, w.y), s[1], b[1]),
+               __builtin_elementwise_fma(sixteen_plus<j>(c, w.z), s[2], b[2]),
+               __builtin_elementwise_fma(sixteen_plus<j>(c, w.w), s[3], b[3]));
 }
 
 // A query's eight channels in the order of key_operand.
@@ -89,7 +111,11 @@ __device__ inline void split_weight(float p0, float p1, half8v& hi, half8v& lo, 
     const auto c = __builtin_amdgcn_cvt_pkrtz(p0, p1);
     hi[i] = (_Float16)c[0];
     hi[i + 1] = (_Float16)c[1];
-    const auto d = __builtin_amdgcn_cvt_pkrtz(p0 - (float)hi[i], p1 - (float)hi[i + 1]);
+    const uint32_t w = __builtin_bit_cast(uint32_t, c);
+    float r0, r1;  // p0 and p1 less the halves of w, one instruction each
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r0) : "v"(w), "v"(p0));
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r1) : "v"(w), "v"(p1));
+    const auto d = __builtin_amdgcn_cvt_pkrtz(r0, r1);
     lo[i] = (_Float16)d[0];
     lo[i + 1] = (_Float16)d[1];
   } else {
@@ -111,19 +137,29 @@ struct Sequence {
   }
 };
 
-// A value that is the same in all lanes, kept in a scalar register.
+// A value that is the same in all lanes, kept in scalar registers.
 __device__ inline int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ inline int64_t uniform(int64_t x) {
+  const uint64_t lo = (uint32_t)uniform((int)x), hi = (uint32_t)uniform((int)(x >> 32));
+  return (int64_t)(hi << 32 | lo);
+}
+// Element i of an array that no kernel writes meanwhile, by a scalar load: its
+// wait holds up none of the vector loads under way.
+__device__ inline int scalar_load(const int32_t* p, int64_t i) {
+  typedef const int32_t __attribute__((address_space(4))) * constant;
+  return ((constant)(uintptr_t)p)[i];
+}
 
 __device__ inline Sequence sequence(const KvAttendArgs& a, int b, bool tell) {
   Sequence s;
   int start = b, end = b + 1;
   if (a.q_start) {
-    start = uniform(a.q_start[b]);
-    end = uniform(a.q_start[b + 1]);
+    start = scalar_load(a.q_start, b);
+    end = scalar_load(a.q_start, b + 1);
   }
-  const int len = uniform(a.kv_len[b]);
+  const int len = scalar_load(a.kv_len, b);
   const int64_t n = (int64_t)end - start;
-  s.off = !a.causal ? (int64_t)1 << 32 : a.q_off ? (int64_t)uniform(a.q_off[b]) : 0;
+  s.off = !a.causal ? (int64_t)1 << 32 : a.q_off ? (int64_t)scalar_load(a.q_off, b) : 0;
   const bool usable = n >= 0 && n <= a.max_q && start >= 0 && end <= a.tokens;
   if (!usable && tell) kv_report(a.err, kKvRows, b, n, a.max_q);
   s.n = usable ? (int)n : 0;
@@ -136,15 +172,28 @@ __device__ inline Sequence sequence(const KvAttendArgs& a, int b, bool tell) {
   return s;
 }
 
-// Block j of a sequence: its bytes, or nullptr if its page is not in the cache.
-__device__ inline const char* block_at(const KvAttendArgs& a, int b, int h, int j, bool tell) {
-  const int in_page = a.L.page_shift - 5;
-  const int page = uniform(a.table[(int64_t)b * a.table_stride + (j >> in_page)]);
-  if (page < 0 || page >= a.L.num_pages) {
-    if (tell) kv_report(a.err, kKvPage, b, page, a.L.num_pages);
-    return nullptr;
+// Page id of block j of a sequence with `end` blocks to take, one at least (past them: some page id).
+__device__ inline int page_of(const KvAttendArgs& a, int b, int j, int end) {
+  return scalar_load(a.table, (int64_t)b * a.table_stride + ((j < end ? j : end - 1) >> (a.L.page_shift - 5)));
+}
+// Byte of block j on page `page`. `lost` keeps the last page id that is not in
+// the cache, for a report after the loop (a store inside it would make every
+// turn wait for all loads).
+struct Lost {
+  int page = 0;
+  bool any = false;
+};
+__device__ inline int64_t block_on(const KvAttendArgs& a, int page, int h, int j, bool& there, Lost& lost) {
+  there = page >= 0 && page < a.L.num_pages;
+  if (!there) {
+    lost.page = page;
+    lost.any = true;
+    page = 0;
   }
-  return a.pages + kv_block_at(a.L, page, h, j & ((1 << in_page) - 1));
+  return kv_block_at(a.L, page, h, j & ((a.L.page_tokens >> 5) - 1));
+}
+__device__ inline void report_lost(const KvAttendArgs& a, int b, const Lost& lost) {
+  if (lost.any) kv_report(a.err, kKvPage, b, lost.page, a.L.num_pages);
 }
 
 // Writes one row's channels d0 .. d0 + N - 1 of a finished output.
@@ -185,35 +234,35 @@ struct RawValues {
   uint4v s, b;
 };
 
+// `at`: this lane's byte of the first tile's keys; the other places of a block follow from it and the lane.
 template <int D>
-__device__ inline void load_keys(RawKeys<D>& r, const char* blk, int col, int quarter) {
+__device__ inline void load_keys(RawKeys<D>& r, const char* blk, uint32_t at, uint32_t pair) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const char* row = blk + (t * 16 + col) * (D / 2) + quarter * (D / 8);
+    const char* row = blk + t * 8 * D;
     if constexpr (D == 64) {
-      const uint2v w = *reinterpret_cast<const uint2v*>(row);
+      const uint2v w = *reinterpret_cast<const uint2v*>(row + at);
       r.w[t][0] = w.x;
       r.w[t][1] = w.y;
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
-        const uint4v w = *reinterpret_cast<const uint4v*>(row + 16 * i);
+        const uint4v w = *reinterpret_cast<const uint4v*>(row + 16 * i + at);
         r.w[t][4 * i] = w.x;
         r.w[t][4 * i + 1] = w.y;
         r.w[t][4 * i + 2] = w.z;
         r.w[t][4 * i + 3] = w.w;
       }
     }
-    r.pair[t] = *reinterpret_cast<const half2v*>(blk + 32 * D + 4 * (t * 16 + col));
+    r.pair[t] = *reinterpret_cast<const half2v*>(blk + 32 * D + 64 * t + pair);
   }
 }
 template <int D>
-__device__ inline void load_values(RawValues<D>& r, const char* blk, int col, int quarter) {
+__device__ inline void load_values(RawValues<D>& r, const char* blk, uint32_t at, uint32_t pair) {
 #pragma unroll
-  for (int g = 0; g < D / 64; ++g)
-    r.w[g] = *reinterpret_cast<const uint4v*>(blk + 16 * D + ((g * 4 + quarter) * 16 + col) * 16);
-  r.s = *reinterpret_cast<const uint4v*>(blk + 32 * D + 128 + quarter * 16);
-  r.b = *reinterpret_cast<const uint4v*>(blk + 32 * D + 192 + quarter * 16);
+  for (int g = 0; g < D / 64; ++g) r.w[g] = *reinterpret_cast<const uint4v*>(blk + (16 * D + g * 1024) + at);
+  r.s = *reinterpret_cast<const uint4v*>(blk + 32 * D + 128 + pair);
+  r.b = *reinterpret_cast<const uint4v*>(blk + 32 * D + 192 + pair);
 }
 
 template <int D, int NT, bool F32>
@@ -221,9 +270,9 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   constexpr int MT = D / 16;
   __shared__ float4v merge[kWaves / 2 * NT * MT * 64];
   __shared__ float heads[2][kWaves][NT * 16];
-  const int lane = threadIdx.x & 63;
+  const uint32_t lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, quarter = lane >> 4;
+  const uint32_t col = lane & 15, quarter = lane >> 4;
   const int item = blockIdx.x, run = blockIdx.y;
   const int b = item / a.L.Hkv, h = item - b * a.L.Hkv;
   const int G = a.L.Hq / a.L.Hkv;
@@ -236,6 +285,25 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   const int chunk = kv_run_blocks(a.plan.chunk, a.plan.splits, nblk);
   const int j1 = nblk < (run + 1) * chunk ? nblk : (run + 1) * chunk;
   int j = run * chunk + wave;
+
+  // A block without a page is read from the first page and hidden from every row.
+  RawKeys<D> k;
+  RawValues<D> v;
+  bool paged = false;
+  Lost lost;
+  const char* blk = a.pages;
+  const uint32_t key_at = col * (D / 2) + quarter * (D / 8);
+  int page = 0;  // of the block after the next
+  auto find = [&](int at) {
+    blk = a.pages + uniform(block_on(a, page, h, at, paged, lost));
+    page = page_of(a, b, at + kWaves, j1);
+  };
+  if (j < j1) {
+    page = page_of(a, b, j, j1);
+    find(j);
+    load_keys<D>(k, blk, key_at, 4 * col);
+    load_values<D>(v, blk, 16 * lane, 16 * quarter);
+  }
 
   half8v q[NT][D / 32];
   float4v o[NT][MT];  // O^T: row 4 quarter + i of tile m is channel (4 quarter + i) D / 16 + m
@@ -258,59 +326,46 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   }
   const int whole = seq.seen(0) >> 5;  // blocks that every row sees whole
   const float factor = a.scale * kLog2e;
+  const Bits bits;
 
-  // A block without a page is read from the first page and hidden from every row.
-  RawKeys<D> k;
-  RawValues<D> v;
-  bool paged = false;
-  const char* blk = nullptr;
-  auto find = [&](int at) {
-    blk = block_at(a, b, h, at, lane == 0);
-    paged = blk != nullptr;
-    if (!paged) blk = a.pages;
-  };
-  if (j < j1) {
-    find(j);
-    load_keys<D>(k, blk, col, quarter);
-    load_values<D>(v, blk, col, quarter);
-  }
-  for (; j < j1; j += kWaves) {
+  // One block; `more`: another follows, whose loads go out on the way.
+  auto take = [&](auto next) {
+    constexpr bool more = decltype(next)::value;
     const bool hide = j >= whole || !paged;
-    const int end = paged ? seq.len - j * 32 : 0;  // tokens of this block that hold anything
-    const bool more = j + kWaves < j1;
-    if (more) find(j + kWaves);
+    int end = paged ? seq.len - j * 32 : 0;  // tokens of this block that hold anything
+    if constexpr (more) find(j + kWaves);
 
     float4v s[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const half2v sc = {k.pair[t].x, k.pair[t].x}, of = {k.pair[t].y, k.pair[t].y};
+    for (int i = 0; i < D / 32; ++i) {
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const half8v kk = key_operand(k.w[t][i], sc, of);
+      for (int t = 0; t < 2; ++t) {
+        const half8v kk = key_operand(bits, k.w[t][i], half2v{k.pair[t].x, k.pair[t].x}, half2v{k.pair[t].y, k.pair[t].y});
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, q[n][i], s[n][t], 0, 0, 0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
-    if (more) load_keys<D>(k, blk, col, quarter);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (more) load_keys<D>(k, blk, key_at, 4 * col);
 
     half8v hi[NT], lo[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float e[8];
       float top;
-      const int left = (end > 0 ? seen[n] - j * 32 : 0) - quarter * 4;
+      int left = (end > 0 ? seen[n] - j * 32 : 0) - (int)quarter * 4;
       auto exponents = [&](float bs) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] = __builtin_fmaf(s[n][i >> 2][i & 3], factor, -bs);
         if (hide) {
+          asm volatile("" : "+v"(left));  // keeps the comparisons in this branch
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if ((i >> 2) * 16 + (i & 3) >= left) e[i] = -__builtin_inff();
         }
-        top = fmaxf(fmaxf(fmaxf(e[0], e[1]), fmaxf(e[2], e[3])), fmaxf(fmaxf(e[4], e[5]), fmaxf(e[6], e[7])));
+        top = max8(e);
       };
       exponents(base[n]);
       if (__any(top > kTop)) {  // a new maximum, for some column
@@ -341,9 +396,10 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
       vb[i] = halves(v.b[i]);
     }
     if (hide) {  // what lies behind the sequence's end may be anything
+      asm volatile("" : "+s"(end));
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if ((e >> 2) * 16 + quarter * 4 + (e & 3) >= end) vs[e >> 1][e & 1] = vb[e >> 1][e & 1] = (_Float16)0.f;
+        if ((e >> 2) * 16 + (int)quarter * 4 + (e & 3) >= end) vs[e >> 1][e & 1] = vb[e >> 1][e & 1] = (_Float16)0.f;
     }
 #pragma unroll
     for (int g = 0; g < D / 64; ++g) {
@@ -354,15 +410,19 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
           if constexpr (F32) o[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, lo[n], o[n][m], 0, 0, 0);
         }
       };
-      multiply(value_operand<0>(v.w[g], vs, vb), 4 * g);
-      multiply(value_operand<1>(v.w[g], vs, vb), 4 * g + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(value_operand<2>(v.w[g], vs, vb), 4 * g + 2);
-      multiply(value_operand<3>(v.w[g], vs, vb), 4 * g + 3);
+      multiply(value_operand<0>(bits, v.w[g], vs, vb), 4 * g);
+      multiply(value_operand<1>(bits, v.w[g], vs, vb), 4 * g + 1);
+      multiply(value_operand<2>(bits, v.w[g], vs, vb), 4 * g + 2);
+      multiply(value_operand<3>(bits, v.w[g], vs, vb), 4 * g + 3);
     }
     __builtin_amdgcn_sched_barrier(0);
-    if (more) load_values<D>(v, blk, col, quarter);
-  }
+    if constexpr (more) load_values<D>(v, blk, 16 * lane, 16 * quarter);
+  };
+  // The last block apart: were the loads conditional inside one loop, the
+  // compiler would have to wait for all of them in every turn.
+  for (; j + kWaves < j1; j += kWaves) take(std::true_type{});
+  if (j < j1) take(std::false_type{});
+  if (lane == 0) report_lost(a, b, lost);
 
   // Join the waves: a common base, then sums by halves, in a fixed order.
 #pragma unroll
@@ -492,6 +552,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
   const int whole = w0 < rows ? seq.seen(w0 / G) >> 5 : 0;
   const int none = w0 < rows ? (seq.seen(w1 / G) + 31) >> 5 : 0;
   const float factor = a.scale * kLog2e;
+  const Bits bits;
 
   float16v o[MT];
 #pragma unroll
@@ -506,12 +567,16 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
   const int vq = (piece >> 4) & 3, vc = piece & 15, vg = piece >> 6;
   uint4v kr, vr, vsr, vbr;
   half2v kpr;
-  int have = 0;  // 1: this thread's block is there
-  auto fetch = [&](int jt) {
+  bool have = false;  // this thread's block is there
+  Lost lost;
+  int next_page = j0 < j1 ? page_of(a, b, j0 + pb, j1) : 0;
+  auto fetch = [&](int jt) {  // called for every tile in turn
     const int j = jt + pb;
-    const char* blk = j < j1 ? block_at(a, b, h, j, piece == 0) : nullptr;
-    have = blk != nullptr;
-    if (!blk) return;
+    const int page = next_page;
+    next_page = page_of(a, b, j + KB, j1);
+    have = false;
+    if (j >= j1) return;
+    const char* blk = a.pages + uniform(block_on(a, page, h, j, have, lost));
     kr = *reinterpret_cast<const uint4v*>(blk + piece * 16);
     kpr = *reinterpret_cast<const half2v*>(blk + 32 * D + 4 * ktok);
     vr = *reinterpret_cast<const uint4v*>(blk + 16 * D + piece * 16);
@@ -532,7 +597,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int w = krun * 4 + i;  // word of the row: step w / 2, half w & 1
-      kl[buf][(pb * KS + (w >> 1)) * 64 + (((w & 1) * 32 + ktok) ^ (krun * (8 / RN)))] = key_operand(kr[i], s2, b2);
+      kl[buf][(pb * KS + (w >> 1)) * 64 + (((w & 1) * 32 + ktok) ^ (krun * (8 / RN)))] = key_operand(bits, kr[i], s2, b2);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -544,8 +609,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
         if (!have || j * 32 + (e >> 2) * 16 + vq * 4 + (e & 3) >= seq.len) vs[i][x] = vb[i][x] = (_Float16)0.f;
       }
     }
-    const half8v v[4] = {value_operand<0>(vr, vs, vb), value_operand<1>(vr, vs, vb), value_operand<2>(vr, vs, vb),
-                         value_operand<3>(vr, vs, vb)};
+    const half8v v[4] = {value_operand<0>(bits, vr, vs, vb), value_operand<1>(bits, vr, vs, vb), value_operand<2>(bits, vr, vs, vb),
+                         value_operand<3>(bits, vr, vs, vb)};
 #pragma unroll
     for (int x = 0; x < 4; ++x)
       vl[buf][((pb * 2 + (vq >> 1)) * MT + 2 * vg + (x >> 1)) * 64 + (vq & 1) * 32 + (x & 1) * 16 + vc] = v[x];
@@ -563,18 +628,18 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
     }
     float e[16];
     float top;
-    const int left = seen - (j * 32 + hh * 4);
+    int left = seen - (j * 32 + hh * 4);
     auto exponents = [&](float bs) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) e[i] = __builtin_fmaf(s[i], factor, -bs);
       if (mask) {
+        asm volatile("" : "+v"(left));  // keeps the comparisons in this branch
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (8 * (i >> 2) + (i & 3) >= left) e[i] = -__builtin_inff();
       }
-      top = e[0];
-#pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(top, e[i]);
+      top = max8(e);
+      top = max3(top, max8(e + 8), top);
     };
     exponents(base);
     if (__any(top > kTop)) {
@@ -627,6 +692,7 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
     }
   }
 
+  if (lane == 0) report_lost(a, b, lost);
   sum += __shfl_xor(sum, 32);
   if (!live) return;
   // O^T: register i of tile m is row R = 8 (i / 4) + 4 hh + i % 4, channel (R % 16) D / 16 + 2 m + R / 16.
