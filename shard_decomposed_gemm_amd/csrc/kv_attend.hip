@@ -221,7 +221,7 @@ __device__ inline void store_out(void* out, int64_t at, const float (&v)[N]) {
 // end. A wave holds all rows of the item as the 16 columns of its products (NT
 // times), and a block of 32 keys as two tiles of 16. The next block's keys are
 // loaded when this block's are used up, its values likewise.
-constexpr int kWaves = 8;
+constexpr int kWaves = kKvWaves;
 
 template <int D>
 struct RawKeys {  // a block's keys as a lane reads them
@@ -268,14 +268,17 @@ __device__ inline void load_values(RawValues<D>& r, const char* blk, uint32_t at
 template <int D, int NT, bool F32>
 __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void kv_attend_few_kernel(KvAttendArgs a) {
   constexpr int MT = D / 16;
-  __shared__ float4v merge[kWaves / 2 * NT * MT * 64];
-  __shared__ float heads[2][kWaves][NT * 16];
+  constexpr int R = 16 * NT, LD = D + 4;  // rows of an item; a row's floats in LDS, padded off the same banks
+  __shared__ __attribute__((aligned(16))) float part[kWaves][R][LD];
+  __shared__ float heads[kWaves][R][2];
   const uint32_t lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t col = lane & 15, quarter = lane >> 4;
   const int item = blockIdx.x, run = blockIdx.y;
   const int b = item / a.L.Hkv, h = item - b * a.L.Hkv;
   const int G = a.L.Hq / a.L.Hkv;
+  // The first page id goes out with the lengths: it is this one unless runs are longer than planned.
+  int page = page_of(a, b, run * a.plan.chunk + wave, a.table_width << (a.L.page_shift - 5));
   const Sequence seq = sequence(a, b, run == 0 && h == 0 && threadIdx.x == 0);
   const int rows = seq.n * G;
   if (rows == 0) return;
@@ -293,13 +296,12 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   Lost lost;
   const char* blk = a.pages;
   const uint32_t key_at = col * (D / 2) + quarter * (D / 8);
-  int page = 0;  // of the block after the next
   auto find = [&](int at) {
     blk = a.pages + uniform(block_on(a, page, h, at, paged, lost));
-    page = page_of(a, b, at + kWaves, j1);
+    page = page_of(a, b, at + kWaves, j1);  // of the block after this one
   };
   if (j < j1) {
-    page = page_of(a, b, j, j1);
+    if (chunk != a.plan.chunk) page = page_of(a, b, j, j1);
     find(j);
     load_keys<D>(k, blk, key_at, 4 * col);
     load_values<D>(v, blk, 16 * lane, 16 * quarter);
@@ -424,73 +426,50 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   if (j < j1) take(std::false_type{});
   if (lane == 0) report_lost(a, b, lost);
 
-  // Join the waves: a common base, then sums by halves, in a fixed order.
+  // Join the waves: all leave their sums in LDS, then each thread adds up four
+  // channels of a row over the waves, in order.
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     sum[n] += __shfl_xor(sum[n], 16);
     sum[n] += __shfl_xor(sum[n], 32);
-    if (quarter == 0) {
-      heads[0][wave][n * 16 + col] = base[n];
-      heads[1][wave][n * 16 + col] = sum[n];
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float top = kNoMax, all = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, heads[0][w][n * 16 + col]);
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) all += heads[1][w][n * 16 + col] * exp2_hw(heads[0][w][n * 16 + col] - top);
-    const float f = exp2_hw(base[n] - top);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) o[n][m] *= f;
-    base[n] = top;
-    sum[n] = all;
-  }
-#pragma unroll
-  for (int half = kWaves / 2; half > 0; half >>= 1) {
-    if (wave >= half && wave < 2 * half) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) merge[((wave - half) * NT * MT + n * MT + m) * 64 + lane] = o[n][m];
-    }
-    __syncthreads();
-    if (wave < half) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) o[n][m] += merge[(wave * NT * MT + n * MT + m) * 64 + lane];
-    }
-    __syncthreads();
-  }
-  if (wave != 0) return;
-
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
     const int r = n * 16 + col;
     if (r >= rows) continue;
-    const int i = r / G;
-    const int64_t at = (seq.row0 + i) * a.L.Hq + h * G + r - i * G;
-    const bool last = runs == 1;
-    float* slot = last ? nullptr : a.ws + ((int64_t)item * a.plan.splits + run) * a.plan.slot_floats;
-    const float inv = !last ? 1.f : sum[n] != 0.f ? 1.f / sum[n] : 0.f;
-#pragma unroll
-    for (int y4 = 0; y4 < 4; ++y4) {
-      float w[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) w[m] = o[n][m][y4] * inv;
-      const int d0 = (quarter * 4 + y4) * MT;
-      if (last) store_out<F32>(a.out, at * D + d0, w);
-      else store_out<true>(slot, (int64_t)r * D + d0, w);
-    }
     if (quarter == 0) {
-      if (last) {
-        if (a.lse) a.lse[at] = sum[n] != 0.f ? (base[n] + log2f(sum[n])) * kLn2 : kLowest;
-      } else {
-        slot[a.plan.rows * D + 2 * r] = base[n];
-        slot[a.plan.rows * D + 2 * r + 1] = sum[n];
+      heads[wave][r][0] = base[n];
+      heads[wave][r][1] = sum[n];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; m += 4)
+        *reinterpret_cast<float4v*>(&part[wave][r][(quarter * 4 + i) * MT + m]) =
+            float4v{o[n][m][i], o[n][m + 1][i], o[n][m + 2][i], o[n][m + 3][i]};
+  }
+  __syncthreads();
+  float* slot = a.ws + ((int64_t)item * a.plan.splits + run) * a.plan.slot_floats;
+  for (int x = threadIdx.x; x < rows * (D / 4); x += kWaves * 64) {
+    const int r = x / (D / 4), d = 4 * (x % (D / 4));
+    float top = kNoMax, all = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, heads[w][r][0]);
+    float4v v4 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = exp2_hw(heads[w][r][0] - top);
+      all += heads[w][r][1] * f;
+      v4 += *reinterpret_cast<const float4v*>(&part[w][r][d]) * f;
+    }
+    if (runs == 1) {
+      const int i = r / G;
+      const int64_t row = (seq.row0 + i) * a.L.Hq + h * G + r - i * G;
+      const float inv = all != 0.f ? 1.f / all : 0.f;
+      store_out<F32, 4>(a.out, row * D + d, {v4.x * inv, v4.y * inv, v4.z * inv, v4.w * inv});
+      if (a.lse && d == 0) a.lse[row] = all != 0.f ? (top + log2f(all)) * kLn2 : kLowest;
+    } else {
+      *reinterpret_cast<float4v*>(slot + r * D + d) = v4;
+      if (d == 0) {
+        slot[a.plan.rows * D + 2 * r] = top;
+        slot[a.plan.rows * D + 2 * r + 1] = all;
       }
     }
   }

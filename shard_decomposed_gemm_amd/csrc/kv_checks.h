@@ -115,6 +115,8 @@ inline int kv_check_attend(const KvLayout& L, const void* pages, const kvc_atten
   if (!isfinite(p->scale)) return kv_refuse(why, AGEMM_EINVAL, "scale must be finite");
   if (p->table_width < 1 || p->table_stride < 0 || (p->table_stride > 0 && p->table_stride < p->table_width))
     return kv_refuse(why, AGEMM_EINVAL, "table_width must be positive and table_stride 0 or at least the width");
+  if ((int64_t)p->batch * p->table_width > (int64_t{1} << 30) / (L.page_tokens / 32))
+    return kv_refuse(why, AGEMM_ESHAPE, "the page table names more than 2^35 tokens");
   if (!p->q_start && (p->max_q != 1 || p->batch > p->tokens))
     return kv_refuse(why, AGEMM_EINVAL, "without q_start max_q is 1 and every sequence has its row");
   if (!kv_stride_ok(p->q_token_stride) || !kv_stride_ok(p->q_head_stride))

@@ -48,6 +48,7 @@ struct KvPlan {
 };
 
 constexpr int kKvMaxSplits = 256;
+constexpr int kKvWaves = 8;  // of a workgroup for few rows: each takes every eighth block of a run
 
 // Blocks that a run of an item with nblk blocks has, and the runs.
 KV_HD inline int kv_run_blocks(int chunk, int splits, int nblk) {
@@ -68,14 +69,28 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
   p.tiles = (int32_t)(p.many ? (rows + p.rows - 1) / p.rows : 1);
   p.items = batch * L.Hkv * p.tiles;
   const int64_t nblk = (max_kv + 31) / 32;
-  // Runs of equal length keep ragged batches even: several for each place on
-  // the chip there, one where a single sequence makes them equal anyway.
-  const int64_t places = (int64_t)num_cus * (p.many ? 4 : batch > 1 ? 16 : 2);
-  int64_t chunk = (p.items * nblk + places - 1) / places;
-  if (chunk < 32) chunk = 32;
+  int64_t chunk;
+  if (p.many) {
+    const int64_t places = (int64_t)num_cus * 4;
+    chunk = (p.items * nblk + places - 1) / places;
+    if (chunk < 32) chunk = 32;
+  } else if (nblk <= 4 * kKvWaves) {
+    chunk = nblk;  // four blocks a wave are done before a join would be
+  } else {
+    // As many runs as run at once, but none so long that the last of them
+    // keep the chip waiting: the more items, the longer they may be.
+    const int64_t places = (int64_t)num_cus * (L.D == 256 || p.rows == 32 ? 1 : 2);
+    chunk = (p.items * nblk + places - 1) / places;
+    if (chunk < kKvWaves) chunk = kKvWaves;
+    const int64_t most = 8 * kKvWaves * ((p.items + places - 1) / places);
+    if (chunk > most) chunk = most;
+  }
   int64_t splits = (nblk + chunk - 1) / chunk;
   if (splits < 1) splits = 1;
-  if (splits > kKvMaxSplits) splits = kKvMaxSplits;
+  if (splits > kKvMaxSplits) {
+    splits = kKvMaxSplits;
+    chunk = (nblk + splits - 1) / splits;
+  }
   p.chunk = (int32_t)(chunk < (int64_t{1} << 26) ? chunk : int64_t{1} << 26);
   p.splits = (int32_t)splits;
   p.slot_floats = (int64_t)p.rows * (L.D + 2);
