@@ -234,35 +234,47 @@ struct RawValues {
   uint4v s, b;
 };
 
+// A block as a raw buffer: loads then take a 32-bit offset from the lane and
+// the rest from scalars, and none can leave the block. They go past L2's
+// retention (nontemporal): a cached byte is read once a call.
+constexpr int kRawBuffer = 0x00020000;  // word 3: raw 32-bit buffer, gfx9 family
+constexpr int kNontemporal = 2;
+template <int D>
+__device__ inline __amdgpu_buffer_rsrc_t block_buffer(const char* blk) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(blk), 0, 32 * (D + 8), kRawBuffer);
+}
+
 // `at`: this lane's byte of the first tile's keys; the other places of a block follow from it and the lane.
 template <int D>
-__device__ inline void load_keys(RawKeys<D>& r, const char* blk, uint32_t at, uint32_t pair) {
+__device__ inline void load_keys(RawKeys<D>& r, __amdgpu_buffer_rsrc_t blk, uint32_t at, uint32_t pair) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const char* row = blk + t * 8 * D;
     if constexpr (D == 64) {
-      const uint2v w = *reinterpret_cast<const uint2v*>(row + at);
+      const uint2v w = __builtin_bit_cast(uint2v, __builtin_amdgcn_raw_buffer_load_b64(blk, at + t * 8 * D, 0, kNontemporal));
       r.w[t][0] = w.x;
       r.w[t][1] = w.y;
     } else {
 #pragma unroll
       for (int i = 0; i < D / 128; ++i) {
-        const uint4v w = *reinterpret_cast<const uint4v*>(row + 16 * i + at);
+        const uint4v w = __builtin_bit_cast(
+            uint4v, __builtin_amdgcn_raw_buffer_load_b128(blk, at + (t * 8 * D + 16 * i), 0, kNontemporal));
         r.w[t][4 * i] = w.x;
         r.w[t][4 * i + 1] = w.y;
         r.w[t][4 * i + 2] = w.z;
         r.w[t][4 * i + 3] = w.w;
       }
     }
-    r.pair[t] = *reinterpret_cast<const half2v*>(blk + 32 * D + 64 * t + pair);
+    const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(blk, pair + 64 * t, 32 * D, kNontemporal);
+    r.pair[t] = halves(w);
   }
 }
 template <int D>
-__device__ inline void load_values(RawValues<D>& r, const char* blk, uint32_t at, uint32_t pair) {
+__device__ inline void load_values(RawValues<D>& r, __amdgpu_buffer_rsrc_t blk, uint32_t at, uint32_t pair) {
 #pragma unroll
-  for (int g = 0; g < D / 64; ++g) r.w[g] = *reinterpret_cast<const uint4v*>(blk + (16 * D + g * 1024) + at);
-  r.s = *reinterpret_cast<const uint4v*>(blk + 32 * D + 128 + pair);
-  r.b = *reinterpret_cast<const uint4v*>(blk + 32 * D + 192 + pair);
+  for (int g = 0; g < D / 64; ++g)
+    r.w[g] = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(blk, at + g * 1024, 16 * D, kNontemporal));
+  r.s = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(blk, pair + 128, 32 * D, kNontemporal));
+  r.b = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(blk, pair + 192, 32 * D, kNontemporal));
 }
 
 template <int D, int NT, bool F32>
@@ -303,8 +315,8 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   if (j < j1) {
     if (chunk != a.plan.chunk) page = page_of(a, b, j, j1);
     find(j);
-    load_keys<D>(k, blk, key_at, 4 * col);
-    load_values<D>(v, blk, 16 * lane, 16 * quarter);
+    load_keys<D>(k, block_buffer<D>(blk), key_at, 4 * col);
+    load_values<D>(v, block_buffer<D>(blk), 16 * lane, 16 * quarter);
   }
 
   half8v q[NT][D / 32];
@@ -314,13 +326,14 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   int seen[NT];       // keys that the column's row sees
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = n * 16 + col;
-    const bool live = r < rows;
+    // Columns past the last row repeat row 0: loads that some lanes leave out
+    // would make the loop's first waits those for everything.
+    const int r = n * 16 + (int)col < rows ? n * 16 + col : 0;
     const int i = r / G;
     const _Float16* src = a.q + (seq.row0 + i) * a.q_ts + (int64_t)(h * G + r - i * G) * a.q_hs + quarter * (D / 4);
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) q[n][x] = live ? query_operand(src + 8 * x) : half8v{};
-    seen[n] = live ? seq.seen(i) : seq.len;
+    for (int x = 0; x < D / 32; ++x) q[n][x] = query_operand(src + 8 * x);
+    seen[n] = seq.seen(i);
     base[n] = kNoMax;
     sum[n] = 0.f;
 #pragma unroll
@@ -350,7 +363,7 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (more) load_keys<D>(k, blk, key_at, 4 * col);
+    if constexpr (more) load_keys<D>(k, block_buffer<D>(blk), key_at, 4 * col);
 
     half8v hi[NT], lo[NT];
 #pragma unroll
@@ -418,7 +431,7 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
       multiply(value_operand<3>(bits, v.w[g], vs, vb), 4 * g + 3);
     }
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (more) load_values<D>(v, blk, 16 * lane, 16 * quarter);
+    if constexpr (more) load_values<D>(v, block_buffer<D>(blk), 16 * lane, 16 * quarter);
   };
   // The last block apart: were the loads conditional inside one loop, the
   // compiler would have to wait for all of them in every turn.
