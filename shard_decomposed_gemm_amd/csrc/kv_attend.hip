@@ -286,7 +286,8 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   const uint32_t lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t col = lane & 15, quarter = lane >> 4;
-  const int item = blockIdx.x, run = blockIdx.y;
+  // Late runs first: of a ragged batch they are the whole ones, and short sequences fill up the end.
+  const int item = blockIdx.x, run = a.plan.splits - 1 - blockIdx.y;
   const int b = item / a.L.Hkv, h = item - b * a.L.Hkv;
   const int G = a.L.Hq / a.L.Hkv;
   // The first page id goes out with the lengths: it is this one unless runs are longer than planned.
@@ -716,16 +717,23 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
 
 // ---------------------------------------------------------------- join
 
-// Joins the partials of the runs of an item, one workgroup a row: its four
-// waves take every fourth run, in order, and their sums meet in LDS.
+// Joins the partials of an item's runs. A workgroup takes `join_rows` of its
+// rows: the weights 2^(exponent - largest) of the runs go to LDS, then each
+// thread adds up four channels of a row over every S-th run, in order, and the
+// S sums of a row meet in LDS. One row a workgroup (S = 2048 / D) where the call has
+// few, so that many runs do not queue; a full workgroup of rows otherwise.
+constexpr int kJoinThreads = 512;
+
 template <int D, bool F32>
-__global__ __launch_bounds__(256) void kv_attend_join_kernel(KvAttendArgs a) {
-  constexpr int E = D / 64;
-  __shared__ float acc[3][D], sums[3];
-  const int rpi = a.plan.rows;
-  const int item = blockIdx.x / a.plan.join_rows, lr = blockIdx.x - item * a.plan.join_rows;
+__global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendArgs a) {
+  constexpr int C = D / 4;  // threads of a row
+  __shared__ float weight[kJoinThreads / C][kKvMaxSplits];
+  __shared__ float4v meet[kJoinThreads];
+  __shared__ float sums[kJoinThreads / C], tops[kJoinThreads / C];
+  const int rpi = a.plan.rows, RW = a.plan.join_rows;
+  const int item = blockIdx.x, l0 = blockIdx.y * RW;
   const int G = a.L.Hq / a.L.Hkv;
-  int b, h, r0;
+  int b, h, r0 = 0;
   if (a.plan.many) {
     h = item % a.L.Hkv;
     const int rest = item / a.L.Hkv;
@@ -734,56 +742,65 @@ __global__ __launch_bounds__(256) void kv_attend_join_kernel(KvAttendArgs a) {
   } else {
     b = item / a.L.Hkv;
     h = item - b * a.L.Hkv;
-    r0 = 0;
   }
   const Sequence seq = sequence(a, b, false);
-  const int rows = seq.n * G, r = r0 + lr;
-  if (r >= rows) return;
+  const int rows = seq.n * G;
+  if (r0 + l0 >= rows) return;
   const int r_last = r0 + rpi - 1 < rows ? r0 + rpi - 1 : rows - 1;
-  const int nblk = (seq.seen(r_last / G) + 31) >> 5;
-  const int runs = kv_runs(a.plan.chunk, a.plan.splits, nblk);
+  const int runs = kv_runs(a.plan.chunk, a.plan.splits, (seq.seen(r_last / G) + 31) >> 5);
   if (runs == 1) return;  // written by its only run
+  const int R = rows - r0 - l0 < RW ? rows - r0 - l0 : RW;
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const float* slot = a.ws + (int64_t)item * a.plan.splits * a.plan.slot_floats;
-  float top = kNoMax;
-  for (int s = lane; s < runs; s += 64) top = fmaxf(top, slot[s * a.plan.slot_floats + rpi * D + 2 * lr]);
+  const float* part = a.ws + (int64_t)item * a.plan.splits * a.plan.slot_floats;
+  for (int r = uniform((int)threadIdx.x >> 6); r < R; r += kJoinThreads / 64) {
+    const float* head = part + rpi * D + 2 * (l0 + r);
+    float e[kKvMaxSplits / 64], n[kKvMaxSplits / 64], top = kNoMax, sum = 0.f;
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
-  float v[E], sum = 0.f;
+    for (int i = 0; i < kKvMaxSplits / 64; ++i) {
+      const int s = 64 * i + lane;
+      e[i] = s < runs ? head[s * a.plan.slot_floats] : kNoMax;
+      n[i] = s < runs ? head[s * a.plan.slot_floats + 1] : 0.f;
+      top = fmaxf(top, e[i]);
+    }
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = 0.f;
-#pragma unroll 4
-  for (int s = wave; s < runs; s += 4) {
-    const float* p = slot + s * a.plan.slot_floats;
-    const float f = exp2_hw(p[rpi * D + 2 * lr] - top);
-    sum += f * p[rpi * D + 2 * lr + 1];
+    for (int m = 1; m < 64; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] += f * p[lr * D + lane * E + e];
-  }
-  if (wave > 0) {
+    for (int i = 0; i < kKvMaxSplits / 64; ++i) {
+      const float f = exp2_hw(e[i] - top);
+      sum += f * n[i];
+      if (64 * i + lane < runs) weight[r][64 * i + lane] = f;
+    }
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[wave - 1][lane * E + e] = v[e];
-    if (lane == 0) sums[wave - 1] = sum;
+    for (int m = 1; m < 64; m <<= 1) sum += __shfl_xor(sum, m);
+    if (lane == 0) {
+      sums[r] = sum;
+      tops[r] = top;
+    }
   }
   __syncthreads();
-  if (wave > 0) return;
-#pragma unroll
-  for (int w = 0; w < 3; ++w) {
-    sum += sums[w];
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] += acc[w][lane * E + e];
+
+  const int S = kJoinThreads / (RW * C);
+  const int d = 4 * ((int)threadIdx.x % C), r = (int)threadIdx.x / C % RW, slice = (int)threadIdx.x / (RW * C);
+  float4v v = {0.f, 0.f, 0.f, 0.f};
+  if (r < R) {
+    const float* p = part + (int64_t)(l0 + r) * D + d;
+#pragma unroll 8
+    for (int s = slice; s < runs; s += S)
+      v += *reinterpret_cast<const float4v*>(p + s * a.plan.slot_floats) * weight[r][s];
   }
-  const int i = r / G;
-  const int64_t o = (seq.row0 + i) * a.L.Hq + h * G + r - i * G;
-  const float inv = sum != 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if constexpr (F32) static_cast<float*>(a.out)[o * D + lane * E + e] = v[e] * inv;
-    else static_cast<_Float16*>(a.out)[o * D + lane * E + e] = (_Float16)(v[e] * inv);
+  if (S > 1) {
+    meet[threadIdx.x] = v;
+    __syncthreads();
+    if (slice > 0) return;
+    for (int s = 1; s < S; ++s) v += meet[s * RW * C + threadIdx.x];
   }
-  if (a.lse && lane == 0) a.lse[o] = sum != 0.f ? (top + log2f(sum)) * kLn2 : kLowest;
+  if (r >= R) return;
+  const int rr = r0 + l0 + r, i = rr / G;
+  const int64_t row = (seq.row0 + i) * a.L.Hq + h * G + rr - i * G;
+  const float inv = sums[r] != 0.f ? 1.f / sums[r] : 0.f;
+  store_out<F32, 4>(a.out, row * D + d, {v.x * inv, v.y * inv, v.z * inv, v.w * inv});
+  if (a.lse && d == 0) a.lse[row] = sums[r] != 0.f ? (tops[r] + log2f(sums[r])) * kLn2 : kLowest;
 }
 
 template <int D, bool F32>
@@ -794,7 +811,8 @@ hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
   else if constexpr (D <= 128)
     hipLaunchKernelGGL((kv_attend_few_kernel<D, 2, F32>), grid, dim3(kWaves * 64), 0, s, a);
   if (a.plan.splits > 1)
-    hipLaunchKernelGGL((kv_attend_join_kernel<D, F32>), dim3((unsigned)(a.plan.items * a.plan.join_rows)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((kv_attend_join_kernel<D, F32>), dim3((unsigned)a.plan.items, (unsigned)a.plan.join_groups),
+                       dim3(kJoinThreads), 0, s, a);
   return hipGetLastError();
 }
 

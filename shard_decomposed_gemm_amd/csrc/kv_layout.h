@@ -38,7 +38,7 @@ KV_HD inline int kv_value_place(int t) { return ((t >> 4) << 2) | (t & 3); }
 struct KvPlan {
   int32_t many;    // 0: the kernel for few rows, 1: for many
   int32_t rows;    // rows of one item
-  int32_t join_rows;  // of them, those that a sequence of max_q queries can have
+  int32_t join_rows, join_groups;  // the join: rows of a workgroup (a power of two), workgroups of an item
   int32_t tiles;   // items of one sequence and kv head
   int32_t splits;
   int32_t chunk;   // blocks of a run
@@ -65,7 +65,6 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
   const int64_t rows = max_q * (L.Hq / L.Hkv);
   p.many = rows > (L.D == 256 ? 16 : 32);
   p.rows = p.many ? 128 : rows > 16 ? 32 : 16;
-  p.join_rows = (int32_t)(rows < p.rows ? rows : p.rows);
   p.tiles = (int32_t)(p.many ? (rows + p.rows - 1) / p.rows : 1);
   p.items = batch * L.Hkv * p.tiles;
   const int64_t nblk = (max_kv + 31) / 32;
@@ -82,7 +81,7 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
     const int64_t places = (int64_t)num_cus * (L.D == 256 || p.rows == 32 ? 1 : 2);
     chunk = (p.items * nblk + places - 1) / places;
     if (chunk < kKvWaves) chunk = kKvWaves;
-    const int64_t most = 8 * kKvWaves * ((p.items + places - 1) / places);
+    const int64_t most = 16 * kKvWaves * ((p.items + places - 1) / places);
     if (chunk > most) chunk = most;
   }
   int64_t splits = (nblk + chunk - 1) / chunk;
@@ -93,6 +92,9 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
   }
   p.chunk = (int32_t)(chunk < (int64_t{1} << 26) ? chunk : int64_t{1} << 26);
   p.splits = (int32_t)splits;
+  const int64_t live = rows < p.rows ? rows : p.rows;  // rows of an item that can exist
+  p.join_rows = p.items * live <= 2 * num_cus ? 1 : 2048 / L.D;
+  p.join_groups = (int32_t)((live + p.join_rows - 1) / p.join_rows);
   p.slot_floats = (int64_t)p.rows * (L.D + 2);
   p.ws_bytes = p.splits > 1 ? p.items * p.splits * p.slot_floats * 4 : 0;
   return p;
