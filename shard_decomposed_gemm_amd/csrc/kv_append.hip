@@ -9,10 +9,13 @@
 // query rows are normed, rotated and written as binary16; key rows are
 // normed, rotated and quantised; value rows are quantised. The rotation's
 // partner of channel i, i +- rope_dims / 2, is in the lane rope_dims / 2
-// channels away.
+// channels away. Sums and extremes over a row are four steps within a row of
+// 16 lanes (DPP rotations).
 //
 // Bound by HBM: 2 bytes in and out a query channel, 2 in and 1/2 out a key or
 // value channel, some 10 operations each.
+#include <type_traits>
+
 #include "kv_internal.h"
 
 namespace agemm {
@@ -26,51 +29,73 @@ struct alignas(E * 2) Halves {
   _Float16 x[E];
 };
 
+// x of the lane n places on in its row of 16.
+template <int n>
+__device__ inline float rotated(float x) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + n, 0xf, 0xf, true));
+}
+template <int n>
+__device__ inline double rotated(double x) {
+  const int64_t v = __builtin_bit_cast(int64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)v, 0x120 + n, 0xf, 0xf, true);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), 0x120 + n, 0xf, 0xf, true);
+  return __builtin_bit_cast(double, (int64_t)hi << 32 | lo);
+}
 template <class T>
 __device__ inline T sum16(T v) {
-#pragma unroll
-  for (int m = 1; m < 16; m <<= 1) v += __shfl_xor(v, m, 16);
-  return v;
+  v += rotated<8>(v);
+  v += rotated<4>(v);
+  v += rotated<2>(v);
+  return v + rotated<1>(v);
 }
-__device__ inline double min16(double v) {
-#pragma unroll
-  for (int m = 1; m < 16; m <<= 1) v = fmin(v, __shfl_xor(v, m, 16));
-  return v;
+__device__ inline float least(float a, float b) { return a < b ? a : b; }
+__device__ inline double least(double a, double b) { return a < b ? a : b; }
+template <class T>
+__device__ inline T min16(T v) {
+  v = least(v, rotated<8>(v));
+  v = least(v, rotated<4>(v));
+  v = least(v, rotated<2>(v));
+  return least(v, rotated<1>(v));
 }
 
 // x (this lane's channels of a head row) normed and rotated in place. `partner`
 // is the row's lane that holds the rotation's other channels.
-template <class T, int E>
-__device__ inline void norm_rope(T (&x)[E], const _Float16* w, float eps, int d0, int R, bool interleaved, int partner,
-                                 const float (&cs)[E], const float (&sn)[E]) {
+enum Rope { kNone, kWhole, kOther };  // no rotation, halves of whole rows, anything else
+
+template <class T, int E, int ROPE>
+__device__ inline void norm_rope(T (&x)[E], bool norm, const Halves<E>& w, float eps, int d0, int R, bool interleaved,
+                                 int partner, const float (&cs)[E], const float (&sn)[E]) {
   constexpr int D = 16 * E;
-  if (w) {
+  if (norm) {
     T ss = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) ss += x[e] * x[e];
     const T inv = T(1) / sqrt(sum16(ss) * T(1.0 / D) + T(eps));
-    const Halves<E> wv = *reinterpret_cast<const Halves<E>*>(w + d0);
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = x[e] * inv * T((float)wv.x[e]);
+    for (int e = 0; e < E; ++e) x[e] = x[e] * inv * T((float)w.x[e]);
   }
-  if (!R) return;
-  if (interleaved) {
-    if (d0 < R) {
+  if constexpr (ROPE == kWhole) {  // the partner is the lane eight places on
+    const T sign = d0 < D / 2 ? T(-1) : T(1);
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const T u = x[e], y = x[e + 1];
-        x[e] = u * T(cs[e]) - y * T(sn[e]);
-        x[e + 1] = y * T(cs[e]) + u * T(sn[e]);
+    for (int e = 0; e < E; ++e) x[e] = x[e] * T(cs[e]) + sign * rotated<8>(x[e]) * T(sn[e]);
+  } else if constexpr (ROPE == kOther) {
+    if (interleaved) {
+      if (d0 < R) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const T u = x[e], y = x[e + 1];
+          x[e] = u * T(cs[e]) - y * T(sn[e]);
+          x[e + 1] = y * T(cs[e]) + u * T(sn[e]);
+        }
       }
-    }
-  } else {
-    T y[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = __shfl(x[e], partner, 16);
-    if (d0 < R) {
+    } else {
       const T sign = d0 < (R >> 1) ? T(-1) : T(1);
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = x[e] * T(cs[e]) + sign * y[e] * T(sn[e]);
+      for (int e = 0; e < E; ++e) {
+        const T y = __shfl(x[e], partner, 16);
+        if (d0 < R) x[e] = x[e] * T(cs[e]) + sign * y * T(sn[e]);
+      }
     }
   }
 }
@@ -83,9 +108,44 @@ __device__ inline _Float16 half_by_float(double x) {
   return (_Float16)f;
 }
 
-// The row's 4-bit form: nibbles n[] of this lane's channels and the pair (s, b).
-// In binary64 (which this part multiplies and adds as fast as binary32): a
-// nibble next to the border between two is then decided as the definition
+// The row's 4-bit form, nibbles n[] of this lane's channels and the pair (s, b),
+// in binary32; false where that cannot be told apart from what binary64 gives
+// (some 10 % of the waves with key rows, 1 % of those with value rows).
+// x is known to `off` times the row's largest size: s, b and (x - b) / s are
+// recomputed at both ends of what their errors allow, or kept away from ties.
+template <int E>
+__device__ inline bool quantise_fast(const float (&x)[E], float off, uint32_t (&n)[E], _Float16& s, _Float16& b) {
+  float lo = x[0], up = -x[0];  // up: the largest value's negative
+  bool sure = true;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    lo = least(lo, x[e]);
+    up = least(up, -x[e]);
+    sure &= fabsf(x[e]) <= kKvLimit;
+  }
+  lo = min16(lo);
+  up = min16(up);
+  const float err = off * fmaxf(fabsf(lo), fabsf(up));
+  const float sf = (-up - lo) * (1.f / 15.f), es = err * (2.f / 15.f) + sf * 0x1p-21f;
+  s = (_Float16)(sf - es);
+  sure &= s == (_Float16)(sf + es);
+  const float sh = (float)s, bf = lo - 16.f * sh, eb = err + fabsf(bf) * 0x1p-22f;
+  b = (_Float16)(bf - eb);
+  sure &= b == (_Float16)(bf + eb) && sh > 0.f;
+  const float bh = (float)b, inv = 1.f / sh;
+  // x - b, 1 / s and their product: each within 2^-24 of a number below 32 + 1 steps
+  const float margin = 0.5f - (err * inv + 32.f * 0x1p-21f);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const float t = (x[e] - bh) * inv, k = rintf(t);
+    sure &= fabsf(t - k) < margin;
+    n[e] = (uint32_t)(int)fminf(fmaxf(k - 16.f, 0.f), 15.f);
+  }
+  return sure;
+}
+
+// The same in binary64, where a
+// nibble next to the border between two is decided as the definition
 // says, ties of (x - b) / s to even. x - b and n s are exact for values of
 // binary16, so the remainder tells a tie where the product with 1 / s cannot.
 template <int E>
@@ -118,105 +178,184 @@ __device__ inline bool quantise(double (&x)[E], uint32_t (&n)[E], _Float16& s, _
   return bad;
 }
 
-// D = 16 E.
-template <int E>
-__global__ __launch_bounds__(kThreads) void kv_append_kernel(KvAppendArgs a) {
+enum Role { kQueries, kKeysValues, kBoth };
+
+// Element i of an array that no kernel writes meanwhile, by a scalar load.
+__device__ inline int64_t scalar_load(const int64_t* p, uint32_t i) {
+  typedef const int64_t __attribute__((address_space(4))) * constant;
+  return ((constant)(uintptr_t)p)[i];
+}
+
+// A wave works on four rows of one token at a time, a quad: four query heads,
+// four keys or four values, so that token, slot and page are scalars and keys
+// and values do not diverge. It takes `a.quads` of them in turn, and loads all
+// before it works on the first. Queries and keys with values have kernels of
+// their own where there are many tokens: quantising takes more registers,
+// which would halve the queries' occupancy. With few tokens one launch has
+// both (blockIdx.y is the role). D = 16 E.
+constexpr int kAhead = 4;
+
+template <int E, int ROLE, int ROPE>
+__global__ __launch_bounds__(kThreads, ROLE == kQueries ? (E > 8 ? 4 : 6) : E > 8 ? 2 : 4) void kv_append_kernel(KvAppendArgs a) {
   using H = Halves<E>;
   constexpr int D = 16 * E;
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x & 15;  // of the row
+  const bool is_q = ROLE == kBoth ? blockIdx.y == 0 : ROLE == kQueries;
+  const int heads = is_q ? a.L.Hq : a.L.Hkv;
+  const uint32_t per_head4 = (uint32_t)(heads + 3) >> 2, quads = is_q ? per_head4 : 2 * per_head4;
+  const uint32_t all = (uint32_t)a.tokens * quads;  // at most 2^28
+  // Workgroups go to the 8 XCDs in turn: those of the 32 tokens of a block,
+  // whose values share lines, go to one, so that its L2 puts the lines
+  // together. The last ones, short of 8 blocks, go as they come.
+  uint32_t wg = blockIdx.x;
+  if (!is_q) {
+    const uint32_t n = a.near, g = wg / (8 * n), in = wg - g * 8 * n;
+    if ((g + 1) * 8 * n <= gridDim.x) wg = g * 8 * n + (in & 7) * n + (in >> 3);
+  }
+  const uint32_t begin = (wg * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * a.quads;
+  if (begin >= all) return;
+  const uint32_t count = all - begin < a.quads ? all - begin : a.quads;
+  const int lane = threadIdx.x & 15, sub = (threadIdx.x >> 4) & 3;  // of the row, row of the quad
   const int d0 = lane * E;
-  const int nq = a.q ? a.L.Hq : 0;
 
-  // This lane's cosines and sines: the same for every row of the token.
-  const int R = a.rope ? a.rope_dims : 0;
-  const int half = R >> 1;
-  float cs[E], sn[E];
-  int partner = lane;  // lane of the row that holds the rotation's other channels
-  if (R) {
-    const int64_t pos = a.positions[t];
-    if (pos < 0 || pos >= a.rope_len) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) kv_report(a.err, kKvPosition, t, pos, a.rope_len);
-      return;
+  struct Quad {
+    uint32_t t, i;  // token, quad of the token
+  };
+  const uint32_t t0 = __builtin_amdgcn_readfirstlane(begin / quads);
+  const Quad start = {t0, begin - t0 * quads};
+  auto after = [&](Quad x) { return x.i + 1 < quads ? Quad{x.t, x.i + 1} : Quad{x.t + 1, 0}; };
+  auto first_head = [&](Quad x) { return (int)(x.i < per_head4 ? x.i : x.i - per_head4) * 4; };
+
+  // The rows, four ahead.
+  const int64_t q_lane = sub * a.q_hs + d0, k_lane = sub * a.k_hs + d0, v_lane = sub * a.v_hs + d0;
+  H ahead[kAhead];
+  Quad x = start;
+#pragma unroll
+  for (uint32_t c = 0; c < kAhead; ++c) {
+    if (c < count) {
+      const int h = first_head(x);
+      if (h + sub < heads) {
+        const _Float16* src = is_q ? a.q + x.t * a.q_ts + h * a.q_hs + q_lane
+                                   : x.i < per_head4 ? a.k + x.t * a.k_ts + h * a.k_hs + k_lane
+                                                     : a.v + x.t * a.v_ts + h * a.v_hs + v_lane;
+        ahead[c] = *reinterpret_cast<const H*>(src);
+      }
+      x = after(x);
     }
-    if (d0 < R) {
-      const float* row = a.rope + pos * R;
-      if (a.interleaved) {
+  }
+
+  const int R = ROPE == kNone ? 0 : ROPE == kWhole ? D : a.rope_dims, half = R >> 1;
+  int partner = lane;  // lane of the row that holds the rotation's other channels
+  if (!a.interleaved && d0 < R) partner = d0 < half ? lane + half / E : lane - half / E;
+  H wn{};
+  const _Float16* weights = is_q ? a.q_norm : a.k_norm;
+  if (weights) wn = *reinterpret_cast<const H*>(weights + d0);
+  float cs[E], sn[E];  // this lane's cosines and sines, of the token at hand
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    cs[e] = 1.f;
+    sn[e] = 0.f;
+  }
+
+  x = start;
+  int64_t pos = 0, slot = 0;
+#pragma unroll
+  for (uint32_t c = 0; c < kAhead; ++c) {
+    if (c >= count) break;
+    const Quad now = x;
+    x = after(x);
+    const bool fresh = c == 0 || now.i == 0;
+    const bool is_k = !is_q && now.i < per_head4;
+    const int h0 = first_head(now);
+    if (fresh) {
+      if (!is_q) slot = scalar_load(a.slots, now.t);
+      if (R) pos = scalar_load(a.positions, now.t);
+    }
+    if (R && (pos < 0 || pos >= a.rope_len)) {
+      if (fresh && (threadIdx.x & 63) == 0) kv_report(a.err, kKvPosition, a.first + now.t, pos, a.rope_len);
+      continue;
+    }
+    if (!is_q && (slot < 0 || slot >= (a.L.num_pages << a.L.page_shift))) {
+      if (slot >= 0 && fresh && (threadIdx.x & 63) == 0)
+        kv_report(a.err, kKvSlot, a.first + now.t, slot, a.L.num_pages << a.L.page_shift);
+      continue;
+    }
+    if (R && (is_q || is_k) && fresh && d0 < R) {
+      const float* rp = a.rope + pos * R;
+      if (ROPE == kOther && a.interleaved) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          cs[e] = row[(d0 + e) >> 1];
-          sn[e] = row[half + ((d0 + e) >> 1)];
+          cs[e] = rp[(d0 + e) >> 1];
+          sn[e] = rp[half + ((d0 + e) >> 1)];
         }
       } else {
         const int i0 = d0 < half ? d0 : d0 - half;
-        partner = d0 < half ? lane + half / E : lane - half / E;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          cs[e] = row[i0 + e];
-          sn[e] = row[half + i0 + e];
+          cs[e] = rp[i0 + e];
+          sn[e] = rp[half + i0 + e];
         }
       }
     }
-  }
-  int64_t slot = -1;
-  if (a.k) {
-    slot = a.slots[t];
-    if (slot >= (a.L.num_pages << a.L.page_shift)) {
-      if (threadIdx.x == 0 && blockIdx.y == 0) kv_report(a.err, kKvSlot, t, slot, a.L.num_pages << a.L.page_shift);
-      slot = -1;
-    }
-  }
-
-  // All 16 lanes of a row take the same path below; `r` is the same for them.
-  for (int r = blockIdx.y * kRowsPerPass + (threadIdx.x >> 4); r < a.rows; r += gridDim.y * kRowsPerPass) {
-    const bool is_q = r < nq;
-    const bool is_k = !is_q && r < nq + a.L.Hkv;
-    const int h = is_q ? r : is_k ? r - nq : r - nq - a.L.Hkv;
-    if (!is_q && slot < 0) continue;
-    const _Float16* src = is_q ? a.q + t * a.q_ts + h * a.q_hs
-                               : is_k ? a.k + t * a.k_ts + h * a.k_hs : a.v + t * a.v_ts + h * a.v_hs;
-    const H in = *reinterpret_cast<const H*>(src + d0);
-    if (is_q) {
-      float x[E];
+    if (h0 + sub >= heads) continue;
+    const H in = ahead[c];
+    float v[E];
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = (float)in.x[e];
-      norm_rope<float, E>(x, a.q_norm, a.eps, d0, R, a.interleaved, partner, cs, sn);
+    for (int e = 0; e < E; ++e) v[e] = (float)in.x[e];
+    auto prepare = [&](auto& y) {
+      typedef typename std::remove_reference<decltype(y[0])>::type T;
+      if (is_q || is_k) norm_rope<T, E, ROPE>(y, weights != nullptr, wn, a.eps, d0, R, a.interleaved, partner, cs, sn);
+    };
+    prepare(v);
+    if (is_q) {
       H out;
 #pragma unroll
-      for (int e = 0; e < E; ++e) out.x[e] = (_Float16)x[e];
-      *reinterpret_cast<H*>(a.q_out + t * a.o_ts + h * a.o_hs + d0) = out;
+      for (int e = 0; e < E; ++e) out.x[e] = (_Float16)v[e];
+      *reinterpret_cast<H*>(a.q_out + now.t * a.o_ts + h0 * a.o_hs + (sub * a.o_hs + d0)) = out;
       continue;
     }
-    double x[E];
+    if constexpr (ROLE != kQueries) {
+      uint32_t n[E];
+      _Float16 s, b;
+      // A norm leaves a relative error below 16 x 2^-24 (E + 4 additions, halved by the root, the root, a quotient, two
+      // products), a rotation then at most 2^(1/2) (16 + 2) 2^-24 of the row's largest size after it: 2^-18 covers both.
+      // For whole rows: their lanes work together.
+      if (__any(!quantise_fast<E>(v, is_k ? 0x1p-18f : 0.f, n, s, b))) {
+        double y[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = (double)in.x[e];
-    if (is_k) norm_rope<double, E>(x, a.k_norm, a.eps, d0, R, a.interleaved, partner, cs, sn);
-    uint32_t n[E];
-    _Float16 s, b;
-    if (quantise<E>(x, n, s, b)) kv_report(a.err, kKvValue, t, h, 0);
-    const int off = (int)(slot & (a.L.page_tokens - 1));
-    const int tok = off & 31;
-    char* blk = a.pages + kv_block_at(a.L, slot >> a.L.page_shift, h, off >> 5);
-    uint32_t word[E / 4];  // 16 bits each: channels 4 i .. 4 i + 3
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) word[i] = n[4 * i] | n[4 * i + 1] << 4 | n[4 * i + 2] << 8 | n[4 * i + 3] << 12;
-    _Float16* par = reinterpret_cast<_Float16*>(blk + 32 * D);
-    if (is_k) {
-      uint16_t* row = reinterpret_cast<uint16_t*>(blk + tok * (D / 2)) + lane * (E / 4);
-#pragma unroll
-      for (int i = 0; i < E / 4; ++i) row[i] = (uint16_t)word[i];
-      if (lane == 0) {
-        par[2 * tok] = s;
-        par[2 * tok + 1] = b;
+        for (int e = 0; e < E; ++e) y[e] = (double)in.x[e];
+        prepare(y);
+        if (quantise<E>(y, n, s, b)) kv_report(a.err, kKvValue, a.first + now.t, h0 + sub, 0);
       }
-    } else {
-      const int qr = kv_value_quarter(tok), e8 = kv_value_place(tok);
-      uint16_t* vb = reinterpret_cast<uint16_t*>(blk + 16 * D);
+      const int off = (int)(slot & (a.L.page_tokens - 1));
+      const int tok = off & 31;
+      char* blk = a.pages + kv_block_at(a.L, slot >> a.L.page_shift, h0, off >> 5) +
+                  (uint32_t)(sub * (a.L.page_tokens >> 5) * 32 * (D + 8));
+      uint32_t word[E / 4];  // 16 bits each: channels 4 i .. 4 i + 3
 #pragma unroll
-      for (int i = 0; i < E / 4; ++i) vb[((i * 4 + qr) * 16 + lane) * 8 + e8] = (uint16_t)word[i];
-      if (lane == 0) {
-        par[64 + qr * 8 + e8] = s;
-        par[96 + qr * 8 + e8] = b;
+      for (int w = 0; w < E / 4; ++w) word[w] = n[4 * w] | n[4 * w + 1] << 4 | n[4 * w + 2] << 8 | n[4 * w + 3] << 12;
+      _Float16* par = reinterpret_cast<_Float16*>(blk + 32 * D);
+      if (is_k) {
+        struct alignas(E / 2) Row {
+          uint16_t x[E / 4];
+        } out;
+#pragma unroll
+        for (int w = 0; w < E / 4; ++w) out.x[w] = (uint16_t)word[w];
+        *reinterpret_cast<Row*>(blk + tok * (D / 2) + lane * (E / 2)) = out;
+        if (lane == 0) {
+          struct alignas(4) Pair {
+            _Float16 s, b;
+          } pair = {s, b};
+          *reinterpret_cast<Pair*>(par + 2 * tok) = pair;
+        }
+      } else {
+        const int qr = kv_value_quarter(tok), e8 = kv_value_place(tok);
+        uint16_t* vb = reinterpret_cast<uint16_t*>(blk + 16 * D);
+#pragma unroll
+        for (int w = 0; w < E / 4; ++w) vb[((w * 4 + qr) * 16 + lane) * 8 + e8] = (uint16_t)word[w];
+        if (lane == 0) {
+          par[64 + qr * 8 + e8] = s;
+          par[96 + qr * 8 + e8] = b;
+        }
       }
     }
   }
@@ -262,20 +401,42 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a) {
 
 }  // namespace
 
-hipError_t launch_kv_append(const KvAppendArgs& a, int num_cus, hipStream_t s) {
-  // One workgroup per token walks its rows, so that the rotation's row is
-  // loaded once; with few tokens the rows go to several workgroups.
-  const int passes = (a.rows + kRowsPerPass - 1) / kRowsPerPass;
-  int64_t split = a.tokens >= 2 * num_cus ? 1 : (2 * num_cus + a.tokens - 1) / a.tokens;
-  if (split > passes) split = passes;
-  const dim3 grid((unsigned)a.tokens, (unsigned)split), block(kThreads);
-  switch (a.L.D) {
-    case 64: hipLaunchKernelGGL(kv_append_kernel<4>, grid, block, 0, s, a); break;
-    case 128: hipLaunchKernelGGL(kv_append_kernel<8>, grid, block, 0, s, a); break;
-    case 256: hipLaunchKernelGGL(kv_append_kernel<16>, grid, block, 0, s, a); break;
-    default: return hipErrorInvalidValue;
+namespace {
+
+template <int E, int ROPE>
+hipError_t launch_append(KvAppendArgs a, int num_cus, hipStream_t s) {
+  constexpr int waves = kThreads / 64;
+  const int64_t nq = a.q ? (a.L.Hq + 3) / 4 : 0, nk = a.k ? (a.L.Hkv + 3) / 4 * 2 : 0;  // quads of a token
+  // Few quads: one to a wave, so that they spread over the chip.
+  const bool few = a.tokens * (nq + nk) <= (int64_t)num_cus * 32;
+  a.quads = few ? 1 : kAhead;
+  a.near = (uint32_t)(32 * nk / (waves * a.quads) > 1 ? 32 * nk / (waves * a.quads) : 1);
+  auto groups = [&](int64_t quads) { return (unsigned)((a.tokens * quads + waves * a.quads - 1) / (waves * a.quads)); };
+  if (few && nq && nk) {
+    hipLaunchKernelGGL((kv_append_kernel<E, kBoth, ROPE>), dim3(groups(nq > nk ? nq : nk), 2), dim3(kThreads), 0, s, a);
+  } else {
+    if (nq) hipLaunchKernelGGL((kv_append_kernel<E, kQueries, ROPE>), dim3(groups(nq)), dim3(kThreads), 0, s, a);
+    if (nk) hipLaunchKernelGGL((kv_append_kernel<E, kKeysValues, ROPE>), dim3(groups(nk)), dim3(kThreads), 0, s, a);
   }
   return hipGetLastError();
+}
+
+template <int E>
+hipError_t launch_rope(const KvAppendArgs& a, int num_cus, hipStream_t s) {
+  if (!a.rope) return launch_append<E, kNone>(a, num_cus, s);
+  if (a.rope_dims == 16 * E && !a.interleaved) return launch_append<E, kWhole>(a, num_cus, s);
+  return launch_append<E, kOther>(a, num_cus, s);
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvAppendArgs& a, int num_cus, hipStream_t s) {
+  switch (a.L.D) {
+    case 64: return launch_rope<4>(a, num_cus, s);
+    case 128: return launch_rope<8>(a, num_cus, s);
+    case 256: return launch_rope<16>(a, num_cus, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t s) {

@@ -34,7 +34,8 @@ struct KvAppendArgs {
   int32_t rope_dims, interleaved;
   const _Float16 *q_norm, *k_norm;
   float eps;
-  int32_t rows;  // heads of one token: Hq (with q) + 2 Hkv (with k)
+  int64_t first;  // number of the call's token that is token 0 here
+  uint32_t quads, near;  // quads of a wave, workgroups of 32 tokens (the launch fills them in)
   ErrWord* err;
 };
 

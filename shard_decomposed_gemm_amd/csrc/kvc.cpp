@@ -136,12 +136,21 @@ int kvc_append(kvc_ctx* ctx, void* pages, const kvc_append_args* p, void* stream
   a.q_norm = static_cast<const _Float16*>(p->q_norm);
   a.k_norm = static_cast<const _Float16*>(p->k_norm);
   a.eps = p->eps;
-  a.rows = (p->q ? L.Hq : 0) + (p->k ? 2 * L.Hkv : 0);
   a.err = ctx->err_dev;
   OnDevice on(ctx->device);
   if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");
-  const hipError_t e = launch_kv_append(a, ctx->num_cus, static_cast<hipStream_t>(stream));
-  return e == hipSuccess ? AGEMM_OK : hip_fail(ctx, e, "append launch");
+  // The kernels count quads of rows in 32 bits, at most 512 a token: one launch up to 2^19 tokens.
+  const int64_t piece = int64_t{1} << 19;
+  for (a.first = 0; a.first < p->tokens; a.first += piece) {
+    KvAppendArgs c = a;
+    c.tokens = p->tokens - a.first < piece ? p->tokens - a.first : piece;
+    if (c.q) c.q += a.first * a.q_ts, c.q_out += a.first * a.o_ts;
+    if (c.k) c.k += a.first * a.k_ts, c.v += a.first * a.v_ts, c.slots += a.first;
+    if (c.positions) c.positions += a.first;
+    const hipError_t e = launch_kv_append(c, ctx->num_cus, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(ctx, e, "append launch");
+  }
+  return AGEMM_OK;
 }
 
 int kvc_attend_workspace(const kvc_ctx* ctx, int32_t batch, int32_t max_q, int64_t max_kv, int64_t* bytes) {
