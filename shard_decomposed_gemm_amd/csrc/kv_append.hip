@@ -49,8 +49,8 @@ __device__ inline T sum16(T v) {
   v += rotated<2>(v);
   return v + rotated<1>(v);
 }
-__device__ inline float least(float a, float b) { return a < b ? a : b; }
-__device__ inline double least(double a, double b) { return a < b ? a : b; }
+__device__ inline float least(float a, float b) { return fminf(a, b); }
+__device__ inline double least(double a, double b) { return fmin(a, b); }
 template <class T>
 __device__ inline T min16(T v) {
   v = least(v, rotated<8>(v));
@@ -108,39 +108,45 @@ __device__ inline _Float16 half_by_float(double x) {
   return (_Float16)f;
 }
 
-// The row's 4-bit form, nibbles n[] of this lane's channels and the pair (s, b),
+// The row's 4-bit form, 16-bit words of this lane's nibbles and the pair (s, b),
 // in binary32; false where that cannot be told apart from what binary64 gives
-// (some 10 % of the waves with key rows, 1 % of those with value rows).
+// (some 13 % of the quads of rows: of values for ties, which binary16 inputs
+// often are).
 // x is known to `off` times the row's largest size: s, b and (x - b) / s are
 // recomputed at both ends of what their errors allow, or kept away from ties.
 template <int E>
-__device__ inline bool quantise_fast(const float (&x)[E], float off, uint32_t (&n)[E], _Float16& s, _Float16& b) {
-  float lo = x[0], up = -x[0];  // up: the largest value's negative
-  bool sure = true;
+__device__ inline bool quantise_fast(const float (&x)[E], float off, uint32_t (&word)[E / 4], _Float16& s, _Float16& b) {
+  float lo = x[0], hi = x[0], finite = 0.f;  // finite: a NaN if some x is not finite
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    lo = least(lo, x[e]);
-    up = least(up, -x[e]);
-    sure &= fabsf(x[e]) <= kKvLimit;
+    lo = fminf(lo, x[e]);
+    hi = fmaxf(hi, x[e]);
+    finite = __builtin_fmaf(x[e], 0.f, finite);
   }
   lo = min16(lo);
-  up = min16(up);
-  const float err = off * fmaxf(fabsf(lo), fabsf(up));
-  const float sf = (-up - lo) * (1.f / 15.f), es = err * (2.f / 15.f) + sf * 0x1p-21f;
+  hi = -min16(-hi);
+  const float size = fmaxf(-lo, hi), err = off * fmaxf(fabsf(lo), fabsf(hi));
+  const float sf = (hi - lo) * (1.f / 15.f), es = err * (2.f / 15.f) + sf * 0x1p-21f;
   s = (_Float16)(sf - es);
-  sure &= s == (_Float16)(sf + es);
-  const float sh = (float)s, bf = lo - 16.f * sh, eb = err + fabsf(bf) * 0x1p-22f;
+  const float sh = (float)s, bf = lo - 16.f * sh;
+  const float eb = off > 0.f ? err + fabsf(bf) * 0x1p-22f : 0.f;  // of exact x, bf is the exact number rounded to binary32
   b = (_Float16)(bf - eb);
-  sure &= b == (_Float16)(bf + eb) && sh > 0.f;
+  bool sure = finite == 0.f && size <= kKvLimit && sh > 0.f && s == (_Float16)(sf + es) && b == (_Float16)(bf + eb);
   const float bh = (float)b, inv = 1.f / sh;
-  // x - b, 1 / s and their product: each within 2^-24 of a number below 32 + 1 steps
-  const float margin = 0.5f - (err * inv + 32.f * 0x1p-21f);
+  float k[E], far = 0.f;  // far: the largest distance of (x - b) / s from a whole number
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const float t = (x[e] - bh) * inv, k = rintf(t);
-    sure &= fabsf(t - k) < margin;
-    n[e] = (uint32_t)(int)fminf(fmaxf(k - 16.f, 0.f), 15.f);
+    const float t = (x[e] - bh) * inv;
+    k[e] = rintf(t);
+    far = fmaxf(far, fabsf(t - k[e]));
+    k[e] = __builtin_amdgcn_fmed3f(k[e], 16.f, 31.f);
   }
+  // x - b, 1 / s and their product: each within 2^-24 of a number below 32 + 1 steps
+  sure = sure && far < 0.5f - (err * inv + 32.f * 0x1p-21f);
+#pragma unroll
+  for (int i = 0; i < E / 4; ++i)  // whole numbers below 2^18: exact
+    word[i] = (uint32_t)__builtin_fmaf(__builtin_fmaf(__builtin_fmaf(k[4 * i + 3], 16.f, k[4 * i + 2]), 16.f, k[4 * i + 1]),
+                                       16.f, k[4 * i]) - 16 * 0x1111;
   return sure;
 }
 
@@ -149,7 +155,7 @@ __device__ inline bool quantise_fast(const float (&x)[E], float off, uint32_t (&
 // says, ties of (x - b) / s to even. x - b and n s are exact for values of
 // binary16, so the remainder tells a tie where the product with 1 / s cannot.
 template <int E>
-__device__ inline bool quantise(double (&x)[E], uint32_t (&n)[E], _Float16& s, _Float16& b) {
+__device__ inline bool quantise(double (&x)[E], uint32_t (&word)[E / 4], _Float16& s, _Float16& b) {
   bool bad = false;
   double lo = kKvLimit, up = kKvLimit;  // up: the largest value's negative
 #pragma unroll
@@ -173,7 +179,8 @@ __device__ inline bool quantise(double (&x)[E], uint32_t (&n)[E], _Float16& s, _
     const double rest = fma(-k, sd, y);
     if (fabs(rest) * 2.0 == sd && ((int)k & 1)) k += rest > 0.0 ? 1.0 : -1.0;
     const int i = (int)k - 16;  // s = 0: k = 0
-    n[e] = (uint32_t)(i < 0 ? 0 : i > 15 ? 15 : i);
+    const uint32_t n = i < 0 ? 0 : i > 15 ? 15 : i;
+    word[e / 4] = (e & 3 ? word[e / 4] : 0) | n << 4 * (e & 3);
   }
   return bad;
 }
@@ -314,25 +321,22 @@ __global__ __launch_bounds__(kThreads, ROLE == kQueries ? (E > 8 ? 4 : 6) : E > 
       continue;
     }
     if constexpr (ROLE != kQueries) {
-      uint32_t n[E];
+      uint32_t word[E / 4];  // channels 4 i .. 4 i + 3
       _Float16 s, b;
       // A norm leaves a relative error below 16 x 2^-24 (E + 4 additions, halved by the root, the root, a quotient, two
       // products), a rotation then at most 2^(1/2) (16 + 2) 2^-24 of the row's largest size after it: 2^-18 covers both.
       // For whole rows: their lanes work together.
-      if (__any(!quantise_fast<E>(v, is_k ? 0x1p-18f : 0.f, n, s, b))) {
+      if (__any(!quantise_fast<E>(v, is_k ? 0x1p-18f : 0.f, word, s, b))) {
         double y[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = (double)in.x[e];
         prepare(y);
-        if (quantise<E>(y, n, s, b)) kv_report(a.err, kKvValue, a.first + now.t, h0 + sub, 0);
+        if (quantise<E>(y, word, s, b)) kv_report(a.err, kKvValue, a.first + now.t, h0 + sub, 0);
       }
       const int off = (int)(slot & (a.L.page_tokens - 1));
       const int tok = off & 31;
       char* blk = a.pages + kv_block_at(a.L, slot >> a.L.page_shift, h0, off >> 5) +
                   (uint32_t)(sub * (a.L.page_tokens >> 5) * 32 * (D + 8));
-      uint32_t word[E / 4];  // 16 bits each: channels 4 i .. 4 i + 3
-#pragma unroll
-      for (int w = 0; w < E / 4; ++w) word[w] = n[4 * w] | n[4 * w + 1] << 4 | n[4 * w + 2] << 8 | n[4 * w + 3] << 12;
       _Float16* par = reinterpret_cast<_Float16*>(blk + 32 * D);
       if (is_k) {
         struct alignas(E / 2) Row {
@@ -407,9 +411,11 @@ template <int E, int ROPE>
 hipError_t launch_append(KvAppendArgs a, int num_cus, hipStream_t s) {
   constexpr int waves = kThreads / 64;
   const int64_t nq = a.q ? (a.L.Hq + 3) / 4 : 0, nk = a.k ? (a.L.Hkv + 3) / 4 * 2 : 0;  // quads of a token
-  // Few quads: one to a wave, so that they spread over the chip.
-  const bool few = a.tokens * (nq + nk) <= (int64_t)num_cus * 32;
-  a.quads = few ? 1 : kAhead;
+  // Few quads: one launch, which the host takes 2.5 us longer to make two of;
+  // and with still fewer one to a wave, so that they spread over the chip.
+  const int64_t all = a.tokens * (nq + nk);
+  const bool few = all <= (int64_t)num_cus * 64;
+  a.quads = all <= (int64_t)num_cus * 32 ? 1 : kAhead;
   a.near = (uint32_t)(32 * nk / (waves * a.quads) > 1 ? 32 * nk / (waves * a.quads) : 1);
   auto groups = [&](int64_t quads) { return (unsigned)((a.tokens * quads + waves * a.quads - 1) / (waves * a.quads)); };
   if (few && nq && nk) {
