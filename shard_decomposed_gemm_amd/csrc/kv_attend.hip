@@ -610,29 +610,53 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
     if (piece == 0) there[buf][pb] = have;
   };
 
-  auto take = [&](int j, int buf, int kb, bool mask) {
-    float16v s;
+  // NB blocks of a tile at once: their scores are independent chains of products.
+  constexpr int NB = KB < 2 ? KB : 2;
+  auto take = [&](int j, int buf, int kb) {
+    float16v s[NB];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = 0.f;
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[n][i] = 0.f;
+    auto key = [&](int n, int u) { return kl[buf][((kb + n) * KS + u) * 64 + (lane ^ ((u >> 1) * (8 / RN)))]; };
+    half8v k[2][NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) k[0][n] = key(n, 0);
 #pragma unroll
     for (int u = 0; u < KS; ++u) {
-      const half8v k = kl[buf][(kb * KS + u) * 64 + (lane ^ ((u >> 1) * (8 / RN)))];
-      s = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[u], s, 0, 0, 0);
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+        if (u + 1 < KS) k[(u + 1) & 1][n] = key(n, u + 1);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) s[n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[u & 1][n], q[u], s[n], 0, 0, 0);
     }
-    float e[16];
+    // A block without a page, or past the run, is hidden from every row.
+    bool hide = j + NB > whole;
+    int left[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const bool here = j + n < j1 && uniform(there[buf][kb + n]);
+      hide |= !here;
+      left[n] = here ? seen - ((j + n) * 32 + hh * 4) : 0;
+    }
+    float e[NB][16];
     float top;
-    int left = seen - (j * 32 + hh * 4);
     auto exponents = [&](float bs) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) e[i] = __builtin_fmaf(s[i], factor, -bs);
-      if (mask) {
-        asm volatile("" : "+v"(left));  // keeps the comparisons in this branch
+      for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (8 * (i >> 2) + (i & 3) >= left) e[i] = -__builtin_inff();
+        for (int i = 0; i < 16; ++i) e[n][i] = __builtin_fmaf(s[n][i], factor, -bs);
+      if (hide) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          asm volatile("" : "+v"(left[n]));  // keeps the comparisons in this branch
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (8 * (i >> 2) + (i & 3) >= left[n]) e[n][i] = -__builtin_inff();
+        }
       }
-      top = max8(e);
-      top = max3(top, max8(e + 8), top);
+      top = max3(max8(e[0]), max8(e[0] + 8), max8(e[NB - 1] + 8));
+      if constexpr (NB > 1) top = max3(top, max8(e[1]), top);
     };
     exponents(base);
     if (__any(top > kTop)) {
@@ -646,23 +670,26 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
       base = nb;
       exponents(nb);
     }
-    half8v hi[2], lo[2];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const float p0 = exp2_hw(e[i]), p1 = exp2_hw(e[i + 1]);
-      sum += p0;
-      sum += p1;
-      // group i / 4 of four keys: elements 0..3 of product 0 and 1, then 4..7
-      split_weight<F32>(p0, p1, hi[(i >> 2) & 1], lo[(i >> 2) & 1], (i >> 3) * 4 + (i & 3));
-    }
+    for (int n = 0; n < NB; ++n) {
+      half8v hi[2], lo[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const half8v v = vl[buf][((kb * 2 + u) * MT + m) * 64 + lane];
-        o[m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, hi[u], o[m], 0, 0, 0);
-        if constexpr (F32) o[m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, lo[u], o[m], 0, 0, 0);
+      for (int i = 0; i < 16; i += 2) {
+        const float p0 = exp2_hw(e[n][i]), p1 = exp2_hw(e[n][i + 1]);
+        sum += p0;
+        sum += p1;
+        // group i / 4 of four keys: elements 0..3 of product 0 and 1, then 4..7
+        split_weight<F32>(p0, p1, hi[(i >> 2) & 1], lo[(i >> 2) & 1], (i >> 3) * 4 + (i & 3));
       }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const half8v v = vl[buf][(((kb + n) * 2 + u) * MT + m) * 64 + lane];
+          o[m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, hi[u], o[m], 0, 0, 0);
+          if constexpr (F32) o[m] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, lo[u], o[m], 0, 0, 0);
+        }
+    }
   };
 
   if (j0 < j1) {
@@ -673,10 +700,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
     int buf = 0;
     for (int jt = j0; jt < j1; jt += KB, buf ^= 1) {
 #pragma unroll 1
-      for (int kb = 0; kb < KB; ++kb) {
-        const int j = jt + kb;
-        if (j < j1 && j < none && uniform(there[buf][kb])) take(j, buf, kb, j >= whole);
-      }
+      for (int kb = 0; kb < KB; kb += NB)
+        if (jt + kb < j1 && jt + kb < none) take(jt + kb, buf, kb);
       if (jt + KB < j1) {
         spread(jt + KB, buf ^ 1);
         if (jt + 2 * KB < j1) fetch(jt + 2 * KB);
