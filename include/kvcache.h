@@ -32,7 +32,9 @@
  * are never used, as long as lengths and page tables do not name them.
  *
  * Shapes: 1 <= Hkv, Hq a multiple of Hkv, Hq <= 1024; D in {64, 128, 256};
- * page_tokens in {32, 64, 128, 256}; num_pages * page_tokens <= 2^40.
+ * page_tokens in {32, 64, 128, 256}; num_pages * page_tokens <= 2^40. A call
+ * takes up to 2^23 tokens; an attention call's batch * table_width *
+ * page_tokens up to 2^35, and fewer than 2^23 workgroups' items (ESHAPE beyond).
  *
  * Every call returns an agemm_status (agemm.h), validates before launching (a
  * failed call launches nothing) and is asynchronous on the given stream (a
@@ -81,7 +83,8 @@ typedef struct {
   const void* q;               /* T x Hq x D, or NULL: no queries */
   const void* k;               /* T x Hkv x D, or NULL with v: no keys and values */
   const void* v;               /* T x Hkv x D */
-  void* q_out;                 /* T x Hq x D; required with q; may be q itself (same strides) */
+  void* q_out;                 /* T x Hq x D; required with q; may be q itself (same strides), else apart
+                                  from q, k and v */
   int64_t q_token_stride, q_head_stride;
   int64_t k_token_stride, k_head_stride;
   int64_t v_token_stride, v_head_stride;
@@ -149,8 +152,8 @@ typedef struct {
  * Reported by kvc_check: a page id outside the cache (its tokens count as not
  * seen), a length that is negative or does not fit the table (clamped), a
  * sequence with more than max_q queries or rows past T (those rows are left).
- * The order of summation depends on the shapes alone: equal calls give equal
- * bits. workspace: at least kvc_attend_workspace bytes, 16-byte aligned (NULL
+ * The order of summation depends on the shapes and lengths alone: equal calls
+ * give equal bits. workspace: at least kvc_attend_workspace bytes, 16-byte aligned (NULL
  * if that is 0); its contents before and after mean nothing. */
 int kvc_attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* args, void* workspace,
                int64_t workspace_bytes, void* stream);

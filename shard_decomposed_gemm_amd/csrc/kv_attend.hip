@@ -131,6 +131,7 @@ struct Sequence {
   int len;       // cached tokens
   int64_t off;   // the first query sees off + 1 tokens
 
+  __device__ int blocks() const { return n > 0 ? (seen(n - 1) + 31) >> 5 : 0; }  // that its last query sees
   __device__ int seen(int i) const {
     const int64_t v = off + i + 1;
     return v < 0 ? 0 : v > len ? len : (int)v;
@@ -150,16 +151,19 @@ __device__ inline int scalar_load(const int32_t* p, int64_t i) {
   return ((constant)(uintptr_t)p)[i];
 }
 
+// b the same in all lanes, or (EACH) one sequence a lane.
+template <bool EACH = false>
 __device__ inline Sequence sequence(const KvAttendArgs& a, int b, bool tell) {
+  auto load = [](const int32_t* p, int64_t i) { return EACH ? p[i] : scalar_load(p, i); };
   Sequence s;
   int start = b, end = b + 1;
   if (a.q_start) {
-    start = scalar_load(a.q_start, b);
-    end = scalar_load(a.q_start, b + 1);
+    start = load(a.q_start, b);
+    end = load(a.q_start, b + 1);
   }
-  const int len = scalar_load(a.kv_len, b);
+  const int len = load(a.kv_len, b);
   const int64_t n = (int64_t)end - start;
-  s.off = !a.causal ? (int64_t)1 << 32 : a.q_off ? (int64_t)scalar_load(a.q_off, b) : 0;
+  s.off = !a.causal ? (int64_t)1 << 32 : a.q_off ? (int64_t)load(a.q_off, b) : 0;
   const bool usable = n >= 0 && n <= a.max_q && start >= 0 && end <= a.tokens;
   if (!usable && tell) kv_report(a.err, kKvRows, b, n, a.max_q);
   s.n = usable ? (int)n : 0;
@@ -170,6 +174,71 @@ __device__ inline Sequence sequence(const KvAttendArgs& a, int b, bool tell) {
   s.len = len < 0 ? 0 : len <= most ? len : (int)most;
   if (a.causal && !a.q_off) s.off = (int64_t)s.len - n;
   return s;
+}
+
+// Sum of x over this lane and the earlier ones.
+__device__ inline int sum_up_to(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);  // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);  // row_shr:2
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);  // row_shr:4
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);  // row_shr:8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return x;
+}
+
+// The largest x of this lane and the earlier ones (x >= 0).
+__device__ inline int largest_up_to(int x) {
+  auto with = [&](int y) { x = x > y ? x : y; };
+  with(__builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
+  with(__builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
+  return x;
+}
+
+// Few rows: the runs of a call, from its lengths. Every wave works them out
+// for itself, 64 sequences at a time (kKvMaxBatch bounds them).
+struct Runs {
+  int chunk;     // blocks of a run
+  int b;         // the sequence found, -1: none
+  int64_t slot;  // its first run
+};
+// The sequence with run `run`, or (run < 0) sequence b. Blocks of a head and
+// runs of a head each sum up to at most 2^31 (the host sees to that).
+__device__ inline Runs find_runs(const KvAttendArgs& a, int64_t run, int b, int lane, bool tell) {
+  auto blocks = [&](int b0, bool& some, bool report) {
+    Sequence s{};
+    if (b0 + lane < a.batch) s = sequence<true>(a, b0 + lane, report);
+    some = s.n > 0;
+    return s.blocks();
+  };
+  bool some;
+  const int first = blocks(0, some, tell);
+  int all = __builtin_amdgcn_readlane(sum_up_to(first), 63), longest = __builtin_amdgcn_readlane(largest_up_to(first), 63);
+  bool other;
+  for (int b0 = 64; b0 < a.batch; b0 += 64) {
+    const int x = blocks(b0, other, tell), top = __builtin_amdgcn_readlane(largest_up_to(x), 63);
+    all += __builtin_amdgcn_readlane(sum_up_to(x), 63);
+    longest = longest > top ? longest : top;
+  }
+  const int chunk = kv_chunk(a.plan, (int64_t)all * a.L.Hkv, longest);
+  int before = 0;  // runs of a head before this group of sequences
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    const int nblk = b0 == 0 ? first : blocks(b0, some, false);
+    const int mine = some ? kv_item_runs(chunk, nblk) : 0;
+    const int upto = before + sum_up_to(mine);
+    const uint64_t at = run < 0 ? (b - b0 < 64 ? uint64_t{1} << (b - b0) : 0) : __ballot((int64_t)upto * a.L.Hkv > run);
+    if (at) {
+      const int l = __builtin_ctzll(at);
+      return {chunk, b0 + l,
+              (int64_t)(__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l)) * a.L.Hkv};
+    }
+    before = __builtin_amdgcn_readlane(upto, 63);
+  }
+  return {chunk, -1, 0};
 }
 
 // Page id of block j of a sequence with `end` blocks to take, one at least (past them: some page id).
@@ -286,20 +355,35 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   const uint32_t lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t col = lane & 15, quarter = lane >> 4;
-  // Late runs first: of a ragged batch they are the whole ones, and short sequences fill up the end.
-  const int item = blockIdx.x, run = a.plan.splits - 1 - blockIdx.y;
-  const int b = item / a.L.Hkv, h = item - b * a.L.Hkv;
   const int G = a.L.Hq / a.L.Hkv;
-  // The first page id goes out with the lengths: it is this one unless runs are longer than planned.
-  int page = page_of(a, b, run * a.plan.chunk + wave, a.table_width << (a.L.page_shift - 5));
-  const Sequence seq = sequence(a, b, run == 0 && h == 0 && threadIdx.x == 0);
+  const int64_t slot_id = blockIdx.x;
+  int b, h, run = 0, chunk = kKvWhole;
+  Sequence seq;
+  if (a.plan.slots <= a.plan.items) {  // one run an item
+    b = (int)blockIdx.x / a.L.Hkv;
+    h = (int)blockIdx.x - b * a.L.Hkv;
+    seq = sequence(a, b, h == 0 && threadIdx.x == 0);
+  } else {
+    if (a.batch == 1) {
+      b = 0;
+      seq = sequence(a, 0, blockIdx.x == 0 && threadIdx.x == 0);
+      chunk = kv_chunk(a.plan, (int64_t)seq.blocks() * a.L.Hkv, seq.blocks());
+      h = (int)blockIdx.x;
+    } else {
+      const Runs runs = find_runs(a, slot_id, 0, lane, blockIdx.x == 0 && wave == 0);
+      if (runs.b < 0) return;
+      b = runs.b;
+      chunk = runs.chunk;
+      seq = sequence(a, b, false);
+      h = (int)(slot_id - runs.slot);
+    }
+    run = h / a.L.Hkv;
+    h -= run * a.L.Hkv;
+  }
   const int rows = seq.n * G;
-  if (rows == 0) return;
-  const int nblk = (seq.seen(seq.n - 1) + 31) >> 5;
-  const int runs = kv_runs(a.plan.chunk, a.plan.splits, nblk);
-  if (run >= runs) return;
-  const int chunk = kv_run_blocks(a.plan.chunk, a.plan.splits, nblk);
-  const int j1 = nblk < (run + 1) * chunk ? nblk : (run + 1) * chunk;
+  const int nblk = seq.blocks(), runs = kv_item_runs(chunk, nblk);
+  if (rows == 0 || run >= runs) return;
+  const int j1 = nblk - run * chunk < chunk ? nblk : (run + 1) * chunk;
   int j = run * chunk + wave;
 
   // A block without a page is read from the first page and hidden from every row.
@@ -309,12 +393,13 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   Lost lost;
   const char* blk = a.pages;
   const uint32_t key_at = col * (D / 2) + quarter * (D / 8);
+  int page = 0;  // of the block after the next
   auto find = [&](int at) {
     blk = a.pages + uniform(block_on(a, page, h, at, paged, lost));
     page = page_of(a, b, at + kWaves, j1);  // of the block after this one
   };
   if (j < j1) {
-    if (chunk != a.plan.chunk) page = page_of(a, b, j, j1);
+    page = page_of(a, b, j, j1);
     find(j);
     load_keys<D>(k, block_buffer<D>(blk), key_at, 4 * col);
     load_values<D>(v, block_buffer<D>(blk), 16 * lane, 16 * quarter);
@@ -460,7 +545,7 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
             float4v{o[n][m][i], o[n][m + 1][i], o[n][m + 2][i], o[n][m + 3][i]};
   }
   __syncthreads();
-  float* slot = a.ws + ((int64_t)item * a.plan.splits + run) * a.plan.slot_floats;
+  float* slot = a.ws + slot_id * a.plan.slot_floats;
   for (int x = threadIdx.x; x < rows * (D / 4); x += kWaves * 64) {
     const int r = x / (D / 4), d = 4 * (x % (D / 4));
     float top = kNoMax, all = 0.f;
@@ -771,21 +856,34 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendAr
   const Sequence seq = sequence(a, b, false);
   const int rows = seq.n * G;
   if (r0 + l0 >= rows) return;
-  const int r_last = r0 + rpi - 1 < rows ? r0 + rpi - 1 : rows - 1;
-  const int runs = kv_runs(a.plan.chunk, a.plan.splits, (seq.seen(r_last / G) + 31) >> 5);
+  const int lane = threadIdx.x & 63;
+  int runs;
+  int64_t slot, step = 1;  // of the first partial, and to the next
+  if (a.plan.many) {
+    const int r_last = r0 + rpi - 1 < rows ? r0 + rpi - 1 : rows - 1;
+    runs = kv_runs(a.plan.chunk, a.plan.splits, (seq.seen(r_last / G) + 31) >> 5);
+    slot = (int64_t)item * a.plan.splits;
+  } else {
+    Runs r = {0, 0, 0};
+    if (a.batch == 1) r.chunk = kv_chunk(a.plan, (int64_t)seq.blocks() * a.L.Hkv, seq.blocks());
+    else r = find_runs(a, -1, b, lane, false);
+    runs = kv_item_runs(r.chunk, seq.blocks());
+    slot = r.slot + h;
+    step = a.L.Hkv;
+  }
   if (runs == 1) return;  // written by its only run
   const int R = rows - r0 - l0 < RW ? rows - r0 - l0 : RW;
 
-  const int lane = threadIdx.x & 63;
-  const float* part = a.ws + (int64_t)item * a.plan.splits * a.plan.slot_floats;
+  const float* part = a.ws + slot * a.plan.slot_floats;
+  step *= a.plan.slot_floats;
   for (int r = uniform((int)threadIdx.x >> 6); r < R; r += kJoinThreads / 64) {
     const float* head = part + rpi * D + 2 * (l0 + r);
     float e[kKvMaxSplits / 64], n[kKvMaxSplits / 64], top = kNoMax, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kKvMaxSplits / 64; ++i) {
       const int s = 64 * i + lane;
-      e[i] = s < runs ? head[s * a.plan.slot_floats] : kNoMax;
-      n[i] = s < runs ? head[s * a.plan.slot_floats + 1] : 0.f;
+      e[i] = s < runs ? head[s * step] : kNoMax;
+      n[i] = s < runs ? head[s * step + 1] : 0.f;
       top = fmaxf(top, e[i]);
     }
 #pragma unroll
@@ -812,7 +910,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendAr
     const float* p = part + (int64_t)(l0 + r) * D + d;
 #pragma unroll 8
     for (int s = slice; s < runs; s += S)
-      v += *reinterpret_cast<const float4v*>(p + s * a.plan.slot_floats) * weight[r][s];
+      v += *reinterpret_cast<const float4v*>(p + s * step) * weight[r][s];
   }
   if (S > 1) {
     meet[threadIdx.x] = v;
@@ -830,12 +928,12 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendAr
 
 template <int D, bool F32>
 hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.plan.items, (unsigned)a.plan.splits);
+  const dim3 grid((unsigned)(a.plan.many ? a.plan.items : a.plan.slots), (unsigned)a.plan.splits);
   if (a.plan.many) hipLaunchKernelGGL((kv_attend_many_kernel<D, F32>), grid, dim3(kManyThreads), 0, s, a);
   else if (a.plan.rows == 16) hipLaunchKernelGGL((kv_attend_few_kernel<D, 1, F32>), grid, dim3(kWaves * 64), 0, s, a);
   else if constexpr (D <= 128)
     hipLaunchKernelGGL((kv_attend_few_kernel<D, 2, F32>), grid, dim3(kWaves * 64), 0, s, a);
-  if (a.plan.splits > 1)
+  if (a.plan.ws_bytes > 0)
     hipLaunchKernelGGL((kv_attend_join_kernel<D, F32>), dim3((unsigned)a.plan.items, (unsigned)a.plan.join_groups),
                        dim3(kJoinThreads), 0, s, a);
   return hipGetLastError();

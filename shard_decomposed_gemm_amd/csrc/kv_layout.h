@@ -31,26 +31,52 @@ KV_HD inline int kv_value_quarter(int t) { return (t >> 2) & 3; }
 KV_HD inline int kv_value_place(int t) { return ((t >> 4) << 2) | (t & 3); }
 
 // How one attention call's work is laid out. Rows of a kv head's item are its
-// query heads of all queries, r = query * G + head. Each item's blocks of 32
-// tokens go in runs of `chunk` to `splits` workgroups at most (longer runs
-// where a sequence has more blocks than that); the partials of an item with
-// several runs meet in the workspace, one slot per (item, run).
+// query heads of all queries, r = query * G + head.
+//
+// Few rows (many = 0): an item is a (sequence, kv head). Its blocks of 32
+// tokens go in runs of equal length, chosen on the device from the lengths of
+// the whole batch (kv_chunk), sequence by sequence, within one run by run and
+// head by head; a workgroup takes one run, and run i of the call leaves its
+// partial in slot i. With slots == items every item is one run.
+//
+// Many rows (many = 1): an item is a (sequence, tile of 128 rows, kv head);
+// its blocks go in runs of `chunk` to `splits` workgroups at most (longer runs
+// where a sequence has more blocks than that), one slot per (item, run).
 struct KvPlan {
-  int32_t many;    // 0: the kernel for few rows, 1: for many
+  int32_t many;
   int32_t rows;    // rows of one item
   int32_t join_rows, join_groups;  // the join: rows of a workgroup (a power of two), workgroups of an item
   int32_t tiles;   // items of one sequence and kv head
-  int32_t splits;
-  int32_t chunk;   // blocks of a run
-  int64_t items;
-  int64_t slot_floats;  // of one partial: rows x D, then rows x (exponent, sum)
+  int32_t splits, chunk;   // many rows
+  int32_t places, least, most;  // few rows: workgroups that run at once, the shortest and the longest run
+  int64_t items, slots;    // slots: few rows, the call's runs at most
+  int64_t slot_floats;     // of one partial: rows x D, then rows x (exponent, sum)
   int64_t ws_bytes;
 };
 
 constexpr int kKvMaxSplits = 256;
+constexpr int kKvMaxBatch = 512;  // sequences whose lengths every workgroup looks through
 constexpr int kKvWaves = 8;  // of a workgroup for few rows: each takes every eighth block of a run
+constexpr int kKvWhole = 1 << 26;  // blocks of the longest sequence
 
-// Blocks that a run of an item with nblk blocks has, and the runs.
+// Few rows: blocks of a run for U blocks in all, `longest` in one item: as many
+// runs as run at once, but none so long that the last of them keep the chip
+// waiting, no more runs than slots (each item has less than one that is not
+// full), and no more of an item than the join takes.
+KV_HD inline int kv_chunk(const KvPlan& p, int64_t U, int longest) {
+  if (p.slots <= p.items) return kKvWhole;
+  int64_t c = (U + p.places - 1) / p.places;
+  c = c < p.least ? p.least : c < p.most ? c : p.most;
+  const int64_t fits = (U + p.slots - p.items - 1) / (p.slots - p.items);
+  c = c > fits ? c : fits;
+  const int64_t joined = ((int64_t)longest + kKvMaxSplits - 1) / kKvMaxSplits;
+  c = c > joined ? c : joined;
+  return (int)(c < kKvWhole ? c : kKvWhole);
+}
+// Few rows: runs of an item of nblk blocks (an item whose rows see nothing has one).
+KV_HD inline int kv_item_runs(int chunk, int nblk) { return nblk <= chunk ? 1 : (nblk + chunk - 1) / chunk; }
+
+// Many rows: blocks that a run of an item with nblk blocks has, and the runs.
 KV_HD inline int kv_run_blocks(int chunk, int splits, int nblk) {
   const int need = (nblk + splits - 1) / splits;
   return need > chunk ? need : chunk;
@@ -61,42 +87,46 @@ KV_HD inline int kv_runs(int chunk, int splits, int nblk) {
 }
 
 inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
-  KvPlan p;
-  const int64_t rows = max_q * (L.Hq / L.Hkv);
+  KvPlan p{};
+  const int64_t rows = max_q * (L.Hq / L.Hkv), nblk = (max_kv + 31) / 32;
   p.many = rows > (L.D == 256 ? 16 : 32);
   p.rows = p.many ? 128 : rows > 16 ? 32 : 16;
   p.tiles = (int32_t)(p.many ? (rows + p.rows - 1) / p.rows : 1);
   p.items = batch * L.Hkv * p.tiles;
-  const int64_t nblk = (max_kv + 31) / 32;
-  int64_t chunk;
-  if (p.many) {
-    const int64_t places = (int64_t)num_cus * 4;
-    chunk = (p.items * nblk + places - 1) / places;
-    if (chunk < 32) chunk = 32;
-  } else if (nblk <= 4 * kKvWaves) {
-    chunk = nblk;  // four blocks a wave are done before a join would be
-  } else {
-    // As many runs as run at once, but none so long that the last of them
-    // keep the chip waiting: the more items, the longer they may be.
-    const int64_t places = (int64_t)num_cus * (L.D == 256 || p.rows == 32 ? 1 : 2);
-    chunk = (p.items * nblk + places - 1) / places;
-    if (chunk < kKvWaves) chunk = kKvWaves;
-    const int64_t most = 16 * kKvWaves * ((p.items + places - 1) / places);
-    if (chunk > most) chunk = most;
-  }
-  int64_t splits = (nblk + chunk - 1) / chunk;
-  if (splits < 1) splits = 1;
-  if (splits > kKvMaxSplits) {
-    splits = kKvMaxSplits;
-    chunk = (nblk + splits - 1) / splits;
-  }
-  p.chunk = (int32_t)(chunk < (int64_t{1} << 26) ? chunk : int64_t{1} << 26);
-  p.splits = (int32_t)splits;
   const int64_t live = rows < p.rows ? rows : p.rows;  // rows of an item that can exist
   p.join_rows = p.items * live <= 2 * num_cus ? 1 : 2048 / L.D;
   p.join_groups = (int32_t)((live + p.join_rows - 1) / p.join_rows);
   p.slot_floats = (int64_t)p.rows * (L.D + 2);
-  p.ws_bytes = p.splits > 1 ? p.items * p.splits * p.slot_floats * 4 : 0;
+  p.splits = 1;
+  p.slots = p.items;
+  if (p.many) {
+    const int64_t places = (int64_t)num_cus * 4;
+    int64_t chunk = (p.items * nblk + places - 1) / places;
+    if (chunk < 32) chunk = 32;
+    int64_t splits = (nblk + chunk - 1) / chunk;
+    if (splits > kKvMaxSplits) {
+      splits = kKvMaxSplits;
+      chunk = (nblk + splits - 1) / splits;
+    }
+    p.chunk = (int32_t)(chunk < kKvWhole ? chunk : kKvWhole);
+    p.splits = (int32_t)splits;
+    p.ws_bytes = p.splits > 1 ? p.items * p.splits * p.slot_floats * 4 : 0;
+  } else {
+    p.places = num_cus * (L.D == 256 || p.rows == 32 ? 1 : 2);
+    // One run an item: up to four blocks a wave are done before a join would
+    // be, and where there are items enough anyway, longer ones too.
+    if (nblk <= 4 * kKvWaves || batch > kKvMaxBatch || (p.items >= 2 * p.places && nblk * p.places <= 64 * p.items)) return p;
+    // A run costs some 8 us beside its blocks (lengths, first loads, the
+    // waves' join). A single sequence leaves most of the chip idle for them;
+    // in a batch, four blocks a wave make up for it.
+    p.least = batch > 1 ? 4 * kKvWaves : kKvWaves;
+    const int64_t most = 16 * kKvWaves * ((p.items + p.places - 1) / p.places);  // the more items, the longer
+    p.most = (int32_t)(most < kKvWhole ? most : kKvWhole);
+    int64_t runs = (p.items * nblk + p.most - 1) / p.most;
+    if (runs > 64 * p.places) runs = 64 * p.places;
+    p.slots = p.items + (runs > p.places ? runs : p.places);
+    p.ws_bytes = p.slots * p.slot_floats * 4;
+  }
   return p;
 }
 

@@ -40,14 +40,19 @@ int64_t kvh_block(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages, in
   return kv_block_at(L, slot >> L.page_shift, h, off >> 5);
 }
 
-// The work plan: many, rows, tiles, splits, chunk, items, slot_floats, ws_bytes.
+// The work plan: many, rows, join_rows, join_groups, tiles, splits, chunk, items, slots, slot_floats, ws_bytes.
+static KvPlan plan_of;
 void kvh_plan(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages, int64_t batch, int64_t max_q, int64_t max_kv,
               int num_cus, int64_t* out) {
   const KvPlan p = kv_attend_plan(kv_layout(Hq, Hkv, D, page_tokens, num_pages), batch, max_q, max_kv, num_cus);
-  const int64_t v[8] = {p.many, p.rows, p.tiles, p.splits, p.chunk, p.items, p.slot_floats, p.ws_bytes};
-  for (int i = 0; i < 8; ++i) out[i] = v[i];
+  plan_of = p;
+  const int64_t v[11] = {p.many, p.rows, p.join_rows, p.join_groups, p.tiles, p.splits, p.chunk, p.items,
+                         p.slots, p.slot_floats, p.ws_bytes};
+  for (int i = 0; i < 11; ++i) out[i] = v[i];
 }
-
+// Blocks of a run in the plan that kvh_plan made last.
+int kvh_chunk(int64_t U, int longest) { return kv_chunk(plan_of, U, longest); }
+int kvh_item_runs(int chunk, int nblk) { return kv_item_runs(chunk, nblk); }
 int kvh_run_blocks(int chunk, int splits, int nblk) { return kv_run_blocks(chunk, splits, nblk); }
 int kvh_runs(int chunk, int splits, int nblk) { return kv_runs(chunk, splits, nblk); }
 

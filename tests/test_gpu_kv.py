@@ -92,6 +92,8 @@ APPENDS = [
     (29, 3, 1, 128, 64, 16, True, False),
     (40, 7, 7, 128, 32, 0, False, True),
     (700, 96, 8, 128, 64, 128, True, True),
+    (4999, 6, 3, 64, 64, 64, False, False),
+    (2050, 16, 2, 128, 128, 64, True, True),
 ]
 
 
@@ -299,14 +301,14 @@ def _check_attend(got, lse, q, K, V, seen, scale, f32):
 
 
 def _run_attend(kv, pages, table, lens, q, starts=None, max_q=1, f32=True, q_off=None, causal=True, scale=None,
-                with_lse=True, extra=0, workspace=None, stream=None):
+                with_lse=True, max_kv=None, workspace=None, stream=None):
     import torch
     T, Hq, D = q.shape[0], q.shape[1], q.shape[2]
     out = torch.full((T, Hq, D), 9.0, dtype=torch.float32 if f32 else torch.float16, device=gu.dev())
     lse = torch.full((T, Hq), 9.0, dtype=torch.float32, device=gu.dev()) if with_lse else None
     i32 = lambda x: None if x is None else _dev(np.asarray(x, dtype=np.int32))  # noqa: E731
     kv.attend(pages, q, i32(lens), i32(table), out, lse=lse, q_start=i32(starts), max_q=max_q, q_off=i32(q_off),
-              causal=causal, scale=scale, workspace=workspace, stream=stream)
+              causal=causal, scale=scale, max_kv=max_kv, workspace=workspace, stream=stream)
     torch.cuda.synchronize()
     kv.check()
     return out.cpu().numpy().astype(np.float64), None if lse is None else lse.cpu().numpy().astype(np.float64)
@@ -377,6 +379,43 @@ def test_attend_several_queries(Hq, Hkv, D, page, shape, q_off, causal, f32):
         rows = slice(starts[i], starts[i + 1])
         _check_attend(got[rows], lse[rows], hq[rows], K[i], V[i], seen, 0.11, f32)
     assert (got[starts[-1]:] == 9).all() and (lse[starts[-1]:] == 9).all()
+
+
+LONG = [
+    # Hq, Hkv, D, page, [(queries, length)], q_off, max_kv: items in several runs, joined
+    (8, 1, 128, 64, [(40, 4200)], None, None),
+    (4, 2, 64, 32, [(70, 3001), (3, 90), (0, 2000), (66, 66)], None, None),
+    (3, 1, 256, 64, [(50, 2100), (17, 1030)], None, None),
+    (2, 1, 128, 32, [(80, 2500), (80, 2500), (80, 40)], [1000, -79, -40], None),
+    (16, 2, 128, 64, [(4, 3000), (2, 1500), (1, 2999)], [2000, -1, -5], None),
+    (5, 1, 64, 32, [(3, 1100), (6, 4000), (0, 3000), (1, 0)], None, None),
+    (4, 1, 128, 64, [(1, 9000), (1, 7), (1, 5000)], None, 64),       # longer than max_kv says
+    (4, 1, 128, 64, [(1, 9000), (1, 7), (1, 20000)], None, 2048),
+    (1, 1, 64, 256, [(1, 90000)], None, 3000),
+    (8, 1, 128, 64, [(40, 9000)], None, 1200),
+    (16, 1, 64, 128, [(1, 70000)], None, None),                      # as many runs as the join takes
+    (2, 2, 64, 32, [(1, 70 * (i % 7 == 0) + i) for i in range(69)] + [(1, 6000)], None, None),
+    (2, 1, 64, 32, [(1, 1400 if i == 200 else i % 9) for i in range(520)], None, None),
+    (2, 1, 64, 32, [(1, 1400 if i == 500 else i % 9) for i in range(512)], None, None),
+]
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,D,page,shape,q_off,max_kv", LONG)
+def test_attend_joins_runs(Hq, Hkv, D, page, shape, q_off, max_kv, f32):
+    print(f"[kv runs] {Hq} {Hkv} {D} {page} {shape[:4]} {len(shape)} {q_off} {max_kv} {f32}", flush=True)
+    lens = [n for _, n in shape]
+    starts = np.concatenate([[0], np.cumsum([q for q, _ in shape])])
+    pages, table, K, V = _sequences(Hq + D, Hkv, D, page, lens)
+    kv = _cache(Hq, Hkv, D, page_tokens=page, num_pages=pages.shape[0])
+    q = np.random.default_rng(4).standard_normal((int(starts[-1]), Hq, D)).astype(np.float16)
+    got, lse = _run_attend(kv, _dev(pages), table, lens, _dev(q), starts=starts, max_q=max(n for n, _ in shape), f32=f32,
+                           q_off=q_off, max_kv=max_kv, with_lse=f32)
+    for i, (n, L) in enumerate(shape):
+        off = L - n if q_off is None else q_off[i]
+        rows = slice(starts[i], starts[i + 1])
+        _check_attend(got[rows], None if lse is None else lse[rows], q[rows], K[i], V[i],
+                      np.clip(off + np.arange(n) + 1, 0, L), D ** -0.5, f32)
 
 
 @pytest.mark.parametrize("nq", [1, 3, 200])
@@ -560,6 +599,49 @@ def test_decode_step_in_a_graph():
         torch.cuda.synchronize()
         kv.check()
         assert torch.equal(out, eo) and torch.equal(lse, ez) and torch.equal(dp, eager_pages)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_joined_runs_in_a_graph(nq):
+    """Attention over long sequences, captured once; replays with other lengths equal the eager calls, and what lies in
+    the workspace before a replay does not matter."""
+    import torch
+    Hq, Hkv, D, page, B = 8, 2, 64, 64, 3
+    pages, table, K, V = _sequences(33, Hkv, D, page, [4000, 2600, 1500])
+    kv = _cache(Hq, Hkv, D, page_tokens=page, num_pages=pages.shape[0])
+    dp, dt = _dev(pages), _dev(table)
+    q = _dev(np.random.default_rng(6).standard_normal((B * nq, Hq, D)).astype(np.float16))
+    starts, lens = _dev(np.arange(B + 1, dtype=np.int32) * nq), torch.zeros(B, dtype=torch.int32, device=gu.dev())
+    out, eo = (torch.zeros(B * nq, Hq, D, device=gu.dev()) for _ in range(2))
+    ws = kv.workspace(B, nq, 4000)
+    assert ws.numel() > 0
+
+    def step(o, w):
+        kv.attend(dp, q, lens, dt, o, q_start=starts, max_q=nq, max_kv=4000, workspace=w)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(out, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(out, ws)
+    for n in ([4000, 2600, 1500], [1, 2600, 0], [nq, 0, 1500], [3999, 33, 700], [4000, 2600, 1500]):
+        lens.copy_(torch.tensor(n))
+        ws.fill_(0xFF)
+        out.fill_(9)
+        eo.fill_(9)
+        graph.replay()
+        step(eo, None)
+        torch.cuda.synchronize()
+        kv.check()
+        assert torch.equal(out, eo)
+    hq = q.cpu().numpy()
+    for i, L in enumerate(n):
+        rows = slice(i * nq, (i + 1) * nq)
+        _check_attend(out[rows].cpu().numpy().astype(np.float64), None, hq[rows], K[i], V[i],
+                      np.clip(L - nq + 1 + np.arange(nq), 0, L), D ** -0.5, True)
 
 
 def test_ranks_append_attend_and_combine():

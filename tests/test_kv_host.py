@@ -39,6 +39,7 @@ def host(tmp_path_factory):
     lib.kvh_block.restype = i64
     lib.kvh_plan.argtypes = shape + [i64, i64, i64, ctypes.c_int, ctypes.POINTER(i64)]
     lib.kvh_plan.restype = None
+    lib.kvh_chunk.argtypes = [i64, ctypes.c_int]
     return lib
 
 
@@ -156,25 +157,41 @@ def test_layout_functions_agree_with_the_oracle(host, D, page_tokens, Hkv):
 
 @pytest.mark.parametrize("Hq,Hkv,D", [(64, 8, 128), (96, 96, 128), (12, 1, 128), (16, 2, 256), (32, 4, 64), (72, 1, 64)])
 def test_plan_covers_every_block_once_within_its_workspace(host, Hq, Hkv, D):
-    """Runs of blocks partition every length, the longest that fits 32 bits among them, in no more runs than the grid
-    and the workspace have; a longer sequence than max_kv is covered too."""
-    v = (ctypes.c_int64 * 8)()
+    """Runs of blocks partition every length, the longest that fits 32 bits among them, in no more runs than the grid,
+    the workspace and the join have; longer sequences than max_kv are covered too."""
+    v = (ctypes.c_int64 * 11)()
+    r = np.random.default_rng(Hq)
     for batch in (1, 2, 7, 64, 500, 8192):
         for max_q in (1, 2, 5, 33, 700):
             for max_kv in (1, 33, 777, 4099, 65536, 262144, (1 << 31) - 1):
                 host.kvh_plan(Hq, Hkv, D, 64, 1000, batch, max_q, max_kv, 256, v)
-                many, rows, tiles, splits, chunk, items, slot, ws = v
-                assert 1 <= splits <= 256 and chunk >= 1 and items == batch * Hkv * tiles
+                many, rows, join_rows, join_groups, tiles, splits, chunk, items, slots, slot, ws = v
+                live = min(rows, max_q * (Hq // Hkv))
+                assert items == batch * Hkv * tiles and slot == rows * (D + 2)
                 assert tiles * rows >= max_q * (Hq // Hkv) and (many or tiles == 1)
-                assert slot == rows * (D + 2) and ws == (items * splits * slot * 4 if splits > 1 else 0)
-                assert splits == 1 or items * rows < 1 << 24  # the join's grid
-                for n in (0, 1, 2, 31, 32, 33, 64, 1000, (max_kv + 31) // 32, (max_kv + 31) // 32 * 3, 1 << 26):
-                    if n > 1 << 26:
-                        continue
-                    c, r = host.kvh_run_blocks(chunk, splits, n), host.kvh_runs(chunk, splits, n)
-                    assert 1 <= r <= splits and c >= 1
-                    assert (r - 1) * c < max(n, 1) <= r * c < 1 << 31
-                    assert n > 0 or r == 1
+                assert join_rows * join_groups >= live and join_rows in (1, 2048 // D)
+                top = min((max_kv + 31) // 32, 1 << 26)
+                if many:
+                    assert 1 <= splits <= 256 and chunk >= 1
+                    assert ws == (items * splits * slot * 4 if splits > 1 else 0)
+                    assert splits == 1 or items < 1 << 24  # the join's grid
+                    for n in (0, 1, 2, 31, 32, 33, 64, 1000, top, min(3 * top, 1 << 26), 1 << 26):
+                        c, k = host.kvh_run_blocks(chunk, splits, n), host.kvh_runs(chunk, splits, n)
+                        assert 1 <= k <= splits and c >= 1
+                        assert (k - 1) * c < max(n, 1) <= k * c < 1 << 31
+                        assert n > 0 or k == 1
+                    continue
+                assert splits == 1 and slots < 1 << 23
+                assert ws == (slots * slot * 4 if slots > items else 0)
+                for kind in range(4):
+                    n = np.minimum(np.maximum(0, [np.full(batch, top), np.full(batch, 3 * top),
+                                                  (top ** r.random(batch)).astype(np.int64),
+                                                  np.where(np.arange(batch) == 0, 1 << 26, r.integers(0, 3, batch))][kind]), 1 << 26)
+                    c = host.kvh_chunk(int(n.sum()) * Hkv, int(n.max()))
+                    runs = np.maximum(1, -(-n // c))
+                    assert runs.sum() * Hkv <= slots and (slots == items or runs.max() <= 256)
+                    assert [host.kvh_item_runs(c, int(x)) for x in n[:20]] == runs[:20].tolist()
+                    assert c <= 1 << 26 and int(runs.max()) * c < 1 << 31
 
 
 # ---------------------------------------------------------------- refusals
