@@ -151,7 +151,8 @@ typedef struct {
  * as two binary16 numbers (22 bits), with a binary16 out as one.
  * Reported by kvc_check: a page id outside the cache (its tokens count as not
  * seen), a length that is negative or does not fit the table (clamped), a
- * sequence with more than max_q queries or rows past T (those rows are left).
+ * sequence with more than max_q queries, rows past T or a negative number of
+ * them (its rows are left; where q_start descends, others' may be too).
  * The order of summation depends on the shapes and lengths alone: equal calls
  * give equal bits. workspace: at least kvc_attend_workspace bytes, 16-byte aligned (NULL
  * if that is 0); its contents before and after mean nothing. */

@@ -241,6 +241,52 @@ __device__ inline Runs find_runs(const KvAttendArgs& a, int64_t run, int b, int 
   return {chunk, -1, 0};
 }
 
+// Many rows: the tile (sequence, tile of its rows) that is k-th of the call's,
+// the last ones of all sequences first: those see the most keys. Every wave
+// works it out for itself, from tiles that each lane holds of up to eight
+// sequences. With more sequences than that, tiles that no sequence has are
+// counted too. b < 0: none.
+struct Tile {
+  int b, tile;
+};
+__device__ inline Tile find_tile(const KvAttendArgs& a, int k, int lane, bool tell) {
+  if (a.batch == 1 || a.batch > kKvMaxBatch) return {k % a.batch, a.plan.tiles - 1 - k / a.batch};
+  constexpr int N = kKvMaxBatch / 64;
+  const int G = a.L.Hq / a.L.Hkv;
+  int tiles[N];
+#pragma unroll
+  for (int g = 0; g < N; ++g) {
+    tiles[g] = 0;
+    if (64 * g < a.batch && 64 * g + lane < a.batch)
+      tiles[g] = (int)(((int64_t)sequence<true>(a, 64 * g + lane, tell).n * G + a.plan.rows - 1) / a.plan.rows);
+  }
+  auto from = [&](int t) {  // tiles of number t and later ones
+    int n = 0;
+#pragma unroll
+    for (int g = 0; g < N; ++g) n += tiles[g] > t ? tiles[g] - t : 0;
+    return __builtin_amdgcn_readlane(sum_up_to(n), 63);
+  };
+  if (from(0) <= k) return {-1, 0};
+  int lo = 0, hi = a.plan.tiles;  // from(lo) > k >= from(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (from(mid) > k) lo = mid;
+    else hi = mid;
+  }
+  int rank = k - from(hi);
+#pragma unroll
+  for (int g = 0; g < N; ++g) {
+    const uint64_t has = __ballot(tiles[g] > lo);
+    const int n = __builtin_popcountll(has);
+    if (rank < n) {
+      const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(has >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)has, 0));
+      return {64 * g + (int)__builtin_ctzll(__ballot(tiles[g] > lo && before == rank)), lo};
+    }
+    rank -= n;
+  }
+  return {-1, 0};  // not reached
+}
+
 // Page id of block j of a sequence with `end` blocks to take, one at least (past them: some page id).
 __device__ inline int page_of(const KvAttendArgs& a, int b, int j, int end) {
   return scalar_load(a.table, (int64_t)b * a.table_stride + ((j < end ? j : end - 1) >> (a.L.page_shift - 5)));
@@ -581,11 +627,9 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
 // turns a tile of 256 / D blocks into binary16 operands in LDS,
 // each thread one 16-byte piece of the keys and one of the values, while the
 // waves multiply the tile before it; one barrier a tile.
-constexpr int kManyThreads = 256;
-
-template <int D, bool F32>
-__global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_kernel(KvAttendArgs a) {
-  constexpr int KB = 256 / D;      // blocks of a tile
+template <int D, int W, bool F32>
+__global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel(KvAttendArgs a) {
+  constexpr int KB = W * 64 / D;   // blocks of a tile
   constexpr int KS = D / 16;       // inner steps of the scores
   constexpr int MT = D / 32;       // channel tiles of the output
   constexpr int RN = D / 32;       // 16-byte pieces of a key row
@@ -599,14 +643,17 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
   const int G = a.L.Hq / a.L.Hkv;
   // Heads innermost: workgroups of one head go to one XCD and share its cache;
   // later tiles, which see more keys, first.
-  const int item = blockIdx.x, run = blockIdx.y;
-  const int h = item % a.L.Hkv, rest = item / a.L.Hkv;
-  const int b = rest % a.batch, tile = a.plan.tiles - 1 - rest / a.batch;
-  const Sequence seq = sequence(a, b, run == 0 && h == 0 && tile == 0 && tid == 0);
+  const int item = blockIdx.x, run = a.plan.splits - 1 - blockIdx.y;
+  const int h = item % a.L.Hkv;
+  const bool tells = run == 0 && h == 0 && wave == 0;
+  const Tile at = find_tile(a, item / a.L.Hkv, lane, tells && item == 0);
+  const int b = at.b, tile = at.tile;
+  if (b < 0) return;
+  const Sequence seq = sequence(a, b, (a.batch == 1 || a.batch > kKvMaxBatch) && tells && tile == 0 && lane == 0);
   const int rows = seq.n * G;
-  const int r0 = tile * 128;
+  const int r0 = tile * (32 * W);
   if (r0 >= rows) return;
-  const int r_last = (r0 + 127 < rows ? r0 + 127 : rows - 1);
+  const int r_last = (r0 + 32 * W - 1 < rows ? r0 + 32 * W - 1 : rows - 1);
   const int nblk = (seq.seen(r_last / G) + 31) >> 5;
   const int runs = kv_runs(a.plan.chunk, a.plan.splits, nblk);
   if (run >= runs) return;
@@ -666,8 +713,8 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
     const int j = jt + pb;
     half2v ks = kpr, vs[4], vb[4];
     // Nothing may come of tokens behind the sequence's end or without a page.
-    const bool kok = have && j * 32 + ktok < seq.len;
-    if (!kok) {
+    const bool part = !have || 32 * j + 32 > seq.len;  // the same in all lanes
+    if (part && !(have && j * 32 + ktok < seq.len)) {
       ks = half2v{(_Float16)0.f, (_Float16)0.f};
       kr = uint4v{0, 0, 0, 0};
     }
@@ -681,11 +728,13 @@ __global__ __launch_bounds__(kManyThreads, D > 128 ? 1 : 2) void kv_attend_many_
     for (int i = 0; i < 4; ++i) {
       vs[i] = halves(vsr[i]);
       vb[i] = halves(vbr[i]);
+    }
+    if (part) {
+      int left = have ? seq.len - (j * 32 + vq * 4) : 0;
+      asm volatile("" : "+v"(left));  // keeps the comparisons in this branch
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int e = 2 * i + x;
-        if (!have || j * 32 + (e >> 2) * 16 + vq * 4 + (e & 3) >= seq.len) vs[i][x] = vb[i][x] = (_Float16)0.f;
-      }
+      for (int e = 0; e < 8; ++e)
+        if ((e >> 2) * 16 + (e & 3) >= left) vs[e >> 1][e & 1] = vb[e >> 1][e & 1] = (_Float16)0.f;
     }
     const half8v v[4] = {value_operand<0>(bits, vr, vs, vb), value_operand<1>(bits, vr, vs, vb), value_operand<2>(bits, vr, vs, vb),
                          value_operand<3>(bits, vr, vs, vb)};
@@ -843,12 +892,14 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendAr
   const int rpi = a.plan.rows, RW = a.plan.join_rows;
   const int item = blockIdx.x, l0 = blockIdx.y * RW;
   const int G = a.L.Hq / a.L.Hkv;
+  const int lane = threadIdx.x & 63;
   int b, h, r0 = 0;
   if (a.plan.many) {
     h = item % a.L.Hkv;
-    const int rest = item / a.L.Hkv;
-    b = rest % a.batch;
-    r0 = (a.plan.tiles - 1 - rest / a.batch) * rpi;
+    const Tile at = find_tile(a, item / a.L.Hkv, lane, false);
+    if (at.b < 0) return;
+    b = at.b;
+    r0 = at.tile * rpi;
   } else {
     b = item / a.L.Hkv;
     h = item - b * a.L.Hkv;
@@ -856,7 +907,6 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendAr
   const Sequence seq = sequence(a, b, false);
   const int rows = seq.n * G;
   if (r0 + l0 >= rows) return;
-  const int lane = threadIdx.x & 63;
   int runs;
   int64_t slot, step = 1;  // of the first partial, and to the next
   if (a.plan.many) {
@@ -928,13 +978,17 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendAr
 
 template <int D, bool F32>
 hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.plan.many ? a.plan.items : a.plan.slots), (unsigned)a.plan.splits);
-  if (a.plan.many) hipLaunchKernelGGL((kv_attend_many_kernel<D, F32>), grid, dim3(kManyThreads), 0, s, a);
-  else if (a.plan.rows == 16) hipLaunchKernelGGL((kv_attend_few_kernel<D, 1, F32>), grid, dim3(kWaves * 64), 0, s, a);
+  const int64_t items = a.plan.many ? kv_many_items(a.plan, a.L, a.batch, a.tokens) : a.plan.items;
+  const dim3 grid((unsigned)(a.plan.many ? items : a.plan.slots), (unsigned)a.plan.splits);
+  if (a.plan.many && a.plan.rows == 128) {
+    hipLaunchKernelGGL((kv_attend_many_kernel<D, 4, F32>), grid, dim3(256), 0, s, a);
+  } else if (a.plan.many) {
+    if constexpr (D == 128) hipLaunchKernelGGL((kv_attend_many_kernel<D, 8, F32>), grid, dim3(512), 0, s, a);
+  } else if (a.plan.rows == 16) hipLaunchKernelGGL((kv_attend_few_kernel<D, 1, F32>), grid, dim3(kWaves * 64), 0, s, a);
   else if constexpr (D <= 128)
     hipLaunchKernelGGL((kv_attend_few_kernel<D, 2, F32>), grid, dim3(kWaves * 64), 0, s, a);
   if (a.plan.ws_bytes > 0)
-    hipLaunchKernelGGL((kv_attend_join_kernel<D, F32>), dim3((unsigned)a.plan.items, (unsigned)a.plan.join_groups),
+    hipLaunchKernelGGL((kv_attend_join_kernel<D, F32>), dim3((unsigned)items, (unsigned)a.plan.join_groups),
                        dim3(kJoinThreads), 0, s, a);
   return hipGetLastError();
 }

@@ -100,9 +100,11 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
   p.splits = 1;
   p.slots = p.items;
   if (p.many) {
-    const int64_t places = (int64_t)num_cus * 4;
+    // A run's partial costs a round through memory, and joins a launch: longer
+    // runs where there are items enough for every CU.
+    const int64_t places = (int64_t)num_cus * 4, least = p.items >= num_cus ? 128 : 16;
     int64_t chunk = (p.items * nblk + places - 1) / places;
-    if (chunk < 32) chunk = 32;
+    if (chunk < least) chunk = least;
     int64_t splits = (nblk + chunk - 1) / chunk;
     if (splits > kKvMaxSplits) {
       splits = kKvMaxSplits;
@@ -128,6 +130,27 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
     p.ws_bytes = p.slots * p.slot_floats * 4;
   }
   return p;
+}
+
+// Many rows: items that a call with `tokens` rows of q can have.
+inline int64_t kv_many_items(const KvPlan& p, const KvLayout& L, int64_t batch, int64_t tokens) {
+  if (batch == 1 || batch > kKvMaxBatch) return p.items;
+  const int64_t items = (tokens * (L.Hq / L.Hkv) / p.rows + batch) * L.Hkv;
+  return items < p.items ? items : p.items;
+}
+
+// Many rows, nothing to join: tiles of 256 rows (kv_attend.hip says why) where
+// the rows still make four items a CU, of 64 blocks or more at the longest. 2 x
+// 2048 queries on 8192 tokens (64 heads, 8 kv heads): 1105 us, in 128 rows 1191;
+// 4 x 4096 (32, 8): 696, 728; but 1 x 4096: 248, 207, and 64 x 256: 169, 123.
+inline void kv_many_wide(KvPlan& p, const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int64_t tokens,
+                         int num_cus) {
+  if (!p.many || p.splits > 1 || L.D != 128 || max_kv < 64 * 32) return;
+  KvPlan w = p;
+  w.rows = 256;
+  w.tiles = (int32_t)((max_q * (L.Hq / L.Hkv) + 255) / 256);
+  w.items = batch * L.Hkv * w.tiles;
+  if (kv_many_items(w, L, batch, tokens) >= 4 * num_cus) p = w;
 }
 
 }  // namespace agemm

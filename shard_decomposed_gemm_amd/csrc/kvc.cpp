@@ -191,6 +191,7 @@ int kvc_attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, void* 
   a.scale = p->scale;
   a.out = p->out;
   a.lse = p->lse;
+  kv_many_wide(plan, ctx->L, p->batch, p->max_q, p->max_kv, p->tokens, ctx->num_cus);
   a.plan = plan;
   a.ws = static_cast<float*>(workspace);
   a.err = ctx->err_dev;

@@ -50,6 +50,16 @@ void kvh_plan(int Hq, int Hkv, int D, int page_tokens, int64_t num_pages, int64_
                          p.slots, p.slot_floats, p.ws_bytes};
   for (int i = 0; i < 11; ++i) out[i] = v[i];
 }
+// Items of the launch of the plan that kvh_plan made last, widened if it can be; its rows and tiles.
+int64_t kvh_many_items(int Hq, int Hkv, int D, int64_t batch, int64_t max_q, int64_t max_kv,
+                       int64_t tokens, int num_cus, int64_t* rows, int64_t* tiles) {
+  KvPlan p = plan_of;
+  const KvLayout L = kv_layout(Hq, Hkv, D, 64, 1000);
+  kv_many_wide(p, L, batch, max_q, max_kv, tokens, num_cus);
+  *rows = p.rows;
+  *tiles = p.tiles;
+  return kv_many_items(p, L, batch, tokens);
+}
 // Blocks of a run in the plan that kvh_plan made last.
 int kvh_chunk(int64_t U, int longest) { return kv_chunk(plan_of, U, longest); }
 int kvh_item_runs(int chunk, int nblk) { return kv_item_runs(chunk, nblk); }

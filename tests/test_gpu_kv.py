@@ -400,8 +400,18 @@ LONG = [
 ]
 
 
+BATCHES = [  # many rows, the same columns: tiles of more than one group of 64 sequences, none of some, and 256-row tiles
+    (4, 1, 64, 32, [(i * 37 % 71, i * 37 % 71 + i % 5) for i in range(130)], None, None),
+    (2, 2, 128, 32, [(70 if i == 300 else i % 2, 80 if i == 300 else i % 40) for i in range(512)], None, None),
+    (1, 1, 64, 32, [(90 if i in (3, 519) else i % 2, 95 if i in (3, 519) else i % 40) for i in range(520)], None, None),
+    (8, 2, 128, 32, [({300: 333, 77: 90}.get(i, i % 3), {300: 350, 77: 60}.get(i, i % 40)) for i in range(512)], None, 4096),
+    (8, 2, 128, 64, [({3: 200, 511: 130}.get(i, 0), 260 - i % 2) for i in range(512)],
+     [-30 if i == 3 else 200 for i in range(512)], 2048),
+]
+
+
 @pytest.mark.parametrize("f32", [True, False])
-@pytest.mark.parametrize("Hq,Hkv,D,page,shape,q_off,max_kv", LONG)
+@pytest.mark.parametrize("Hq,Hkv,D,page,shape,q_off,max_kv", LONG + BATCHES)
 def test_attend_joins_runs(Hq, Hkv, D, page, shape, q_off, max_kv, f32):
     print(f"[kv runs] {Hq} {Hkv} {D} {page} {shape[:4]} {len(shape)} {q_off} {max_kv} {f32}", flush=True)
     lens = [n for _, n in shape]

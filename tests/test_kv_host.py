@@ -40,6 +40,8 @@ def host(tmp_path_factory):
     lib.kvh_plan.argtypes = shape + [i64, i64, i64, ctypes.c_int, ctypes.POINTER(i64)]
     lib.kvh_plan.restype = None
     lib.kvh_chunk.argtypes = [i64, ctypes.c_int]
+    lib.kvh_many_items.argtypes = [ctypes.c_int] * 3 + [i64] * 4 + [ctypes.c_int] + [ctypes.POINTER(i64)] * 2
+    lib.kvh_many_items.restype = i64
     return lib
 
 
@@ -180,6 +182,16 @@ def test_plan_covers_every_block_once_within_its_workspace(host, Hq, Hkv, D):
                         assert 1 <= k <= splits and c >= 1
                         assert (k - 1) * c < max(n, 1) <= k * c < 1 << 31
                         assert n > 0 or k == 1
+                    for T in (max_q, 1, batch * max_q, batch + max_q):
+                        wide, wtiles = ctypes.c_int64(), ctypes.c_int64()
+                        grid = host.kvh_many_items(Hq, Hkv, D, batch, max_q, max_kv, T, 256, wide, wtiles)
+                        wide, wtiles = wide.value, wtiles.value
+                        assert wide == rows or (wide == 256 and splits == 1 and grid >= 1024)
+                        assert wide * wtiles >= max_q * (Hq // Hkv) and 0 < grid <= batch * wtiles * Hkv
+                        # T rows cut into sequences of max_q at most, in whatever way
+                        cuts = np.sort(r.integers(0, T + 1, batch - 1)) if batch > 1 else np.empty(0, np.int64)
+                        n = np.minimum(np.diff(np.concatenate([[0], cuts, [T]])), max_q)
+                        assert (-(-n * (Hq // Hkv) // wide)).sum() * Hkv <= grid
                     continue
                 assert splits == 1 and slots < 1 << 23
                 assert ws == (slots * slot * 4 if slots > items else 0)
