@@ -5,15 +5,17 @@
 // A head row of D channels is the work of 16 lanes, D / 16 consecutive
 // channels each, so that a lane's channels are exactly one run of the key
 // row's nibbles and one value run c of the block layout, and no nibble changes
-// lanes. A workgroup of 256 threads takes 16 rows of one token at a time:
-// query rows are normed, rotated and written as binary16; key rows are
-// normed, rotated and quantised; value rows are quantised. The rotation's
-// partner of channel i, i +- rope_dims / 2, is in the lane rope_dims / 2
-// channels away. Sums and extremes over a row are four steps within a row of
-// 16 lanes (DPP rotations).
+// lanes. A wave takes four rows of one token at a time: query rows are normed,
+// rotated and written as binary16; key rows are normed, rotated and quantised;
+// value rows are quantised. The rotation's partner of channel i, i +-
+// rope_dims / 2, is in the lane rope_dims / 2 channels away. Sums and extremes
+// over a row are four steps within a row of 16 lanes (DPP rotations).
 //
 // Bound by HBM: 2 bytes in and out a query channel, 2 in and 1/2 out a key or
-// value channel, some 10 operations each.
+// value channel, some 10 operations each. Measured on 16384 tokens of 64 + 2 x 8
+// heads (D 128, whole rotation): queries 112 us, 4.8 TB/s of the 4.96 that a
+// copy reaches; keys and values 52 us, 1.8 TB/s (their arithmetic: some 40
+// operations a channel, and one quad in eight again in binary64).
 #include <type_traits>
 
 #include "kv_internal.h"
@@ -365,7 +367,8 @@ __global__ __launch_bounds__(kThreads, ROLE == kQueries ? (E > 8 ? 4 : 6) : E > 
   }
 }
 
-// One row of 16 lanes per (token, kv head).
+// One row of 16 lanes per (token, kv head). HBM-bound: 16384 tokens of 8 kv
+// heads (D 128) in 17.4 us, 4.9 TB/s of bytes in and out.
 template <int E>
 __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a) {
   using H = Halves<E>;
