@@ -137,7 +137,7 @@ typedef struct {
   int64_t max_kv;              /* the longest kv_len to expect, >= 1: it only chooses how work is split */
   float scale;                 /* factor of q . k, finite */
   int32_t out_f32;             /* out is binary32 (1) or binary16 (0) */
-  void* out;                   /* T x Hq x D, contiguous */
+  void* out;                   /* T x Hq x D, contiguous, apart from q */
   float* lse;                  /* T x Hq, contiguous, or NULL */
 } kvc_attend_args;
 
@@ -147,7 +147,7 @@ typedef struct {
  *   lse = ln sum_j e^(S_j).
  * A row that sees no token: out = 0 and lse = -FLT_MAX, which the combine
  * takes as a partial without weight. Rows of q past the last sequence's are
- * left as they were in out and lse. Sums, maxima and statistics in binary32;
+ * left as they were in out and lse. Scores must fit binary32. Sums, maxima and statistics in binary32;
  * with a binary32 out the softmax weights enter the product with the values
  * as two binary16 numbers (22 bits), with a binary16 out as one.
  * Reported by kvc_check: a page id outside the cache (its tokens count as not

@@ -211,7 +211,7 @@ __global__ __launch_bounds__(kThreads, ROLE == kQueries ? (E > 8 ? 4 : 6) : E > 
   const bool is_q = ROLE == kBoth ? blockIdx.y == 0 : ROLE == kQueries;
   const int heads = is_q ? a.L.Hq : a.L.Hkv;
   const uint32_t per_head4 = (uint32_t)(heads + 3) >> 2, quads = is_q ? per_head4 : 2 * per_head4;
-  const uint32_t all = (uint32_t)a.tokens * quads;  // at most 2^28
+  const uint32_t all = (uint32_t)a.tokens * quads;  // below 2^28
   // Workgroups go to the 8 XCDs in turn: those of the 32 tokens of a block,
   // whose values share lines, go to one, so that its L2 puts the lines
   // together. The last ones, short of 8 blocks, go as they come.
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a) {
   const int64_t slot = a.slots[t];
   if (slot < 0) return;
   if (slot >= (a.L.num_pages << a.L.page_shift)) {
-    if (lane == 0 && h == 0) kv_report(a.err, kKvSlot, t, slot, a.L.num_pages << a.L.page_shift);
+    if (lane == 0 && h == 0) kv_report(a.err, kKvSlot, a.first + t, slot, a.L.num_pages << a.L.page_shift);
     return;
   }
   const int off = (int)(slot & (a.L.page_tokens - 1));

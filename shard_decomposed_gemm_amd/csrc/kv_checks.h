@@ -17,8 +17,8 @@ namespace agemm {
 constexpr size_t kKvWhy = 256;  // bytes of a reason
 constexpr int kKvNothing = -1;  // nothing to refuse and nothing to do
 
-constexpr int64_t kKvMaxTokens = int64_t{1} << 23;  // rows of one call: grids stay below 2^32 threads
-constexpr int64_t kKvMaxItems = (int64_t{1} << 23) - 1;  // of an attention call, for the same reason
+constexpr int64_t kKvMaxTokens = int64_t{1} << 23;  // rows of one call
+constexpr int64_t kKvMaxItems = (int64_t{1} << 23) - 1;  // of an attention call: grids stay below 2^32 threads
 constexpr int64_t kKvMaxStride = int64_t{1} << 40;
 
 inline int kv_refuse(char* why, int code, const char* fmt, ...) __attribute__((format(printf, 3, 4)));

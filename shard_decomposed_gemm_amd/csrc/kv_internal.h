@@ -45,6 +45,7 @@ struct KvReadArgs {
   int64_t tokens;
   const int64_t* slots;
   _Float16 *k_out, *v_out;
+  int64_t first;  // number of the call's token that is token 0 here
   ErrWord* err;
 };
 

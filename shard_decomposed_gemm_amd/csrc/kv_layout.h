@@ -30,6 +30,14 @@ KV_HD inline int64_t kv_block_at(const KvLayout& L, int64_t page, int h, int i) 
 KV_HD inline int kv_value_quarter(int t) { return (t >> 2) & 3; }
 KV_HD inline int kv_value_place(int t) { return ((t >> 4) << 2) | (t & 3); }
 
+// Tokens of one launch of the append and of the read: grids stay below 2^32
+// threads, and the append's quads of rows below 2^28.
+inline int64_t kv_append_piece(const KvLayout& L) {
+  const int64_t quads = (L.Hq + 3) / 4 > (L.Hkv + 3) / 4 * 2 ? (L.Hq + 3) / 4 : (L.Hkv + 3) / 4 * 2;
+  return ((int64_t{1} << 28) - 64) / quads;
+}
+inline int64_t kv_read_piece(const KvLayout& L) { return ((int64_t{1} << 28) - 64) / L.Hkv; }
+
 // How one attention call's work is laid out. Rows of a kv head's item are its
 // query heads of all queries, r = query * G + head.
 //

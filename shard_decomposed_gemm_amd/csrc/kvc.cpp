@@ -139,8 +139,7 @@ int kvc_append(kvc_ctx* ctx, void* pages, const kvc_append_args* p, void* stream
   a.err = ctx->err_dev;
   OnDevice on(ctx->device);
   if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");
-  // The kernels count quads of rows in 32 bits, at most 512 a token: one launch up to 2^19 tokens.
-  const int64_t piece = int64_t{1} << 19;
+  const int64_t piece = kv_append_piece(L);
   for (a.first = 0; a.first < p->tokens; a.first += piece) {
     KvAppendArgs c = a;
     c.tokens = p->tokens - a.first < piece ? p->tokens - a.first : piece;
@@ -211,15 +210,19 @@ int kvc_read(kvc_ctx* ctx, const void* pages, int64_t tokens, const int64_t* slo
   KvReadArgs a{};
   a.L = ctx->L;
   a.pages = static_cast<const char*>(pages);
-  a.tokens = tokens;
-  a.slots = slots;
-  a.k_out = static_cast<_Float16*>(k_out);
-  a.v_out = static_cast<_Float16*>(v_out);
   a.err = ctx->err_dev;
   OnDevice on(ctx->device);
   if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");
-  const hipError_t e = launch_kv_read(a, static_cast<hipStream_t>(stream));
-  return e == hipSuccess ? AGEMM_OK : hip_fail(ctx, e, "read launch");
+  const int64_t piece = kv_read_piece(ctx->L), row = (int64_t)ctx->L.Hkv * ctx->L.D;
+  for (a.first = 0; a.first < tokens; a.first += piece) {
+    a.tokens = tokens - a.first < piece ? tokens - a.first : piece;
+    a.slots = slots + a.first;
+    a.k_out = static_cast<_Float16*>(k_out) + a.first * row;
+    a.v_out = static_cast<_Float16*>(v_out) + a.first * row;
+    const hipError_t e = launch_kv_read(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(ctx, e, "read launch");
+  }
+  return AGEMM_OK;
 }
 
 int kvc_check(kvc_ctx* ctx) {

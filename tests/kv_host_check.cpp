@@ -66,4 +66,9 @@ int kvh_item_runs(int chunk, int nblk) { return kv_item_runs(chunk, nblk); }
 int kvh_run_blocks(int chunk, int splits, int nblk) { return kv_run_blocks(chunk, splits, nblk); }
 int kvh_runs(int chunk, int splits, int nblk) { return kv_runs(chunk, splits, nblk); }
 
+int64_t kvh_piece(int Hq, int Hkv, int D, int read) {
+  const KvLayout L = kv_layout(Hq, Hkv, D, 64, 1000);
+  return read ? kv_read_piece(L) : kv_append_piece(L);
+}
+
 }  // extern "C"

@@ -206,6 +206,17 @@ def test_plan_covers_every_block_once_within_its_workspace(host, Hq, Hkv, D):
                     assert c <= 1 << 26 and int(runs.max()) * c < 1 << 31
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (64, 8), (96, 96), (1024, 1), (1024, 1024), (1023, 1023), (5, 5)])
+def test_launches_of_append_and_read_stay_within_32_bits(host, Hq, Hkv):
+    host.kvh_piece.restype = ctypes.c_int64
+    for D in (64, 128, 256):
+        quads = max(-(-Hq // 4), 2 * -(-Hkv // 4))
+        rows = host.kvh_piece(Hq, Hkv, D, 0) * quads
+        # four quads a wave, four waves a workgroup of 256 threads; the read: 16 threads a row
+        assert 0 < rows < 1 << 28 and -(-rows // 16) * 256 < 1 << 32
+        assert 0 < -(-host.kvh_piece(Hq, Hkv, D, 1) * Hkv // 16) * 256 < 1 << 32
+
+
 # ---------------------------------------------------------------- refusals
 
 SHAPE = (16, 4, 128, 64, 10)
