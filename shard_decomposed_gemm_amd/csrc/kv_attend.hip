@@ -199,46 +199,59 @@ __device__ inline int largest_up_to(int x) {
   return x;
 }
 
+// The sequence that lane l holds, in all lanes.
+__device__ inline Sequence of_lane(const Sequence& s, int l) {
+  auto wide = [&](int64_t x) {
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), l) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane((int)x, l));
+  };
+  Sequence r;
+  r.row0 = wide(s.row0);
+  r.n = __builtin_amdgcn_readlane(s.n, l);
+  r.len = __builtin_amdgcn_readlane(s.len, l);
+  r.off = wide(s.off);
+  return r;
+}
+
 // Few rows: the runs of a call, from its lengths. Every wave works them out
 // for itself, 64 sequences at a time (kKvMaxBatch bounds them).
 struct Runs {
   int chunk;     // blocks of a run
   int b;         // the sequence found, -1: none
   int64_t slot;  // its first run
+  Sequence seq;
 };
 // The sequence with run `run`, or (run < 0) sequence b. Blocks of a head and
 // runs of a head each sum up to at most 2^31 (the host sees to that).
 __device__ inline Runs find_runs(const KvAttendArgs& a, int64_t run, int b, int lane, bool tell) {
-  auto blocks = [&](int b0, bool& some, bool report) {
+  auto load = [&](int b0, bool report) {
     Sequence s{};
     if (b0 + lane < a.batch) s = sequence<true>(a, b0 + lane, report);
-    some = s.n > 0;
-    return s.blocks();
+    return s;
   };
-  bool some;
-  const int first = blocks(0, some, tell);
+  const Sequence group0 = load(0, tell);
+  const int first = group0.blocks();
   int all = __builtin_amdgcn_readlane(sum_up_to(first), 63), longest = __builtin_amdgcn_readlane(largest_up_to(first), 63);
-  bool other;
   for (int b0 = 64; b0 < a.batch; b0 += 64) {
-    const int x = blocks(b0, other, tell), top = __builtin_amdgcn_readlane(largest_up_to(x), 63);
+    const int x = load(b0, tell).blocks(), top = __builtin_amdgcn_readlane(largest_up_to(x), 63);
     all += __builtin_amdgcn_readlane(sum_up_to(x), 63);
     longest = longest > top ? longest : top;
   }
   const int chunk = kv_chunk(a.plan, (int64_t)all * a.L.Hkv, longest);
   int before = 0;  // runs of a head before this group of sequences
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    const int nblk = b0 == 0 ? first : blocks(b0, some, false);
-    const int mine = some ? kv_item_runs(chunk, nblk) : 0;
+    const Sequence s = b0 == 0 ? group0 : load(b0, false);
+    const int mine = s.n > 0 ? kv_item_runs(chunk, s.blocks()) : 0;
     const int upto = before + sum_up_to(mine);
     const uint64_t at = run < 0 ? (b - b0 < 64 ? uint64_t{1} << (b - b0) : 0) : __ballot((int64_t)upto * a.L.Hkv > run);
     if (at) {
       const int l = __builtin_ctzll(at);
-      return {chunk, b0 + l,
-              (int64_t)(__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l)) * a.L.Hkv};
+      return {chunk, b0 + l, (int64_t)(__builtin_amdgcn_readlane(upto, l) - __builtin_amdgcn_readlane(mine, l)) * a.L.Hkv,
+              of_lane(s, l)};
     }
     before = __builtin_amdgcn_readlane(upto, 63);
   }
-  return {chunk, -1, 0};
+  return {chunk, -1, 0, Sequence{}};
 }
 
 // Many rows: the tile (sequence, tile of its rows) that is k-th of the call's,
@@ -429,7 +442,7 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
       if (runs.b < 0) return;
       b = runs.b;
       chunk = runs.chunk;
-      seq = sequence(a, b, false);
+      seq = runs.seq;
       h = (int)(slot_id - runs.slot);
     }
     run = h / a.L.Hkv;
@@ -915,34 +928,40 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendAr
   const int item = blockIdx.x, l0 = blockIdx.y * RW;
   const int G = a.L.Hq / a.L.Hkv;
   const int lane = threadIdx.x & 63;
-  int b, h, r0 = 0;
+  int b = 0, h, r0 = 0, runs;
+  int64_t slot, step = 1;  // of the first partial, and to the next
+  Sequence seq;
   if (a.plan.many) {
     h = item % a.L.Hkv;
     const Tile at = find_tile(a, item / a.L.Hkv, lane, false);
     if (at.b < 0) return;
     b = at.b;
+    seq = sequence(a, b, false);
     r0 = at.tile * rpi;
-  } else {
-    b = item / a.L.Hkv;
-    h = item - b * a.L.Hkv;
-  }
-  const Sequence seq = sequence(a, b, false);
-  const int rows = seq.n * G;
-  if (r0 + l0 >= rows) return;
-  int runs;
-  int64_t slot, step = 1;  // of the first partial, and to the next
-  if (a.plan.many) {
+    const int rows = seq.n * G;
+    if (r0 >= rows) return;
     const int r_last = r0 + rpi - 1 < rows ? r0 + rpi - 1 : rows - 1;
     runs = kv_runs(a.plan.chunk, a.plan.splits, (seq.seen(r_last / G) + 31) >> 5);
     slot = (int64_t)item * a.plan.splits;
   } else {
-    Runs r = {0, 0, 0};
-    if (a.batch == 1) r.chunk = kv_chunk(a.plan, (int64_t)seq.blocks() * a.L.Hkv, seq.blocks());
-    else r = find_runs(a, -1, b, lane, false);
-    runs = kv_item_runs(r.chunk, seq.blocks());
-    slot = r.slot + h;
+    b = item / a.L.Hkv;
+    h = item - b * a.L.Hkv;
+    slot = h;
+    int chunk;
+    if (a.batch == 1) {
+      seq = sequence(a, 0, false);
+      chunk = kv_chunk(a.plan, (int64_t)seq.blocks() * a.L.Hkv, seq.blocks());
+    } else {
+      const Runs r = find_runs(a, -1, b, lane, false);
+      seq = r.seq;
+      chunk = r.chunk;
+      slot += r.slot;
+    }
+    runs = kv_item_runs(chunk, seq.blocks());
     step = a.L.Hkv;
   }
+  const int rows = seq.n * G;
+  if (r0 + l0 >= rows) return;
   if (runs == 1) return;  // written by its only run
   const int R = rows - r0 - l0 < RW ? rows - r0 - l0 : RW;
 
