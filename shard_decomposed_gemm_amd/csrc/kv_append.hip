@@ -14,8 +14,8 @@
 // Bound by HBM: 2 bytes in and out a query channel, 2 in and 1/2 out a key or
 // value channel, some 10 operations each. Measured on 16384 tokens of 64 + 2 x 8
 // heads (D 128, whole rotation): queries 112 us, 4.8 TB/s of the 4.96 that a
-// copy reaches; keys and values 52 us, 1.8 TB/s (their arithmetic: some 40
-// operations a channel, and one quad in eight again in binary64).
+// copy reaches; keys and values 51 us, 1.8 TB/s (their arithmetic: some 40
+// operations a channel, and one quad in ten again in binary64).
 #include <type_traits>
 
 #include "kv_internal.h"
@@ -112,7 +112,7 @@ __device__ inline _Float16 half_by_float(double x) {
 
 // The row's 4-bit form, 16-bit words of this lane's nibbles and the pair (s, b),
 // in binary32; false where that cannot be told apart from what binary64 gives
-// (some 13 % of the quads of rows: of values for ties, which binary16 inputs
+// (some tenth of the quads of rows: of values for ties, which binary16 inputs
 // often are).
 // x is known to `off` times the row's largest size: s, b and (x - b) / s are
 // recomputed at both ends of what their errors allow, or kept away from ties.
@@ -152,9 +152,8 @@ __device__ inline bool quantise_fast(const float (&x)[E], float off, uint32_t (&
   return sure;
 }
 
-// The same in binary64, where a
-// nibble next to the border between two is decided as the definition
-// says, ties of (x - b) / s to even. x - b and n s are exact for values of
+// The same in binary64, where a nibble next to the border between two is
+// decided as the definition says, ties of (x - b) / s to even. x - b and n s are exact for values of
 // binary16, so the remainder tells a tie where the product with 1 / s cannot.
 template <int E>
 __device__ inline bool quantise(double (&x)[E], uint32_t (&word)[E / 4], _Float16& s, _Float16& b) {
@@ -325,10 +324,11 @@ __global__ __launch_bounds__(kThreads, ROLE == kQueries ? (E > 8 ? 4 : 6) : E > 
     if constexpr (ROLE != kQueries) {
       uint32_t word[E / 4];  // channels 4 i .. 4 i + 3
       _Float16 s, b;
-      // A norm leaves a relative error below 16 x 2^-24 (E + 4 additions, halved by the root, the root, a quotient, two
-      // products), a rotation then at most 2^(1/2) (16 + 2) 2^-24 of the row's largest size after it: 2^-18 covers both.
+      // In units of 2^-24: a norm leaves a relative error below 16 (E + 4 additions, halved by the root, the root, a
+      // quotient, two products); a rotation of (x, y) by (c, s) then one below 16 + 2 of |x c| + |y s|, which is at
+      // most 2^(1/2) times the larger of the two results. 2^-19 covers 18 2^(1/2).
       // For whole rows: their lanes work together.
-      if (__any(!quantise_fast<E>(v, is_k ? 0x1p-18f : 0.f, word, s, b))) {
+      if (__any(!quantise_fast<E>(v, is_k ? 0x1p-19f : 0.f, word, s, b))) {
         double y[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = (double)in.x[e];
