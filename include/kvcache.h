@@ -105,9 +105,8 @@ typedef struct {
 /* For each token: q_out = rope(norm(q)), rounded to binary16 once; the key
  * rope(norm(k)) and the value v go to the token's slot in 4 bits, rounded
  * once. Norm: x_d / sqrt(mean x^2 + eps) * w_d. Rotation of a pair (x, y):
- * (x cos - y sin, y cos + x sin). Sums and products in binary32; what
- * is quantised comes out as if scale, offset and nibbles had been worked out
- * from it in binary64.
+ * (x cos - y sin, y cos + x sin). Sums and products in binary32; what is
+ * quantised comes out as if all of it had been worked out in binary64.
  * A key or value channel outside +-20000 is held as that limit, a NaN as 0,
  * and kvc_check reports it: the cache holds finite numbers only, so a token
  * that a query's mask hides cannot reach its result. A position outside

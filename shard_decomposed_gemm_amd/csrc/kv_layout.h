@@ -97,6 +97,9 @@ KV_HD inline int kv_runs(int chunk, int splits, int nblk) {
 inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
   KvPlan p{};
   const int64_t rows = max_q * (L.Hq / L.Hkv), nblk = (max_kv + 31) / 32;
+  // As many rows as the kernel for few rows holds, it takes: 16 x 4 queries of 64
+  // heads (8 kv heads, D 128) on 8192 tokens 44.5 us, the one for many 82; 16 x 2
+  // of 16 heads (2, D 256) 26, 77.
   p.many = rows > (L.D == 256 ? 16 : 32);
   p.rows = p.many ? 128 : rows > 16 ? 32 : 16;
   p.tiles = (int32_t)(p.many ? (rows + p.rows - 1) / p.rows : 1);
@@ -108,16 +111,22 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
   p.splits = 1;
   p.slots = p.items;
   if (p.many) {
-    // A run's partial costs a round through memory, and joins a launch: longer
-    // runs where there are items enough for every CU.
-    const int64_t places = (int64_t)num_cus * 4, least = p.items >= num_cus ? 128 : 16;
+    // As many runs as run at once, of equal length. A run's partial takes a
+    // round through memory and the join a launch: in short runs only where
+    // items leave CUs idle. In us, 32 heads, 8 kv heads, D 128:
+    //   least run, blocks                     8    16    32   128  whole
+    //   40 queries on 1000 tokens          19.5  25.7  31.8  31.6   31.7
+    //   64 on 4096                         24.7  28.0  39.5   105    105
+    //   4 x 40 on 16384                     106   105   106   131    403
+    //   1777 on themselves (448 items)     74.1  73.7  73.4  59.8   57.6
+    //   1024 on 16384 (256 items)           351   349   345   355    437
+    const int64_t places = (int64_t)num_cus * 2, least = p.items >= num_cus ? 128 : 8;
     int64_t chunk = (p.items * nblk + places - 1) / places;
     if (chunk < least) chunk = least;
     int64_t splits = (nblk + chunk - 1) / chunk;
-    if (splits > kKvMaxSplits) {
-      splits = kKvMaxSplits;
-      chunk = (nblk + splits - 1) / splits;
-    }
+    if (splits > kKvMaxSplits) splits = kKvMaxSplits;
+    if (splits < 1) splits = 1;
+    chunk = (nblk + splits - 1) / splits;
     p.chunk = (int32_t)(chunk < kKvWhole ? chunk : kKvWhole);
     p.splits = (int32_t)splits;
     p.ws_bytes = p.splits > 1 ? p.items * p.splits * p.slot_floats * 4 : 0;
