@@ -659,7 +659,7 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
 // Measured: 2 x 2048 queries of 64 heads (8 kv heads, D 128) on 8192 tokens in
 // 966 to 1070 us (box to box), 962 GFLOP at 0.90 to 1.00 PFLOP/s; a 8192^3
 // library product reaches 1.14 on the same part. Matrix units busy 45 % and
-// vector units 51 % of the cycles, at 1.9 GHz: the part's power holds the clock.
+// vector units 51 % of the cycles, at 1.9 GHz of 2.4: power seems to hold the clock.
 template <int D, int W, bool F32>
 __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel(KvAttendArgs a) {
   constexpr int KB = W * 64 / D;   // blocks of a tile
