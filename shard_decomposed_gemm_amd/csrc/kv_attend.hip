@@ -131,7 +131,7 @@ struct Sequence {
   int len;       // cached tokens
   int64_t off;   // the first query sees off + 1 tokens
 
-  __device__ int blocks() const { return n > 0 ? (seen(n - 1) + 31) >> 5 : 0; }  // that its last query sees
+  __device__ int blocks() const { return n > 0 ? kv_blocks(seen(n - 1)) : 0; }  // that its last query sees
   __device__ int seen(int i) const {
     const int64_t v = off + i + 1;
     return v < 0 ? 0 : v > len ? len : (int)v;
@@ -687,7 +687,7 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
   const int r0 = tile * (32 * W);
   if (r0 >= rows) return;
   const int r_last = (r0 + 32 * W - 1 < rows ? r0 + 32 * W - 1 : rows - 1);
-  const int nblk = (seq.seen(r_last / G) + 31) >> 5;
+  const int nblk = kv_blocks(seq.seen(r_last / G));
   const int runs = kv_runs(a.plan.chunk, a.plan.splits, nblk);
   if (run >= runs) return;
   const int chunk = kv_run_blocks(a.plan.chunk, a.plan.splits, nblk);
@@ -708,7 +708,7 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
   // Wave-uniform: blocks below `whole` are seen whole by every row of the wave, none at or past `none`.
   const int w0 = r0 + wave * 32, w1 = (w0 + 31 < rows ? w0 + 31 : rows - 1);
   const int whole = w0 < rows ? seq.seen(w0 / G) >> 5 : 0;
-  const int none = w0 < rows ? (seq.seen(w1 / G) + 31) >> 5 : 0;
+  const int none = w0 < rows ? kv_blocks(seq.seen(w1 / G)) : 0;
   const float factor = a.scale * kLog2e;
   const Bits bits;
 
@@ -746,7 +746,7 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
     const int j = jt + pb;
     half2v ks = kpr, vs[4], vb[4];
     // Nothing may come of tokens behind the sequence's end or without a page.
-    const bool part = !have || 32 * j + 32 > seq.len;  // the same in all lanes
+    const bool part = !have || seq.len - 32 * j < 32;  // the same in all lanes
     if (part && !(have && j * 32 + ktok < seq.len)) {
       ks = half2v{(_Float16)0.f, (_Float16)0.f};
       kr = uint4v{0, 0, 0, 0};
@@ -941,7 +941,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendAr
     const int rows = seq.n * G;
     if (r0 >= rows) return;
     const int r_last = r0 + rpi - 1 < rows ? r0 + rpi - 1 : rows - 1;
-    runs = kv_runs(a.plan.chunk, a.plan.splits, (seq.seen(r_last / G) + 31) >> 5);
+    runs = kv_runs(a.plan.chunk, a.plan.splits, kv_blocks(seq.seen(r_last / G)));
     slot = (int64_t)item * a.plan.splits;
   } else {
     b = item / a.L.Hkv;

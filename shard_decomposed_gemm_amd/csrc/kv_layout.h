@@ -26,6 +26,8 @@ KV_HD inline int64_t kv_block_bytes(int D) { return 32 * (D + 8); }
 KV_HD inline int64_t kv_block_at(const KvLayout& L, int64_t page, int h, int i) {
   return page * L.page_bytes + ((int64_t)h * (L.page_tokens >> 5) + i) * kv_block_bytes(L.D);
 }
+// Blocks of 32 tokens that n >= 0 tokens take (n + 31 passes 2^31 for the longest lengths).
+KV_HD inline int kv_blocks(int n) { return (int)(((uint32_t)n + 31u) >> 5); }
 // Place of token t of a block among the eight of its quarter (value order).
 KV_HD inline int kv_value_quarter(int t) { return (t >> 2) & 3; }
 KV_HD inline int kv_value_place(int t) { return ((t >> 4) << 2) | (t & 3); }
