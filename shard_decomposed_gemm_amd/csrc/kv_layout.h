@@ -112,6 +112,7 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
   p.slot_floats = (int64_t)p.rows * (L.D + 2);
   p.splits = 1;
   p.slots = p.items;
+  if (p.items == 0) return p;  // an empty batch
   if (p.many) {
     // As many runs as run at once, of equal length. A run's partial takes a
     // round through memory and the join a launch: in short runs only where

@@ -54,3 +54,18 @@ def test_attend_lengths_up_to_the_largest_int32(queries, lens):
             # a run's sums stay below 2^24 tokens; the waves and the at most 256 runs add up with a rounding each
             assert kx.close(got[i * queries + row], lse[i * queries + row], O[None], np.array([n]), True,
                             (8 + 256) * kx.ROUND).all(), (i, row)
+
+
+# ---------------------------------------------------------------- nothing to do
+
+@pytest.mark.parametrize("max_q", [1, 50])
+def test_attend_an_empty_batch_with_long_lengths(max_q):
+    import torch
+    from shard_decomposed_gemm_amd import KvCache
+    kv = KvCache(8, 2, 64, page_tokens=64, num_pages=2)
+    none = lambda *shape, dtype=torch.int32: torch.zeros(*shape, dtype=dtype, device=gu.dev())  # noqa: E731
+    assert kv.workspace(0, max_q, 262144).numel() > 0
+    kv.attend(kv.new_pages(), none(0, 8, 64, dtype=torch.float16), none(0), none(0, 5000), none(0, 8, 64, dtype=torch.float32),
+              q_start=none(1), max_q=max_q)
+    torch.cuda.synchronize()
+    kv.check()
