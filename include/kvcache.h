@@ -155,12 +155,16 @@ typedef struct {
  * sequence with more than max_q queries, rows past T or a negative number of
  * them (its rows are left; where q_start descends, others' may be too).
  * The order of summation depends on the shapes and lengths alone: equal calls
- * give equal bits. workspace: at least kvc_attend_workspace bytes, 16-byte aligned (NULL
- * if that is 0); its contents before and after mean nothing. */
+ * give equal bits. workspace: at least kvc_attend_workspace bytes of bounds that
+ * hold this call's batch, max_q and max_kv, 16-byte aligned (NULL if that is
+ * 0); its contents before and after mean nothing. */
 int kvc_attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* args, void* workspace,
                int64_t workspace_bytes, void* stream);
 
-/* Workspace that a kvc_attend call with these bounds needs (any out type). */
+/* Workspace that holds every kvc_attend call of up to `batch` sequences, max_q
+ * queries and max_kv tokens (any out type): one made for a server's largest
+ * batch, chunk and length serves its smaller calls too, which may need more
+ * than the largest one does. */
 int kvc_attend_workspace(const kvc_ctx* ctx, int32_t batch, int32_t max_q, int64_t max_kv, int64_t* bytes);
 
 /* Copies the keys and values of the tokens in `slots` (T, device) out of the

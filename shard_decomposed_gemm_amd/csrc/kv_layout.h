@@ -152,6 +152,34 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
   return p;
 }
 
+// Workspace bytes that suffice for every call of up to `batch` sequences, max_q
+// queries and max_kv tokens. (The plan's own need is not monotone: calls with
+// fewer items have more runs an item, calls with many none.) Few rows: an item
+// count that still splits, and the most runs that kv_attend_plan gives as many
+// items or fewer. Many rows: splits > 1 takes items < places, and then
+// items x splits < places + items.
+inline int64_t kv_attend_bound(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
+  const int64_t G = L.Hq / L.Hkv, nblk = (max_kv + 31) / 32;
+  const int few = L.D == 256 ? 16 : 32;  // rows of the kernel for few
+  auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+  auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
+  int64_t floats = 0;
+  for (int rows = 16; rows <= few; rows *= 2) {
+    const int64_t q = rows == 16 ? 1 : 16 / G + 1;  // the fewest queries of this form
+    if (q > max_q || q * G > rows || nblk <= 4 * kKvWaves) continue;
+    const int64_t places = (int64_t)num_cus * (L.D == 256 || rows == 32 ? 1 : 2);
+    const int64_t items = least(least(batch, kKvMaxBatch) * L.Hkv, most(2 * places, (nblk * places + 63) / 64) - 1);
+    if (items < L.Hkv) continue;
+    const int64_t runs = least((least(items, places) * nblk + 16 * kKvWaves - 1) / (16 * kKvWaves), 64 * places);
+    floats = most(floats, (items + most(runs, places)) * rows * (L.D + 2));
+  }
+  const int64_t places = (int64_t)num_cus * 2;
+  const int64_t items = least(batch * L.Hkv * ((max_q * G + 127) / 128), places - 1);
+  if (max_q * G > few && items >= L.Hkv && nblk > 8)
+    floats = most(floats, least(places + items - 1, items * least(kKvMaxSplits, (nblk + 7) / 8)) * 128 * (L.D + 2));
+  return floats * 4;
+}
+
 // Many rows: items that a call with `tokens` rows of q can have.
 inline int64_t kv_many_items(const KvPlan& p, const KvLayout& L, int64_t batch, int64_t tokens) {
   if (batch == 1 || batch > kKvMaxBatch) return p.items;

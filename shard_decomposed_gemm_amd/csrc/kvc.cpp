@@ -155,9 +155,7 @@ int kvc_append(kvc_ctx* ctx, void* pages, const kvc_append_args* p, void* stream
 int kvc_attend_workspace(const kvc_ctx* ctx, int32_t batch, int32_t max_q, int64_t max_kv, int64_t* bytes) {
   if (!ctx || !bytes || batch < 0 || max_q < 1 || max_kv < 1) return AGEMM_EINVAL;
   if (batch > kKvMaxTokens || max_q > kKvMaxTokens) return AGEMM_ESHAPE;
-  const KvPlan plan = kv_attend_plan(ctx->L, batch, max_q, max_kv, ctx->num_cus);
-  if (plan.items > kKvMaxItems) return AGEMM_ESHAPE;
-  *bytes = plan.ws_bytes;
+  *bytes = kv_attend_bound(ctx->L, batch, max_q, max_kv, ctx->num_cus);
   return AGEMM_OK;
 }
 

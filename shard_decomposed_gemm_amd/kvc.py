@@ -135,7 +135,8 @@ class KvCache:
         return torch.zeros(self.num_pages, self.page_bytes, dtype=torch.uint8, device=self.device)
 
     def workspace(self, batch: int, max_q: int = 1, max_kv: int = 1):
-        """Workspace for ``attend`` calls within these bounds: one for each call that may run at the same time."""
+        """Workspace for every ``attend`` call within these bounds (smaller batches, chunks and lengths too): one for
+        each call that may run at the same time."""
         import torch
         n = _i64()
         rc = self._lib.kvc_attend_workspace(self._h, int(batch), int(max_q), int(max_kv), ctypes.byref(n))
@@ -187,8 +188,8 @@ class KvCache:
         float16 or float32 and lse (T, Hq) float32.
 
         kv_len (batch,), q_start (batch + 1,), q_off (batch,) and page_table (batch, width) int32. scale: 1 / sqrt(D)
-        unless given. max_kv: the longest length to expect (the table's width unless given). Without a workspace one is
-        allocated on the stream for this call."""
+        unless given. max_kv: the longest length to expect (the table's width unless given). Without a workspace one
+        that ``workspace`` makes for the call's own bounds is allocated on the stream for this call."""
         T = q.shape[0]
         B = kv_len.shape[0]
         plain = self._plain

@@ -69,3 +69,33 @@ def test_attend_an_empty_batch_with_long_lengths(max_q):
               q_start=none(1), max_q=max_q)
     torch.cuda.synchronize()
     kv.check()
+
+
+# ---------------------------------------------------------------- one workspace for a server's calls
+
+def test_one_workspace_for_every_smaller_call():
+    """The workspace of the largest batch, chunk and length takes smaller calls, which split their work further."""
+    import torch
+    from shard_decomposed_gemm_amd import KvCache
+    Hq, Hkv, D, page, P = 16, 2, 64, 64, 40
+    r = np.random.default_rng(1)
+    kn, vn, shown = kx.tokens(r, (P * page, Hkv), D)
+    kn[0], shown[0] = 0, True
+    kv = KvCache(Hq, Hkv, D, page_tokens=page, num_pages=P)
+    pages, L = _dev(kx.pack(kn, vn, page)), P * page
+    ws = kv.workspace(600, 300, 2 * L)
+    count, total = np.cumsum(shown, 0), np.cumsum(shown[..., None] * vn.astype(np.int64), 0)
+    for batch, nq, max_kv in ((600, 1, L), (300, 1, L), (3, 1, L), (1, 1, 2 * L), (200, 3, L), (1, 4, L), (1, 40, L), (2, 300, L)):
+        T = batch * nq
+        q = torch.full((T, Hq, D), -1.0, dtype=torch.float16, device=gu.dev())
+        out, lse = torch.full((T, Hq, D), 9.0, device=gu.dev()), torch.full((T, Hq), 9.0, device=gu.dev())
+        kv.attend(pages, q, torch.full((batch,), L, dtype=torch.int32, device=gu.dev()),
+                  torch.arange(P, dtype=torch.int32, device=gu.dev()).expand(batch, P), out, lse=lse, max_q=nq,
+                  q_start=torch.arange(batch + 1, dtype=torch.int32, device=gu.dev()) * nq, scale=kx.SCALE, max_kv=max_kv,
+                  workspace=ws)
+        torch.cuda.synchronize()
+        kv.check()
+        last = L - nq + np.arange(T) % nq
+        n = np.repeat(count[last], Hq // Hkv, 1)
+        O = np.repeat(total[last], Hq // Hkv, 1) / n[..., None]
+        assert kx.close(out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64), O, n, True).all()

@@ -5,6 +5,7 @@ import re
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -21,7 +22,8 @@ def units(tmp_path_factory):
                     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
                     os.path.join(ROOT, "tests", "kv_units_check.cpp"), "-o", so], check=True)
     lib = ctypes.CDLL(so)
-    lib.kvu_needs.argtypes, lib.kvu_needs.restype = [ctypes.c_int] * 3 + [ctypes.c_int64] * 3 + [ctypes.c_int], ctypes.c_int64
+    for f in (lib.kvu_workspace, lib.kvu_needs):
+        f.argtypes, f.restype = [ctypes.c_int] * 3 + [ctypes.c_int64] * 3 + [ctypes.c_int], ctypes.c_int64
     return lib
 
 
@@ -41,3 +43,36 @@ def test_plan_of_an_empty_batch(units, Hq, Hkv, D):
     for max_q in (1, 3, 700):
         for max_kv in (1, 1024, 1025, 262144, (1 << 31) - 1):
             assert units.kvu_needs(Hq, Hkv, D, 0, max_q, max_kv, 256) == 0
+
+
+# ---------------------------------------------------------------- the workspace of calls within bounds
+
+def _sizes(top):
+    """Every size up to 70, then some of each octave and both sides of its ends, up to top."""
+    few = list(range(1, 71))
+    for p in range(6, 32):
+        few += [(1 << p) + d for d in (-1, 0, 1)] + [3 << (p - 1), (5 << (p - 2)) + 1]
+    return sorted({x for x in few if x <= top} | {top})
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(64, 8, 128), (32, 8, 128), (96, 8, 128), (96, 96, 128), (12, 1, 128), (1, 1, 64),
+                                      (17, 1, 64), (32, 4, 64), (16, 2, 256), (8, 8, 256), (40, 2, 128), (1024, 1024, 64),
+                                      (600, 600, 128), (1024, 1, 64)])
+def test_workspace_of_bounds_holds_every_smaller_call(units, Hq, Hkv, D):
+    """A server's workspace, made once for its largest batch, chunk and length, serves its smaller steps too."""
+    r = np.random.default_rng(Hq + D)
+    for batch, max_q, max_kv in ((256, 1, 8192), (64, 1, 8192), (8, 2048, 8192), (4, 2048, 16384), (512, 64, 40000),
+                                 (700, 4, 1 << 20), (1, 1, 262144), (3, 40, 1000), (2, 5, (1 << 31) - 1), (8192, 700, 33),
+                                 (1, 1, 1), (0, 1, 8192)):
+        size = units.kvu_workspace(Hq, Hkv, D, batch, max_q, max_kv, 256)
+        pick = lambda top, n: r.choice(_sizes(top), min(n, len(_sizes(top))), replace=False).tolist() + [top]  # noqa: E731
+        worst = 0
+        for b in pick(batch, 60) if batch else [0]:
+            for q in pick(max_q, 24):
+                for kv in pick(max_kv, 24):
+                    worst = max(worst, units.kvu_needs(Hq, Hkv, D, b, q, kv, 256))
+        assert worst <= size, (batch, max_q, max_kv)
+        # and it is no more than calls within the bounds come to, but for a factor
+        assert size <= 4 * worst + (1 << 20), (batch, max_q, max_kv, worst, size)
+        for b, q, kv in ((batch // 2, max_q, max_kv), (batch, max(1, max_q // 3), max_kv), (batch, max_q, max(1, max_kv - 1))):
+            assert units.kvu_workspace(Hq, Hkv, D, b, q, kv, 256) <= size
