@@ -96,9 +96,14 @@ KV_HD inline int kv_runs(int chunk, int splits, int nblk) {
   return nblk <= c ? 1 : (nblk + c - 1) / c;
 }
 
+// Blocks of a sequence of max_kv tokens, or of the longest there can be.
+inline int64_t kv_expected_blocks(int64_t max_kv) {
+  return max_kv < (int64_t)kKvWhole * 32 ? (max_kv + 31) / 32 : kKvWhole;
+}
+
 inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
   KvPlan p{};
-  const int64_t rows = max_q * (L.Hq / L.Hkv), nblk = (max_kv + 31) / 32;
+  const int64_t rows = max_q * (L.Hq / L.Hkv), nblk = kv_expected_blocks(max_kv);
   // As many rows as the kernel for few rows holds, it takes: 16 x 4 queries of 64
   // heads (8 kv heads, D 128) on 8192 tokens 44.5 us, the one for many 82; 16 x 2
   // of 16 heads (2, D 256) 26, 77.
@@ -124,7 +129,7 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
     //   1777 on themselves (448 items)     74.1  73.7  73.4  59.8   57.6
     //   1024 on 16384 (256 items)           351   349   345   355    437
     const int64_t places = (int64_t)num_cus * 2, least = p.items >= num_cus ? 128 : 8;
-    int64_t chunk = (p.items * nblk + places - 1) / places;
+    int64_t chunk = p.items < places ? (p.items * nblk + places - 1) / places : nblk;
     if (chunk < least) chunk = least;
     int64_t splits = (nblk + chunk - 1) / chunk;
     if (splits > kKvMaxSplits) splits = kKvMaxSplits;
@@ -159,7 +164,7 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
 // items or fewer. Many rows: splits > 1 takes items < places, and then
 // items x splits < places + items.
 inline int64_t kv_attend_bound(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
-  const int64_t G = L.Hq / L.Hkv, nblk = (max_kv + 31) / 32;
+  const int64_t G = L.Hq / L.Hkv, nblk = kv_expected_blocks(max_kv);
   const int few = L.D == 256 ? 16 : 32;  // rows of the kernel for few
   auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
   auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };

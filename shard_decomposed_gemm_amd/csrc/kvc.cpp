@@ -163,7 +163,8 @@ int kvc_attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, void* 
                void* stream) {
   if (!ctx) return AGEMM_EINVAL;
   KvPlan plan{};
-  if (p && p->batch >= 0 && p->max_q >= 1 && p->max_kv >= 1)  // refused below otherwise
+  if (p && p->batch >= 0 && p->batch <= kKvMaxTokens && p->max_q >= 1 && p->max_q <= kKvMaxTokens &&
+      p->max_kv >= 1)  // refused below otherwise
     plan = kv_attend_plan(ctx->L, p->batch, p->max_q, p->max_kv, ctx->num_cus);
   char why[kKvWhy];
   const int rc = kv_check_attend(ctx->L, pages, p, plan, workspace, workspace_bytes, why);

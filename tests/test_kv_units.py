@@ -76,3 +76,14 @@ def test_workspace_of_bounds_holds_every_smaller_call(units, Hq, Hkv, D):
         assert size <= 4 * worst + (1 << 20), (batch, max_q, max_kv, worst, size)
         for b, q, kv in ((batch // 2, max_q, max_kv), (batch, max(1, max_q // 3), max_kv), (batch, max_q, max(1, max_kv - 1))):
             assert units.kvu_workspace(Hq, Hkv, D, b, q, kv, 256) <= size
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(64, 8, 128), (96, 96, 128), (1, 1, 64), (16, 2, 256), (1024, 1, 64)])
+def test_plan_of_lengths_beyond_the_longest(units, Hq, Hkv, D):
+    """max_kv is only what to expect: beyond the longest length it stands for that, up to the largest number."""
+    for batch, max_q in ((1, 1), (3, 40), (400, 2), (8, 700), (1 << 23, 1 << 23)):
+        for f in (units.kvu_needs, units.kvu_workspace):
+            want = f(Hq, Hkv, D, batch, max_q, 1 << 31, 256)
+            assert want >= 0
+            for max_kv in ((1 << 31) + 1, 1 << 40, (1 << 63) - 40, (1 << 63) - 1):
+                assert f(Hq, Hkv, D, batch, max_q, max_kv, 256) == want
