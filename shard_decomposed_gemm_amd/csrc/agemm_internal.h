@@ -14,8 +14,7 @@ constexpr int kMaxTiles = 64;   // T = W * KT; one wave polls every flag at once
 
 // Device error word (lives in host-pinned, device-mapped memory).
 struct ErrWord {
-  uint32_t code;     // 0 = none, 1 = flag wait timed out, 2 = inbox guard wait timed out (producer);
-                     // the key/value cache has its own cases (KvErr in kv_internal.h)
+  uint32_t code;     // 0 = none, 1 = flag wait timed out, 2 = inbox guard wait timed out (producer)
   uint32_t tile;     // tile id (code 1) or guard counter (code 2) that timed out
   uint32_t target;   // value waited for
   uint32_t seen;     // last value observed

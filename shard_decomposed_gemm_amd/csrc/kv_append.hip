@@ -279,12 +279,11 @@ __global__ __launch_bounds__(kThreads, ROLE == kQueries ? (E > 8 ? 4 : 6) : E > 
       if (R) pos = scalar_load(a.positions, now.t);
     }
     if (R && (pos < 0 || pos >= a.rope_len)) {
-      if (fresh && (threadIdx.x & 63) == 0) kv_report(a.err, kKvPosition, a.first + now.t, pos, a.rope_len);
+      if (fresh && (threadIdx.x & 63) == 0) kv_report(a.err, kKvPosition, a.first + now.t, pos);
       continue;
     }
     if (!is_q && (slot < 0 || slot >= (a.L.num_pages << a.L.page_shift))) {
-      if (slot >= 0 && fresh && (threadIdx.x & 63) == 0)
-        kv_report(a.err, kKvSlot, a.first + now.t, slot, a.L.num_pages << a.L.page_shift);
+      if (slot >= 0 && fresh && (threadIdx.x & 63) == 0) kv_report(a.err, kKvSlot, a.first + now.t, slot);
       continue;
     }
     if (R && (is_q || is_k) && fresh && d0 < R) {
@@ -333,7 +332,7 @@ __global__ __launch_bounds__(kThreads, ROLE == kQueries ? (E > 8 ? 4 : 6) : E > 
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = (double)in.x[e];
         prepare(y);
-        if (quantise<E>(y, word, s, b)) kv_report(a.err, kKvValue, a.first + now.t, h0 + sub, 0);
+        if (quantise<E>(y, word, s, b)) kv_report(a.err, kKvValue, a.first + now.t, h0 + sub);
       }
       const int off = (int)(slot & (a.L.page_tokens - 1));
       const int tok = off & 31;
@@ -381,7 +380,7 @@ __global__ __launch_bounds__(kThreads) void kv_read_kernel(KvReadArgs a) {
   const int64_t slot = a.slots[t];
   if (slot < 0) return;
   if (slot >= (a.L.num_pages << a.L.page_shift)) {
-    if (lane == 0 && h == 0) kv_report(a.err, kKvSlot, a.first + t, slot, a.L.num_pages << a.L.page_shift);
+    if (lane == 0 && h == 0) kv_report(a.err, kKvSlot, a.first + t, slot);
     return;
   }
   const int off = (int)(slot & (a.L.page_tokens - 1));

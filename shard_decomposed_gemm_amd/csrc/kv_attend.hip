@@ -165,12 +165,12 @@ __device__ inline Sequence sequence(const KvAttendArgs& a, int b, bool tell) {
   const int64_t n = (int64_t)end - start;
   s.off = !a.causal ? (int64_t)1 << 32 : a.q_off ? (int64_t)load(a.q_off, b) : 0;
   const bool usable = n >= 0 && n <= a.max_q && start >= 0 && end <= a.tokens;
-  if (!usable && tell) kv_report(a.err, kKvRows, b, n, a.max_q);
+  if (!usable && tell) kv_report(a.err, kKvRows, b, n);
   s.n = usable ? (int)n : 0;
   s.row0 = start;
   const int64_t most = (int64_t)a.table_width << a.L.page_shift;
   const bool fits = len >= 0 && len <= most;
-  if (!fits && tell) kv_report(a.err, kKvLength, b, len, most);
+  if (!fits && tell) kv_report(a.err, kKvLength, b, len);
   s.len = len < 0 ? 0 : len <= most ? len : (int)most;
   if (a.causal && !a.q_off) s.off = (int64_t)s.len - n;
   return s;
@@ -321,7 +321,7 @@ __device__ inline int64_t block_on(const KvAttendArgs& a, int page, int h, int j
   return kv_block_at(a.L, page, h, j & ((a.L.page_tokens >> 5) - 1));
 }
 __device__ inline void report_lost(const KvAttendArgs& a, int b, const Lost& lost) {
-  if (lost.any) kv_report(a.err, kKvPage, b, lost.page, a.L.num_pages);
+  if (lost.any) kv_report(a.err, kKvPage, b, lost.page);
 }
 
 // Writes one row's channels d0 .. d0 + N - 1 of a finished output.

@@ -4,19 +4,9 @@
 
 #include "agemm_internal.h"
 #include "kv_layout.h"
+#include "kv_report.h"
 
 namespace agemm {
-
-// Cases of the error word (ErrWord.code) of the cache's kernels; `tile` is the
-// index of the token or sequence, `seen` the value met, `target` its bound.
-enum KvErr : uint32_t {
-  kKvSlot = 1,      // slot past the last page
-  kKvPosition = 2,  // position outside the rotation table
-  kKvValue = 3,     // key or value not finite or beyond the limit
-  kKvPage = 4,      // page id outside the cache
-  kKvLength = 5,    // length negative or beyond the page table
-  kKvRows = 6,      // query rows beyond max_q or T, or not ascending
-};
 
 constexpr float kKvLimit = 20000.f;  // |x| held: (16 + n) s + b and b = -3.14 |x| at worst stay in binary16
 
@@ -36,7 +26,7 @@ struct KvAppendArgs {
   float eps;
   int64_t first;  // number of the call's token that is token 0 here
   uint32_t quads, near;  // quads of a wave, workgroups of 32 tokens (the launch fills them in)
-  ErrWord* err;
+  uint64_t* err;  // kv_report.h
 };
 
 struct KvReadArgs {
@@ -46,7 +36,7 @@ struct KvReadArgs {
   const int64_t* slots;
   _Float16 *k_out, *v_out;
   int64_t first;  // number of the call's token that is token 0 here
-  ErrWord* err;
+  uint64_t* err;  // kv_report.h
 };
 
 struct KvAttendArgs {
@@ -64,7 +54,7 @@ struct KvAttendArgs {
   float* lse;
   KvPlan plan;
   float* ws;  // plan.ws_bytes of partials
-  ErrWord* err;
+  uint64_t* err;  // kv_report.h
 };
 
 hipError_t launch_kv_append(const KvAppendArgs& a, int num_cus, hipStream_t s);
@@ -72,11 +62,8 @@ hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t s);
 hipError_t launch_kv_attend(const KvAttendArgs& a, bool out_f32, hipStream_t s);
 
 #ifdef __HIPCC__
-__device__ inline void kv_report(ErrWord* err, uint32_t code, int64_t index, int64_t seen, int64_t bound) {
-  __hip_atomic_store(&err->tile, (uint32_t)index, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-  __hip_atomic_store(&err->target, (uint32_t)bound, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-  __hip_atomic_store(&err->seen, (uint32_t)seen, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
-  __hip_atomic_store(&err->code, code, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_SYSTEM);
+__device__ inline void kv_report(uint64_t* err, uint32_t code, int64_t index, int64_t seen) {
+  __hip_atomic_store(err, kv_report_word(code, index, seen), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
 }
 #endif
 

@@ -8,7 +8,6 @@
 
 #include <cstdarg>
 #include <cstdio>
-#include <cstring>
 #include <new>
 #include <string>
 
@@ -22,8 +21,8 @@ struct kvc_ctx {
   KvLayout L{};
   int device = 0;
   int num_cus = 0;
-  ErrWord* err_host = nullptr;
-  ErrWord* err_dev = nullptr;
+  uint64_t* err_host = nullptr;  // the last report (kv_report.h), 0: none
+  uint64_t* err_dev = nullptr;
   std::string last_error;
 };
 
@@ -70,13 +69,13 @@ int kvc_create(kvc_ctx** out, int Hq, int Hkv, int D, int page_tokens, int64_t n
   hipError_t e = hipGetDevice(&c->device);
   if (e == hipSuccess) e = hipDeviceGetAttribute(&c->num_cus, hipDeviceAttributeMultiprocessorCount, c->device);
   void* hp = nullptr;
-  if (e == hipSuccess) e = hipHostMalloc(&hp, sizeof(ErrWord), hipHostMallocMapped | hipHostMallocCoherent);
+  if (e == hipSuccess) e = hipHostMalloc(&hp, sizeof(uint64_t), hipHostMallocMapped | hipHostMallocCoherent);
   if (e == hipSuccess) {
-    c->err_host = static_cast<ErrWord*>(hp);
-    std::memset(hp, 0, sizeof(ErrWord));
+    c->err_host = static_cast<uint64_t*>(hp);
+    *c->err_host = 0;
     void* dp = nullptr;
     e = hipHostGetDevicePointer(&dp, hp, 0);
-    c->err_dev = static_cast<ErrWord*>(dp);
+    c->err_dev = static_cast<uint64_t*>(dp);
   }
   if (e != hipSuccess) {
     if (hp) (void)hipHostFree(hp);
@@ -226,20 +225,11 @@ int kvc_read(kvc_ctx* ctx, const void* pages, int64_t tokens, const int64_t* slo
 
 int kvc_check(kvc_ctx* ctx) {
   if (!ctx) return AGEMM_EINVAL;
-  volatile ErrWord* w = ctx->err_host;
-  const unsigned code = w->code, at = w->tile, seen = w->seen, bound = w->target;
-  if (code == 0) return AGEMM_OK;
-  w->code = 0;
-  const int v = (int)seen;
-  switch (code) {
-    case kKvSlot: return fail(ctx, AGEMM_EINVAL, "token %u: slot %d past the last page (%u slots)", at, v, bound);
-    case kKvPosition: return fail(ctx, AGEMM_EINVAL, "token %u: position %d outside the rotation table (%u rows)", at, v, bound);
-    case kKvValue: return fail(ctx, AGEMM_EINVAL, "token %u: a key or value of kv head %u not finite or beyond the limit", at, seen);
-    case kKvPage: return fail(ctx, AGEMM_EINVAL, "sequence %u: page id %d outside the cache (%u pages)", at, v, bound);
-    case kKvLength: return fail(ctx, AGEMM_EINVAL, "sequence %u: length %d outside 0..%u", at, v, bound);
-    case kKvRows: return fail(ctx, AGEMM_EINVAL, "sequence %u: %d query rows, or rows outside q (at most %u)", at, v, bound);
-    default: return fail(ctx, AGEMM_EINVAL, "unknown case %u", code);
-  }
+  const uint64_t word = __atomic_exchange_n(ctx->err_host, uint64_t{0}, __ATOMIC_ACQ_REL);
+  if (word == 0) return AGEMM_OK;
+  char what[kKvWhy];
+  kv_report_text(what, sizeof what, word, ctx->L.num_pages << ctx->L.page_shift, ctx->L.num_pages);
+  return fail(ctx, AGEMM_EINVAL, "%s", what);
 }
 
 const char* kvc_last_error(kvc_ctx* ctx) { return ctx ? ctx->last_error.c_str() : ""; }

@@ -24,6 +24,8 @@ def units(tmp_path_factory):
     lib = ctypes.CDLL(so)
     for f in (lib.kvu_workspace, lib.kvu_needs):
         f.argtypes, f.restype = [ctypes.c_int] * 3 + [ctypes.c_int64] * 3 + [ctypes.c_int], ctypes.c_int64
+    lib.kvu_report.argtypes = [ctypes.c_uint32] + [ctypes.c_int64] * 4 + [ctypes.c_char_p]
+    lib.kvu_report.restype = None
     return lib
 
 
@@ -87,3 +89,30 @@ def test_plan_of_lengths_beyond_the_longest(units, Hq, Hkv, D):
             assert want >= 0
             for max_kv in ((1 << 31) + 1, 1 << 40, (1 << 63) - 40, (1 << 63) - 1):
                 assert f(Hq, Hkv, D, batch, max_q, max_kv, 256) == want
+
+
+# ---------------------------------------------------------------- reports
+
+def test_report_says_what_was_met(units):
+    buf = ctypes.create_string_buffer(256)
+
+    def text(code, index, seen):
+        units.kvu_report(code, index, seen, 1 << 40, 77, buf)
+        return buf.value.decode()
+
+    top = (1 << 23) - 1
+    for at in (0, 5, 4097, top):
+        for v in (1 << 40, (1 << 32) + 5, (1 << 31), (1 << 35) - 2, 64):
+            said = f"from {(1 << 35) - 1}" if v >= (1 << 35) - 1 else v
+            assert text(1, at, v) == f"token {at}: slot {said} past the last page ({1 << 40} slots)"
+            assert text(2, at, v) == f"token {at}: position {said} outside the rotation table"
+        for v in (-1, -5, -(1 << 31) - 1, -(1 << 35) + 1):
+            assert text(2, at, v) == f"token {at}: position {v} outside the rotation table"
+        assert text(2, at, -(1 << 63)) == f"token {at}: position up to {-(1 << 35)} outside the rotation table"
+        assert f"token {at}: " in text(3, at, 1023) and "kv head 1023" in text(3, at, 1023)
+        for v in (-(1 << 31), -1, 77, (1 << 31) - 1):
+            assert text(4, at, v) == f"sequence {at}: page id {v} outside the cache (77 pages)"
+            assert text(5, at, v).startswith(f"sequence {at}: length {v} ")
+        for v in (-(1 << 32) + 1, -1, (1 << 32) - 1):
+            assert text(6, at, v).startswith(f"sequence {at}: {v} query rows")
+    assert "unknown case 0" in text(0, 0, 0)
