@@ -420,13 +420,11 @@ hipError_t launch_append(KvAppendArgs a, int num_cus, hipStream_t s) {
   a.quads = all <= (int64_t)num_cus * 32 ? 1 : kAhead;
   a.near = (uint32_t)(32 * nk / (waves * a.quads) > 1 ? 32 * nk / (waves * a.quads) : 1);
   auto groups = [&](int64_t quads) { return (unsigned)((a.tokens * quads + waves * a.quads - 1) / (waves * a.quads)); };
-  if (few && nq && nk) {
-    hipLaunchKernelGGL((kv_append_kernel<E, kBoth, ROPE>), dim3(groups(nq > nk ? nq : nk), 2), dim3(kThreads), 0, s, a);
-  } else {
-    if (nq) hipLaunchKernelGGL((kv_append_kernel<E, kQueries, ROPE>), dim3(groups(nq)), dim3(kThreads), 0, s, a);
-    if (nk) hipLaunchKernelGGL((kv_append_kernel<E, kKeysValues, ROPE>), dim3(groups(nk)), dim3(kThreads), 0, s, a);
-  }
-  return hipGetLastError();
+  if (few && nq && nk) return kv_launch(kv_append_kernel<E, kBoth, ROPE>, dim3(groups(nq > nk ? nq : nk), 2), kThreads, s, a);
+  hipError_t e = hipSuccess;
+  if (nq) e = kv_launch(kv_append_kernel<E, kQueries, ROPE>, dim3(groups(nq)), kThreads, s, a);
+  if (nk && e == hipSuccess) e = kv_launch(kv_append_kernel<E, kKeysValues, ROPE>, dim3(groups(nk)), kThreads, s, a);
+  return e;
 }
 
 template <int E>
@@ -449,14 +447,13 @@ hipError_t launch_kv_append(const KvAppendArgs& a, int num_cus, hipStream_t s) {
 
 hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t s) {
   const int64_t rows = a.tokens * a.L.Hkv;
-  const dim3 grid((unsigned)((rows + kRowsPerPass - 1) / kRowsPerPass)), block(kThreads);
+  const dim3 grid((unsigned)((rows + kRowsPerPass - 1) / kRowsPerPass));
   switch (a.L.D) {
-    case 64: hipLaunchKernelGGL(kv_read_kernel<4>, grid, block, 0, s, a); break;
-    case 128: hipLaunchKernelGGL(kv_read_kernel<8>, grid, block, 0, s, a); break;
-    case 256: hipLaunchKernelGGL(kv_read_kernel<16>, grid, block, 0, s, a); break;
+    case 64: return kv_launch(kv_read_kernel<4>, grid, kThreads, s, a);
+    case 128: return kv_launch(kv_read_kernel<8>, grid, kThreads, s, a);
+    case 256: return kv_launch(kv_read_kernel<16>, grid, kThreads, s, a);
     default: return hipErrorInvalidValue;
   }
-  return hipGetLastError();
 }
 
 }  // namespace agemm

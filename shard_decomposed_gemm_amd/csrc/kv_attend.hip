@@ -1021,17 +1021,19 @@ template <int D, bool F32>
 hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
   const int64_t items = a.plan.many ? kv_many_items(a.plan, a.L, a.batch, a.tokens) : a.plan.items;
   const dim3 grid((unsigned)(a.plan.many ? items : a.plan.slots), (unsigned)a.plan.splits);
+  hipError_t e = hipErrorInvalidValue;
   if (a.plan.many && a.plan.rows == 128) {
-    hipLaunchKernelGGL((kv_attend_many_kernel<D, 4, F32>), grid, dim3(256), 0, s, a);
+    e = kv_launch(kv_attend_many_kernel<D, 4, F32>, grid, 256, s, a);
   } else if (a.plan.many) {
-    if constexpr (D == 128) hipLaunchKernelGGL((kv_attend_many_kernel<D, 8, F32>), grid, dim3(512), 0, s, a);
-  } else if (a.plan.rows == 16) hipLaunchKernelGGL((kv_attend_few_kernel<D, 1, F32>), grid, dim3(kWaves * 64), 0, s, a);
-  else if constexpr (D <= 128)
-    hipLaunchKernelGGL((kv_attend_few_kernel<D, 2, F32>), grid, dim3(kWaves * 64), 0, s, a);
-  if (a.plan.ws_bytes > 0)
-    hipLaunchKernelGGL((kv_attend_join_kernel<D, F32>), dim3((unsigned)items, (unsigned)a.plan.join_groups),
-                       dim3(kJoinThreads), 0, s, a);
-  return hipGetLastError();
+    if constexpr (D == 128) e = kv_launch(kv_attend_many_kernel<D, 8, F32>, grid, 512, s, a);
+  } else if (a.plan.rows == 16) {
+    e = kv_launch(kv_attend_few_kernel<D, 1, F32>, grid, kWaves * 64, s, a);
+  } else if constexpr (D <= 128) {
+    e = kv_launch(kv_attend_few_kernel<D, 2, F32>, grid, kWaves * 64, s, a);
+  }
+  if (a.plan.ws_bytes > 0 && e == hipSuccess)
+    e = kv_launch(kv_attend_join_kernel<D, F32>, dim3((unsigned)items, (unsigned)a.plan.join_groups), kJoinThreads, s, a);
+  return e;
 }
 
 }  // namespace

@@ -62,6 +62,14 @@ hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t s);
 hipError_t launch_kv_attend(const KvAttendArgs& a, bool out_f32, hipStream_t s);
 
 #ifdef __HIPCC__
+// Launches and gives this launch's own status (hipGetLastError would give any
+// earlier failure of the thread).
+template <class A>
+hipError_t kv_launch(void (*kernel)(A), dim3 grid, unsigned threads, hipStream_t s, A a) {
+  void* args[] = {&a};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), args, 0, s);
+}
+
 __device__ inline void kv_report(uint64_t* err, uint32_t code, int64_t index, int64_t seen) {
   __hip_atomic_store(err, kv_report_word(code, index, seen), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_SYSTEM);
 }

@@ -72,3 +72,32 @@ def test_reports_of_many_sequences_do_not_mix():
         said = re.search(r"sequence (\d+): (page id|length) (\d+) ", _message(kv))
         at = int(said[1])
         assert (said[2], int(said[3])) == (("page id", 5 + 3 * at) if at % 2 == 0 else ("length", 97 + at))
+
+
+def test_an_earlier_failed_hip_call_is_not_taken_for_the_cache_s():
+    """A runtime call that failed before, somewhere else in the process, leaves its error for hipGetLastError; the
+    cache's calls say what became of their own launches."""
+    import ctypes
+
+    import torch
+    from shard_decomposed_gemm_amd import KvCache
+    kv = KvCache(2, 1, 64, page_tokens=32, num_pages=64)
+    x, out = torch.ones(3, 1, 64, dtype=torch.float16, device=gu.dev()), torch.empty(1, 2, 64, device=gu.dev())
+    q, slots, pages = torch.ones(1, 2, 64, dtype=torch.float16, device=gu.dev()), _dev(np.arange(3)), kv.new_pages()
+    table = torch.arange(64, dtype=torch.int32, device=gu.dev())[None]
+    lens = torch.full((1,), 3, dtype=torch.int32, device=gu.dev())
+    ws, back = kv.workspace(1, 1, 2048), torch.empty_like(x)
+    torch.cuda.synchronize()
+    hip = ctypes.CDLL([line.split()[-1] for line in open("/proc/self/maps") if "libamdhip64" in line][0])
+    fail = lambda: hip.hipSetDevice(100000)  # noqa: E731 (refused)
+    try:
+        for call in (lambda: kv.append(pages, k=x, v=x, slots=slots), lambda: kv.read(pages, slots, back, torch.empty_like(x)),
+                     lambda: kv.attend(pages, q, lens, table, out, workspace=ws)):
+            assert fail() != 0
+            call()
+            assert hip.hipGetLastError() != 0  # and it is still there for whoever asks
+    finally:
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    kv.check()
+    assert (out == 1).all() and (back == 1).all()
