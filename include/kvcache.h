@@ -147,9 +147,11 @@ typedef struct {
  * A row that sees no token: out = 0 and lse = -FLT_MAX, which the combine
  * takes as a partial without weight. Rows of q past the last sequence's are
  * left as they were in out and lse. Scores must fit binary32. Sums, maxima and
- * statistics in binary32; with a binary32 out the softmax weights enter the
- * product with the values as two binary16 numbers (22 bits), with a binary16
- * out as one.
+ * statistics in binary32. The softmax weights enter the product with the
+ * values in binary16: with a binary32 out as two numbers, cut, which a weight
+ * w is off by at most max(2^-21 w, 2^-36 of the row's largest weight) - over
+ * L tokens of tiny weights up to L 2^-36 max |V| in out; with a binary16 out as
+ * one, rounded: max(2^-11 w, 2^-37 of the largest). lse has all of every weight.
  * Reported by kvc_check: a page id outside the cache (its tokens count as not
  * seen), a length that is negative or does not fit the table (clamped), a
  * sequence with more than max_q queries, rows past T or a negative number of

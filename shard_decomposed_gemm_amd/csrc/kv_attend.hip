@@ -18,9 +18,17 @@
 // The running maximum m of the softmax is replaced only when a score passes it
 // by 2^3: weights are kept as 2^(x - m + 12) (x the score in units of log 2),
 // at most 2^15, so the usual block needs no maximum across lanes and no
-// rescaling. Below 2^(m - 26) weights lose bits to binary16's subnormals.
-// With binary32 outputs a weight enters the product as two binary16 numbers,
-// its value cut to binary16 and the rest.
+// rescaling. The largest weight is at least 2^12; binary16 has multiples of
+// 2^-24 at the least, 2^-36 of that.
+//
+// With binary16 outputs a weight enters the product rounded to binary16 once
+// (off by 2^-11 of it, as the output itself is, or half of 2^-24): a second
+// number would be as many matrix instructions again for a bit that the output
+// does not hold. Against 64 bits outputs are off by 2.4 to 2.9e-4 (norms),
+// one rounding of them alone by 2.1e-4. With binary32 outputs it enters as two
+// numbers, its value cut to binary16 and the rest cut again: off by less than
+// 2^-21 of it or 2^-24, whichever is more. Cut, because one instruction cuts
+// two numbers. The sum of the weights takes them whole.
 #include <type_traits>
 
 #include "kv_internal.h"

@@ -99,3 +99,43 @@ def test_one_workspace_for_every_smaller_call():
         n = np.repeat(count[last], Hq // Hkv, 1)
         O = np.repeat(total[last], Hq // Hkv, 1) / n[..., None]
         assert kx.close(out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64), O, n, True).all()
+
+
+# ---------------------------------------------------------------- tiny weights
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("queries", [1, 40])
+@pytest.mark.parametrize("part", [3326.99, 1663.5, 52.9, 3.98])
+def test_attend_a_flat_tail_under_one_large_weight(part, queries, f32):
+    """One token has all but a little of the weight, and 2^18 others the same tiny weight each, part x 2^-36 of the
+    largest: a multiple of binary16's least number that the cut to two numbers (the rounding to one) makes whole."""
+    import torch
+    from shard_decomposed_gemm_amd import KvCache
+    D, page, L = 64, 256, 1 << 18
+    P = L // page
+    kn, vn = np.zeros((L, 1, D), dtype=np.uint8), np.full((L, 1, D), 15, dtype=np.uint8)
+    kn[:, :, 0], kn[0], vn[0] = 15, 0, 0
+    kv = KvCache(1, 1, D, page_tokens=page, num_pages=P)
+    q = torch.zeros(queries, 1, D, dtype=torch.float16, device=gu.dev())
+    q[..., 0] = -1
+    out = torch.empty(queries, 1, D, dtype=torch.float32 if f32 else torch.float16, device=gu.dev())
+    lse = torch.empty(queries, 1, device=gu.dev())
+    scale = float(np.float32((36 - np.log2(part)) * np.log(2) / 15))
+    i32 = lambda x: _dev(np.asarray(x, dtype=np.int32))  # noqa: E731
+    kv.attend(_dev(kx.pack(kn, vn, page)), q, i32([L]), i32(np.arange(P)[None]), out, lse=lse, q_start=i32([0, queries]),
+              max_q=queries, causal=False, scale=scale)
+    torch.cuda.synchronize()
+    kv.check()
+    w = np.exp(-15 * scale)
+    total = 1 + (L - 1) * w
+    want = 15 * (L - 1) * w / total
+    # The score -15 scale is one exact product; its factor scale log2(e) and the exponent round three times, and the
+    # power once more: d of a weight. 256 runs; a wave of few rows adds 32 times in a lane of its four blocks, one of
+    # many rows 512 (and both up to 128 products in a row), then the waves and runs add up.
+    d = 3 * 15 * scale * kx.ROUND + 2.0 ** -22
+    sums = (512 + 128 + 8 + 256) * kx.ROUND
+    bound = want * (2 * d + 2 * sums + (2.0 ** -21 if f32 else 2.0 ** -11)) + 15 * L * (2.0 ** -36 if f32 else 2.0 ** -37)
+    bound += want * 2.0 ** -23 if f32 else max(want * 2.0 ** -11, 2.0 ** -25)
+    assert (np.abs(out.cpu().numpy().astype(np.float64) - want) <= bound).all()
+    got = lse.cpu().numpy().astype(np.float64)
+    assert (np.abs(got - np.log(total)) <= (total - 1) / total * (d + sums) + sums + 2.0 ** -18).all()
