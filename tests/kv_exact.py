@@ -47,3 +47,41 @@ def close(got, lse, O, count, f32, sums=2 * ROUND):
     # a rounded constant
     want = np.where(some, np.log(np.maximum(count, 1)), okv.LOWEST)
     return ok & np.where(some, np.abs(lse - want) <= 2.0 ** -18 + sums + np.abs(want) * 2 * ROUND, lse == okv.LOWEST)
+
+
+class Sequences:
+    """A cache of sequences of these lengths, pages shuffled, the bytes of no sequence NaN pairs; what their rows are."""
+
+    def __init__(self, seed, Hkv, D, page, lens, top=15):
+        r = np.random.default_rng(seed)
+        need = [-(-n // page) for n in lens]
+        ids = r.permutation(sum(need) + 1).astype(np.int32)
+        slots = (sum(need) + 1) * page
+        kn, vn, shown = tokens(r, (slots, Hkv), D, top)
+        self.table = np.full((len(lens), max(1, max(need))), -7, dtype=np.int32)  # nothing reads the rest
+        self.shown, self.values, used, at = [], [], np.zeros(slots, dtype=bool), 0
+        for i, n in enumerate(lens):
+            self.table[i, :need[i]] = ids[at:at + need[i]]
+            at += need[i]
+            slot = (self.table[i, :need[i], None].astype(np.int64) * page + np.arange(page)).reshape(-1)[:n]
+            kn[slot[:1]], shown[slot[:1]], used[slot] = 0, True, True
+            self.shown.append(shown[slot])
+            self.values.append(vn[slot])
+        s, b = pairs((slots, Hkv))
+        s[~used], b[~used] = np.nan, np.nan
+        self.pages = okv.pack(kn, s, b, vn, s, b, page)
+
+    def rows(self, i, seen, G):
+        """(O (n, Hq, D), count (n, Hq)) of rows of sequence i that see the first seen[n] tokens."""
+        shown, values = self.shown[i], self.values[i]
+        if len(shown) == 0:
+            shown, values = np.zeros((1, *shown.shape[1:]), dtype=bool), np.zeros((1, *values.shape[1:]), dtype=np.uint8)
+        last = np.maximum(np.asarray(seen) - 1, 0)
+        least, span = last.min(initial=0), last.max(initial=0) + 1
+        kept = values * shown[..., None]
+        count, total = shown[:least].sum(0, dtype=np.int64), kept[:least].sum(0, dtype=np.int64)
+        count = count + np.cumsum(shown[least:span], 0, dtype=np.int64)[last - least]
+        total = total + np.cumsum(kept[least:span], 0, dtype=np.int64)[last - least]
+        count[np.asarray(seen) <= 0] = 0
+        O = np.where(count[..., None] > 0, total / np.maximum(count, 1)[..., None], 0.0)
+        return np.repeat(O, G, 1), np.repeat(count, G, 1)

@@ -5,6 +5,7 @@ import pytest
 
 from tests import gpu_util as gu
 from tests import kv_exact as kx
+from tests.test_gpu_kv import BATCHES, LONG
 
 pytestmark = pytest.mark.gpu
 
@@ -139,3 +140,36 @@ def test_attend_a_flat_tail_under_one_large_weight(part, queries, f32):
     assert (np.abs(out.cpu().numpy().astype(np.float64) - want) <= bound).all()
     got = lse.cpu().numpy().astype(np.float64)
     assert (np.abs(got - np.log(total)) <= (total - 1) / total * (d + sums) + sums + 2.0 ** -18).all()
+
+
+# ---------------------------------------------------------------- every token once
+
+BIG = [
+    # Hq, Hkv, D, page, [(queries, length)], q_off, max_kv: single tokens of long sequences, prompts on long ones
+    (12, 1, 128, 256, [(1, 262144)], None, None),
+    (3, 3, 64, 32, [(1, 131072 + 77)], None, None),
+    (4, 2, 256, 64, [(1, 50001), (1, 9), (1, 20000)], None, None),
+    (8, 2, 128, 64, [(1, 4000 + 131 * i) for i in range(40)], None, None),
+    (8, 1, 64, 64, [(5, 60000)], None, None),
+    (1, 1, 128, 64, [(1000, 5000)], None, None),
+    (16, 2, 128, 64, [(96, 20000), (200, 7777)], None, None),
+    (6, 1, 256, 128, [(60, 9000)], None, None),
+]
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,D,page,shape,q_off,max_kv", LONG + BATCHES + BIG)
+def test_attend_takes_every_token_once(Hq, Hkv, D, page, shape, q_off, max_kv, f32):
+    """Runs, tiles and their joins leave out no block, take none twice, and pair keys with their own values."""
+    from shard_decomposed_gemm_amd import KvCache
+    print(f"[kv every] {Hq} {Hkv} {D} {page} {shape[:4]} {len(shape)} {q_off} {max_kv} {f32}", flush=True)
+    lens = [n for _, n in shape]
+    starts = np.concatenate([[0], np.cumsum([q for q, _ in shape])])
+    c = kx.Sequences(Hq + D, Hkv, D, page, lens)
+    kv = KvCache(Hq, Hkv, D, page_tokens=page, num_pages=c.pages.shape[0])
+    got, lse = _attend(kv, _dev(c.pages), _dev(c.table), lens, starts, max(n for n, _ in shape), f32, q_off, max_kv)
+    for i, (n, L) in enumerate(shape):
+        off = L - n if q_off is None else q_off[i]
+        O, count = c.rows(i, np.clip(off + np.arange(n) + 1, 0, L), Hq // Hkv)
+        rows = slice(starts[i], starts[i + 1])
+        assert kx.close(got[rows], lse[rows], O, count, f32).all(), i
