@@ -49,8 +49,26 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kNoMax = -3.0e38f;  // exponent base before the first score
 constexpr float kShift = 12.f;      // weights are 2^(x - m + kShift)
 constexpr float kTop = 15.f;        // and at most 2^kTop
+constexpr float kFar = 0x1p24f;     // from here on binary32 holds no fractions of an exponent
 
 __device__ inline float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The exponent base of a largest score `top`: kShift less, or top itself where
+// binary32 would make more than kTop of that.
+__device__ inline float base_of(float top) {
+  const float b = top - kShift;
+  return top - b > kTop ? top : b;
+}
+// Where a base is so large that binary32 holds no fractions of it, the product
+// of a score and the factor is rounded before the base is taken off, so that
+// equal scores have equal weights: a multiply-add, which has the exact product,
+// would give each block's whatever the base's rounding leaves. Every block then
+// goes the way of a new maximum.
+__device__ inline bool is_far(float base) { return fabsf(base) >= kFar && base > kNoMax; }
+__device__ inline float less_base(float rounded, float base) {
+  asm("" : "+v"(rounded));  // no multiply-add
+  return rounded - base;
+}
 
 // The constants that make (16 + n) of a nibble, in registers: with both as
 // literals the compiler takes an AND and an OR, with registers one instruction.
@@ -503,6 +521,7 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   }
   const int whole = seq.seen(0) >> 5;  // blocks that every row sees whole
   const float factor = a.scale * kLog2e;
+  float limit = kTop;  // of the exponents, the same in all lanes; -inf once some row's base is far
   const Bits bits;
 
   // One block; `more`: another follows, whose loads go out on the way.
@@ -545,17 +564,23 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
         top = max8(e);
       };
       exponents(base[n]);
-      if (__any(top > kTop)) {  // a new maximum, for some column
+      if (__any(top > limit)) {  // a new maximum, for some column
         exponents(0.f);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float nb = fmaxf(base[n], top - kShift);
+        const float nb = fmaxf(base[n], base_of(top));
+        if (__any(is_far(nb))) limit = -__builtin_inff();
         const float f = exp2_hw(base[n] - nb);
         sum[n] *= f;
 #pragma unroll
         for (int m = 0; m < MT; ++m) o[n][m] *= f;
         base[n] = nb;
-        exponents(nb);
+        if (limit == kTop) {
+          exponents(nb);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) e[i] = less_base(e[i], nb);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
@@ -726,6 +751,7 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[m][i] = 0.f;
   float base = kNoMax, sum = 0.f;
+  float limit = kTop;  // of the exponents, the same in all lanes; -inf once some row's base is far
 
   // This thread's piece of a tile: block, and within it the key row's piece and the value piece.
   const int piece = tid & (D - 1), pb = uniform(tid / D);
@@ -834,16 +860,24 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
       if constexpr (NB > 1) top = max3(top, max8(e[1]), top);
     };
     exponents(base);
-    if (__any(top > kTop)) {
+    if (__any(top > limit)) {
       exponents(0.f);
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float nb = fmaxf(base, top - kShift);
+      const float nb = fmaxf(base, base_of(top));
+      if (__any(is_far(nb))) limit = -__builtin_inff();
       const float f = exp2_hw(base - nb);
       sum *= f;
 #pragma unroll
       for (int m = 0; m < MT; ++m) o[m] *= f;
       base = nb;
-      exponents(nb);
+      if (limit == kTop) {
+        exponents(nb);
+      } else {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) e[n][i] = less_base(e[n][i], nb);
+      }
     }
 #pragma unroll
     for (int n = 0; n < NB; ++n) {

@@ -173,3 +173,48 @@ def test_attend_takes_every_token_once(Hq, Hkv, D, page, shape, q_off, max_kv, f
         O, count = c.rows(i, np.clip(off + np.arange(n) + 1, 0, L), Hq // Hkv)
         rows = slice(starts[i], starts[i + 1])
         assert kx.close(got[rows], lse[rows], O, count, f32).all(), i
+
+
+# ---------------------------------------------------------------- far scores
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("queries", [1, 40])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attend_scores_of_any_size(sign, queries, f32):
+    """Shown tokens share one score, the largest, of 2^14 to 2^120: where binary32 has no fractions left of it too, they
+    have equal weights and the hidden ones none."""
+    import torch
+    from shard_decomposed_gemm_amd import KvCache
+    D, page, L = 64, 64, 3200
+    r = np.random.default_rng(sign + 1)
+    kn, vn, shown = kx.tokens(r, (L, 1), D)
+    level = 15 if sign > 0 else 7
+    kn = np.maximum(kn, level) if sign < 0 else np.minimum(kn, 15)
+    at = r.integers(0, D, (L, 1, 1))
+    np.put_along_axis(kn, at, np.full((L, 1, 1), 15 if sign < 0 else 7, dtype=np.uint8), -1)  # 8 or more off the level
+    kn[0], shown[0] = level, True
+    kn[shown] = level
+    kv = KvCache(2, 1, D, page_tokens=page, num_pages=L // page)
+    pages, table = _dev(kx.pack(kn, vn, page)), _dev(np.arange(L // page, dtype=np.int32)[None])
+    q = torch.full((queries, 2, D), float(sign), dtype=torch.float16, device=gu.dev())
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=gu.dev())  # noqa: E731
+    last = np.arange(L - queries, L)
+    n = np.cumsum(shown[:, 0])[last]
+    O = np.cumsum(shown * vn[:, 0].astype(np.int64), 0)[last] / n[:, None]
+    for k in (4, 8, 13, 14, 15, 16, 17, 18, 19, 20, 21, 22, 24, 27, 33, 50, 90, 110):
+        for scale in (2.0 ** k, 1.37 * 2.0 ** k):
+            scale = float(np.float32(scale))
+            out = torch.empty(queries, 2, D, dtype=torch.float32 if f32 else torch.float16, device=gu.dev())
+            lse = torch.empty(queries, 2, device=gu.dev())
+            kv.attend(pages, q, i32(L), table, out, lse=lse, q_start=i32(0, queries), max_q=queries, scale=scale)
+            torch.cuda.synchronize()
+            kv.check()
+            got = out.cpu().numpy().astype(np.float64)
+            # equal weights, a power of two or that of a fraction that all share, cut or rounded alike: means, off by
+            # the weight's rounding, the sums' (1600 numbers in a row at most) and the output's
+            bound = O * ((2.0 ** -21 if f32 else 2.0 ** -11) + 3200 * kx.ROUND)
+            bound = bound + (O * 2.0 ** -23 if f32 else np.maximum(O * 2.0 ** -11, 2.0 ** -25))
+            assert (np.abs(got - O[:, None]) <= bound[:, None]).all(), (k, scale)
+            want = sign * level * D * scale + np.log(n)
+            # the factor, the product, the logarithm's sum and the product with ln 2
+            assert (np.abs(lse.cpu().numpy() - want[:, None]) <= np.abs(want[:, None]) * 5 * kx.ROUND + 2.0 ** -13).all(), (k, scale)
