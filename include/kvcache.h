@@ -134,7 +134,7 @@ typedef struct {
                                   kv_len - (its queries): they are the last of the cached tokens.
                                   0: every query sees all kv_len */
   int64_t max_kv;              /* the longest kv_len to expect, >= 1: it only chooses how work is split */
-  float scale;                 /* factor of q . k, finite */
+  float scale;                 /* factor of q . k, below 2^127 in size */
   int32_t out_f32;             /* out is binary32 (1) or binary16 (0) */
   void* out;                   /* T x Hq x D, contiguous, apart from q */
   float* lse;                  /* T x Hq, contiguous, or NULL */
@@ -146,12 +146,13 @@ typedef struct {
  *   lse = ln sum_j e^(S_j).
  * A row that sees no token: out = 0 and lse = -FLT_MAX, which the combine
  * takes as a partial without weight. Rows of q past the last sequence's are
- * left as they were in out and lse. Scores must fit binary32. Sums, maxima and
- * statistics in binary32. The softmax weights enter the product with the
- * values in binary16: with a binary32 out as two numbers, cut, which a weight
- * w is off by at most max(2^-21 w, 2^-36 of the row's largest weight) - over
- * L tokens of tiny weights up to L 2^-36 max |V| in out; with a binary16 out as
- * one, rounded: max(2^-11 w, 2^-37 of the largest). lse has all of every weight.
+ * left as they were in out and lse. Scores must be below 2^127 in size (times
+ * log2(e) they fit binary32). Sums, maxima and statistics in binary32. The
+ * softmax weights enter the product with the values in binary16: with a
+ * binary32 out as two numbers, cut, which a weight w is off by at most
+ * max(2^-21 w, 2^-36 of the row's largest weight) - over L tokens of tiny
+ * weights up to L 2^-36 max |V| in out; with a binary16 out as one, rounded:
+ * max(2^-11 w, 2^-37 of the largest). lse has all of every weight.
  * Reported by kvc_check: a page id outside the cache (its tokens count as not
  * seen), a length that is negative or does not fit the table (clamped), a
  * sequence with more than max_q queries, rows past T or a negative number of

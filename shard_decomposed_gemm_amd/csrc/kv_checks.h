@@ -112,7 +112,7 @@ inline int kv_check_attend(const KvLayout& L, const void* pages, const kvc_atten
   if (plan.items > kKvMaxItems) return kv_refuse(why, AGEMM_ESHAPE, "batch and max_q too large for one call");
   if (p->causal != 0 && p->causal != 1) return kv_refuse(why, AGEMM_EINVAL, "causal must be 0 or 1");
   if (p->out_f32 != 0 && p->out_f32 != 1) return kv_refuse(why, AGEMM_EINVAL, "out_f32 must be 0 or 1");
-  if (!isfinite(p->scale)) return kv_refuse(why, AGEMM_EINVAL, "scale must be finite");
+  if (!(fabsf(p->scale) < 0x1p127f)) return kv_refuse(why, AGEMM_EINVAL, "scale must be below 2^127 in size");
   if (p->table_width < 1 || p->table_stride < 0 || (p->table_stride > 0 && p->table_stride < p->table_width))
     return kv_refuse(why, AGEMM_EINVAL, "table_width must be positive and table_stride 0 or at least the width");
   if ((int64_t)p->batch * p->table_width > (int64_t{1} << 30) / (L.page_tokens / 32))
