@@ -14,8 +14,9 @@
 // Bound by HBM: 2 bytes in and out a query channel, 2 in and 1/2 out a key or
 // value channel, some 10 operations each. Measured on 16384 tokens of 64 + 2 x 8
 // heads (D 128, whole rotation): queries 112 us, 4.8 TB/s of the 4.96 that a
-// copy reaches; keys and values 51 us, 1.8 TB/s (their arithmetic: some 40
-// operations a channel, and one quad in ten again in binary64).
+// copy reaches; keys and values 51 us, 1.8 TB/s: some 40 operations a channel,
+// and one quad in ten again in binary64, keep the vector units busy 55 % of the
+// cycles, and a wave loads, works and stores one after the other.
 #include <type_traits>
 
 #include "kv_internal.h"

@@ -376,14 +376,15 @@ __device__ inline void store_out(void* out, int64_t at, const float (&v)[N]) {
 // times), and a block of 32 keys as two tiles of 16. The next block's keys are
 // loaded when this block's are used up, its values likewise, so that two
 // workgroups a CU keep some 140 KB in flight. A block costs a wave some 260
-// vector and 32 matrix instructions (D 128); the vector units are what a CU
-// with few waves waits for.
+// vector and 32 matrix instructions (D 128).
 //
 // Measured, this kernel alone: 262144 tokens of 8 kv heads (D 128, 12 rows) in
-// 50.5 us, 5.65 TB/s of 7.14 that a plain read reaches; 32768 tokens of 96 kv
-// heads (one row) in 71 us, 6.0 TB/s; 777 tokens, 8.4 us, all of it latency.
+// 52 us, 5.5 TB/s of 7.14 that a plain read reaches; 32768 tokens of 96 kv
+// heads (one row) in 72 us, 5.9 TB/s; 777 tokens, 8.2 us, all of it latency.
 // The rest of each workgroup is lengths, page ids and first loads (3 to 6 us,
-// one after the other) and the waves' join (3 us).
+// one after the other) and the waves' join (3 us). A ragged batch (64 sequences
+// up to 8192 tokens, 36 us for 18 of bytes) waits for its last runs: vector units
+// are busy 43 % of the cycles, matrix units 7 %.
 constexpr int kWaves = kKvWaves;
 
 template <int D>
@@ -690,16 +691,19 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
 // overlap, which short items need more (kv_many_wide has the figures).
 //
 // Measured: 2 x 2048 queries of 64 heads (8 kv heads, D 128) on 8192 tokens in
-// 966 to 1070 us (box to box), 962 GFLOP at 0.90 to 1.00 PFLOP/s; a 8192^3
-// library product reaches 1.14 on the same part. Matrix units busy 45 % and
-// vector units 51 % of the cycles, at 1.9 GHz of 2.4: power seems to hold the clock.
+// 966 to 1085 us from part to part (call after call; the first twenty after a
+// pause take up to 1400, until the clock settles), 962 GFLOP at 0.89 to 1.00
+// PFLOP/s; a 8192^3 library product reaches 1.14. Matrix units busy 44 % and
+// vector units 50 % of the cycles, at 1.9 GHz of 2.4: power seems to hold the clock.
+// Binary32 out, which has twice the value products: 1394 us. D 64: 708 (binary32
+// 883), D 256 with half the heads: 1552 (1850), one block a tile there.
 template <int D, int W, bool F32>
 __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel(KvAttendArgs a) {
   constexpr int KB = W * 64 / D;   // blocks of a tile
   constexpr int KS = D / 16;       // inner steps of the scores
   constexpr int MT = D / 32;       // channel tiles of the output
   constexpr int RN = D / 32;       // 16-byte pieces of a key row
-  constexpr int KFRAG = KB * KS * 64, VFRAG = KB * 2 * MT * 64;  // 16-byte operands of a tile: 1024 each
+  constexpr int KFRAG = KB * KS * 64, VFRAG = KB * 2 * MT * 64;  // 16-byte operands of a tile: 256 W each
   __shared__ half8v kl[2][KFRAG];
   __shared__ half8v vl[2][VFRAG];
 

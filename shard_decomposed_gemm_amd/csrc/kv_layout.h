@@ -49,7 +49,7 @@ inline int64_t kv_read_piece(const KvLayout& L) { return ((int64_t{1} << 28) - 6
 // head by head; a workgroup takes one run, and run i of the call leaves its
 // partial in slot i. With slots == items every item is one run.
 //
-// Many rows (many = 1): an item is a (sequence, tile of 128 rows, kv head);
+// Many rows (many = 1): an item is a (sequence, tile of 128 or 256 rows, kv head);
 // its blocks go in runs of `chunk` to `splits` workgroups at most (longer runs
 // where a sequence has more blocks than that), one slot per (item, run).
 struct KvPlan {
@@ -105,8 +105,10 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
   KvPlan p{};
   const int64_t rows = max_q * (L.Hq / L.Hkv), nblk = kv_expected_blocks(max_kv);
   // As many rows as the kernel for few rows holds, it takes: 16 x 4 queries of 64
-  // heads (8 kv heads, D 128) on 8192 tokens 44.5 us, the one for many 82; 16 x 2
-  // of 16 heads (2, D 256) 26, 77.
+  // heads (8 kv heads, D 128) on 8192 tokens 44 us, the one for many 82; 16 x 2
+  // of 16 heads (2, D 256) 26, 77. Rows above that fill a third of a 128-row tile
+  // at first: 5 such queries take 82 us, 8 85, 16 111; of D 256 3 take 76, 8 90.
+  // A form between the two would be for them.
   p.many = rows > (L.D == 256 ? 16 : 32);
   p.rows = p.many ? 128 : rows > 16 ? 32 : 16;
   p.tiles = (int32_t)(p.many ? (rows + p.rows - 1) / p.rows : 1);
@@ -194,8 +196,10 @@ inline int64_t kv_many_items(const KvPlan& p, const KvLayout& L, int64_t batch, 
 
 // Many rows, nothing to join: tiles of 256 rows (kv_attend.hip says why) where
 // the rows still make four items a CU, of 64 blocks or more at the longest. 2 x
-// 2048 queries on 8192 tokens (64 heads, 8 kv heads): 1105 us, in 128 rows 1191;
-// 4 x 4096 (32, 8): 696, 728; but 1 x 4096: 248, 207, and 64 x 256: 169, 123.
+// 2048 queries on 8192 tokens (64 heads, 8 kv heads): 1085 us, in 128 rows 1190;
+// 4 x 4096 on themselves (32, 8): 679, 714; but 64 x 256: 169, 128. With two items
+// a CU, 1 x 4096 on itself, 256 rows would take 173, 128 take 197: the limit of
+// four is on the safe side.
 inline void kv_many_wide(KvPlan& p, const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int64_t tokens,
                          int num_cus) {
   if (!p.many || p.splits > 1 || L.D != 128 || max_kv < 64 * 32) return;
