@@ -163,8 +163,8 @@ inline KvPlan kv_attend_plan(const KvLayout& L, int64_t batch, int64_t max_q, in
 // queries and max_kv tokens. (The plan's own need is not monotone: calls with
 // fewer items have more runs an item, calls with many none.) Few rows: an item
 // count that still splits, and the most runs that kv_attend_plan gives as many
-// items or fewer. Many rows: splits > 1 takes items < places, and then
-// items x splits < places + items.
+// items or fewer. Many rows: splits > 1 takes items x nblk <= places x (nblk - 1),
+// and then items x splits < places + items.
 inline int64_t kv_attend_bound(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
   const int64_t G = L.Hq / L.Hkv, nblk = kv_expected_blocks(max_kv);
   const int few = L.D == 256 ? 16 : 32;  // rows of the kernel for few
@@ -181,7 +181,7 @@ inline int64_t kv_attend_bound(const KvLayout& L, int64_t batch, int64_t max_q, 
     floats = most(floats, (items + most(runs, places)) * rows * (L.D + 2));
   }
   const int64_t places = (int64_t)num_cus * 2;
-  const int64_t items = least(batch * L.Hkv * ((max_q * G + 127) / 128), places - 1);
+  const int64_t items = least(batch * L.Hkv * ((max_q * G + 127) / 128), (nblk - 1) * places / nblk);
   if (max_q * G > few && items >= L.Hkv && nblk > 8)
     floats = most(floats, least(places + items - 1, items * least(kKvMaxSplits, (nblk + 7) / 8)) * 128 * (L.D + 2));
   return floats * 4;

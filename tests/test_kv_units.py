@@ -57,27 +57,28 @@ def _sizes(top):
     return sorted({x for x in few if x <= top} | {top})
 
 
+@pytest.mark.parametrize("cus", [256, 32, 304])
 @pytest.mark.parametrize("Hq,Hkv,D", [(64, 8, 128), (32, 8, 128), (96, 8, 128), (96, 96, 128), (12, 1, 128), (1, 1, 64),
                                       (17, 1, 64), (32, 4, 64), (16, 2, 256), (8, 8, 256), (40, 2, 128), (1024, 1024, 64),
                                       (600, 600, 128), (1024, 1, 64)])
-def test_workspace_of_bounds_holds_every_smaller_call(units, Hq, Hkv, D):
+def test_workspace_of_bounds_holds_every_smaller_call(units, Hq, Hkv, D, cus):
     """A server's workspace, made once for its largest batch, chunk and length, serves its smaller steps too."""
     r = np.random.default_rng(Hq + D)
     for batch, max_q, max_kv in ((256, 1, 8192), (64, 1, 8192), (8, 2048, 8192), (4, 2048, 16384), (512, 64, 40000),
                                  (700, 4, 1 << 20), (1, 1, 262144), (3, 40, 1000), (2, 5, (1 << 31) - 1), (8192, 700, 33),
                                  (1, 1, 1), (0, 1, 8192)):
-        size = units.kvu_workspace(Hq, Hkv, D, batch, max_q, max_kv, 256)
+        size = units.kvu_workspace(Hq, Hkv, D, batch, max_q, max_kv, cus)
         pick = lambda top, n: r.choice(_sizes(top), min(n, len(_sizes(top))), replace=False).tolist() + [top]  # noqa: E731
         worst = 0
         for b in pick(batch, 60) if batch else [0]:
             for q in pick(max_q, 24):
                 for kv in pick(max_kv, 24):
-                    worst = max(worst, units.kvu_needs(Hq, Hkv, D, b, q, kv, 256))
+                    worst = max(worst, units.kvu_needs(Hq, Hkv, D, b, q, kv, cus))
         assert worst <= size, (batch, max_q, max_kv)
         # and it is no more than calls within the bounds come to, but for a factor
         assert size <= 4 * worst + (1 << 20), (batch, max_q, max_kv, worst, size)
         for b, q, kv in ((batch // 2, max_q, max_kv), (batch, max(1, max_q // 3), max_kv), (batch, max_q, max(1, max_kv - 1))):
-            assert units.kvu_workspace(Hq, Hkv, D, b, q, kv, 256) <= size
+            assert units.kvu_workspace(Hq, Hkv, D, b, q, kv, cus) <= size
 
 
 @pytest.mark.parametrize("Hq,Hkv,D", [(64, 8, 128), (96, 96, 128), (1, 1, 64), (16, 2, 256), (1024, 1, 64)])
