@@ -18,8 +18,8 @@
 // The running maximum m of the softmax is replaced only when a score passes it
 // by 2^3: weights are kept as 2^(x - m + 12) (x the score in units of log 2),
 // at most 2^15, so the usual block needs no maximum across lanes and no
-// rescaling. The largest weight is at least 2^12; binary16 has multiples of
-// 2^-24 at the least, 2^-36 of that.
+// rescaling. The largest weight is at least 2^12 (short of scores of 2^26, base_of);
+// binary16 has multiples of 2^-24 at the least, 2^-36 of that.
 //
 // With binary16 outputs a weight enters the product rounded to binary16 once
 // (off by 2^-11 of it, as the output itself is, or half of 2^-24): a second
