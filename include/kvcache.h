@@ -1,6 +1,7 @@
 /*
  * C-ABI of the 4-bit paged key/value cache on one GPU (gfx950): appending to
- * it, attention over it, reading it back.
+ * it, attention over it, reading it back; and a step of speculative decoding on
+ * it: drafted tokens in a tree, their attention, verification and commit.
  *
  * It makes what the Flash-Decode combine (fdcombine.h) takes: each of W ranks
  * attends over its own shard of the cache (kvc_attend with a binary32 output)
@@ -169,6 +170,136 @@ int kvc_attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* args, voi
  * batch, chunk and length serves its smaller calls too, which may need more
  * than the largest one does. */
 int kvc_attend_workspace(const kvc_ctx* ctx, int32_t batch, int32_t max_q, int64_t max_kv, int64_t* bytes);
+
+/* A step with drafted tokens. The tokens of a sequence's step form a tree of up
+ * to 1024 nodes, in an order in which parents come first. Node 0 is the token
+ * that the last step decided, whose keys and values are not cached yet; every
+ * other node is a draft of the token that follows its parent. The nodes are the
+ * rows q_start[i] .. q_start[i + 1] - 1 of sequence i, and node j's key and value
+ * lie at place kv_len + j of the sequence until they are committed:
+ *   kvc_tree         masks, positions and slots of the nodes;
+ *   kvc_append       of the nodes with those, in every layer;
+ *   kvc_attend_tree  with the masks, in every layer;
+ *   kvc_verify       against the target's probabilities: the accepted path and
+ *                    the token that follows it;
+ *   kvc_commit       the path's keys and values go to places kv_len, kv_len + 1,
+ *                    ..., in all layers; the lengths that the next step starts with.
+ * Nothing of it needs the host, so a step can be captured into a graph. Up to
+ * 2^20 sequences and 2^23 rows a call. */
+
+/* Arguments of kvc_tree. */
+typedef struct {
+  int32_t batch;               /* sequences, >= 0 */
+  int32_t max_q;               /* upper bound of the nodes of one tree, 1 .. 64 mask_words */
+  int64_t tokens;              /* rows T of parent and of the outputs but total_len */
+  const int32_t* q_start;      /* batch + 1, device: sequence i's nodes are rows q_start[i] .. q_start[i+1]-1 */
+  const int32_t* kv_len;       /* batch, device: cached tokens before the tree */
+  const int32_t* parent;       /* T, device: the node that a node follows, counted from its sequence's first
+                                  row; less than its own number; -1: it follows the cached tokens */
+  const int32_t* page_table;   /* batch rows of table_width page ids, table_stride apart; required with slots */
+  int64_t table_stride;        /* in elements, >= table_width or 0 (a shared row) */
+  int32_t table_width;         /* >= 1 */
+  int32_t mask_words;          /* 1 .. 16 */
+  uint64_t* mask;              /* T x mask_words, contiguous: bit j % 64 of word j / 64 is node j */
+  int64_t* positions;          /* T, or NULL */
+  int64_t* slots;              /* T, or NULL */
+  int32_t* total_len;          /* batch, or NULL */
+} kvc_tree_args;
+
+/* For each node: its mask has itself and its ancestors, its position is kv_len +
+ * the number of its ancestors, its slot that of place kv_len + its number in the
+ * page table. total_len = kv_len + the sequence's nodes. Rows of no sequence get
+ * an empty mask, position 0 and slot -1, so that kvc_append keeps nothing of
+ * them. The outputs must lie apart from the inputs and each other.
+ * Reported by kvc_check: a parent that is no earlier node (taken as -1); a page
+ * id outside the cache (slot -1); a sequence with more than max_q nodes, rows
+ * past T or a negative number of them, or whose tree does not fit behind its
+ * length (a negative one, or too long for the table): those of its rows that
+ * there are count as rows of no sequence, and total_len is kv_len. */
+int kvc_tree(kvc_ctx* ctx, const kvc_tree_args* args, void* stream);
+
+/* kvc_attend (causal = 1) with a tree: query i of a sequence sees the first q_off
+ * of its cached tokens, and token q_off + j where bit j of row i of `mask` is set
+ * (no token past kv_len; q_off NULL stands for kv_len - its queries). mask: T x
+ * mask_words (1 .. 16), contiguous, device, as kvc_tree leaves it. The queries
+ * need not be all of the tree's nodes: with q_off given, those of its last level
+ * attend to what is cached of the others. Everything else as in kvc_attend; the
+ * workspace too (kvc_attend_workspace). */
+int kvc_attend_tree(kvc_ctx* ctx, const void* pages, const kvc_attend_args* args, const uint64_t* mask,
+                    int32_t mask_words, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Arguments of kvc_verify. */
+typedef struct {
+  int32_t batch;               /* sequences, >= 0 */
+  int32_t max_q;               /* upper bound of the nodes of one tree, 1 .. 1024 */
+  int64_t tokens;              /* rows T of token, parent, p, q, u and path */
+  const int32_t* q_start;      /* batch + 1, device */
+  const int32_t* parent;       /* T, device, as in kvc_tree; nodes that do not descend from node 0 are left out */
+  const int64_t* token;        /* T, device: the drafted tokens; node 0's is not read */
+  const float* p;              /* T x vocab, rows p_stride apart: the target's probabilities of the token that
+                                  follows a node */
+  const float* q;              /* T x vocab, rows q_stride apart: the draft's, from which a node's children were
+                                  drawn one after another without replacement; NULL: the children are certain */
+  int64_t p_stride, q_stride;  /* in elements, >= vocab or 0 (a shared row) */
+  int64_t vocab;               /* 1 .. 2^28 */
+  const float* u;              /* T, device: random numbers in [0, 1), one for each draft; node 0's is for the
+                                  token at the end */
+  int32_t max_children;        /* the most children of one node to expect, >= 1: it only chooses how work is split */
+  int32_t* path;               /* T: the accepted nodes, node 0 first, then -1 */
+  int32_t* count;              /* batch: their number */
+  int64_t* next;               /* batch: the token that follows them */
+} kvc_verify_args;
+
+/* Accepts drafts so that the accepted tokens and the one after them are
+ * distributed as the target's are. At a node, from node 0 on, its children c are
+ * tried in their order. With x = token[c], and for the first child w = p, d = q:
+ * c is accepted if u[c] d(x) < w(x), and the walk goes on from it; else w becomes
+ * max(0, w - d), normalised, and d loses x and is normalised (a whole row of p or
+ * q counts as a sum of 1). Without q, d is 1 at x and 0 elsewhere for each child. Where no child is accepted (or none is
+ * there) the walk ends, and next is the smallest token t with
+ *   sum_{s <= t} w(s) > u[node 0] sum_s w(s).
+ * A child whose token an earlier one of the same parent had is passed over, and so
+ * are those behind children that had all of d or left w 0 everywhere; next is
+ * drawn from p then.
+ * In 64 bits; the weights w of the sums as multiples of 2^-50, whose sums are
+ * exact below 8 in any order: equal calls give equal results however they are
+ * split. Entries of p, q outside 0..1 count as the nearer end, NaN as 0; so does u,
+ * its upper end the largest number below 1.
+ * A sequence without rows has count 0 and next -1. Reported by kvc_check: a
+ * parent as in kvc_tree (of node 0, anything but -1), a drafted token outside the
+ * vocabulary (passed over), a row of p without any weight (next -1), and rows as
+ * in kvc_tree (count 0, next -1, path as it was). workspace: at least
+ * kvc_verify_workspace bytes of bounds that hold this call's batch and vocab,
+ * 16-byte aligned; its contents before and after mean nothing. */
+int kvc_verify(kvc_ctx* ctx, const kvc_verify_args* args, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace that holds every kvc_verify call of up to `batch` sequences and `vocab` tokens. */
+int kvc_verify_workspace(const kvc_ctx* ctx, int32_t batch, int64_t vocab, int64_t* bytes);
+
+/* Arguments of kvc_commit. */
+typedef struct {
+  int32_t batch;               /* sequences, >= 0 */
+  int32_t max_q;               /* upper bound of the nodes of one tree, 1 .. 1024 */
+  int64_t tokens;              /* rows T of path */
+  const int32_t* q_start;      /* batch + 1, device */
+  const int32_t* kv_len;       /* batch, device: cached tokens before the tree */
+  const int32_t* path;         /* T, device: the accepted nodes of a sequence in its first rows, ascending */
+  const int32_t* count;        /* batch, device: their number, 0 .. the sequence's nodes */
+  const int32_t* page_table;   /* as in kvc_tree; the trees of two sequences share no slot */
+  int64_t table_stride;
+  int32_t table_width;
+  int32_t* new_len;            /* batch, or NULL: kv_len + count; apart from the inputs */
+} kvc_commit_args;
+
+/* Moves the key and value of node path[i] of each sequence to place kv_len + i of
+ * it, bit for bit, in each of `layers` caches of the context's shape (pages: a
+ * host array of as many device pointers, no two of them equal), with the same
+ * page table. Other slots stay as they are.
+ * Reported by kvc_check, and that sequence left, its new_len kv_len: rows and
+ * lengths as in kvc_tree, a count out of its range, a path that is not
+ * ascending or leaves the tree. A page id outside the cache is reported, and the
+ * nodes on it or bound for it are not moved. */
+int kvc_commit(kvc_ctx* ctx, void* const* pages, int32_t layers, const kvc_commit_args* args, void* stream);
 
 /* Copies the keys and values of the tokens in `slots` (T, device) out of the
  * cache as the binary16 numbers they stand for: k_out and v_out T x Hkv x D,

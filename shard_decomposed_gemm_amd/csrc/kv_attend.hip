@@ -156,10 +156,12 @@ struct Sequence {
   int n;         // its queries, 0 if they cannot be used
   int len;       // cached tokens
   int64_t off;   // the first query sees off + 1 tokens
+  int least;     // with a tree: its nodes less one, which are the most that any query sees beyond off; else 0
 
+  __device__ int below_tree() const { return off < 0 ? 0 : off > len ? len : (int)off; }  // seen by every query
   __device__ int blocks() const { return n > 0 ? kv_blocks(seen(n - 1)) : 0; }  // that its last query sees
-  __device__ int seen(int i) const {
-    const int64_t v = off + i + 1;
+  __device__ int seen(int i) const {  // with a tree: at most
+    const int64_t v = off + (i > least ? i : least) + 1;
     return v < 0 ? 0 : v > len ? len : (int)v;
   }
 };
@@ -199,7 +201,43 @@ __device__ inline Sequence sequence(const KvAttendArgs& a, int b, bool tell) {
   if (!fits && tell) kv_report(a.err, kKvLength, b, len);
   s.len = len < 0 ? 0 : len <= most ? len : (int)most;
   if (a.causal && !a.q_off) s.off = (int64_t)s.len - n;
+  s.least = a.tree ? 64 * a.tree_words - 1 : 0;
   return s;
+}
+
+// The tree's nodes that a row sees: the first 64 in registers, which is all for
+// most trees, the others where they are asked for.
+struct TreeRow {
+  const uint32_t* mask;
+  uint32_t m0, m1;
+};
+__device__ inline TreeRow tree_row(const KvAttendArgs& a, int64_t row) {
+  TreeRow t;
+  t.mask = reinterpret_cast<const uint32_t*>(a.tree) + row * (2 * a.tree_words);
+  t.m0 = t.mask[0];
+  t.m1 = t.mask[1];
+  return t;
+}
+// Bit i: the row sees token first + i. first the same in all lanes; ones below
+// the tree, zeros past the sequence's end.
+__device__ inline uint32_t tree_seen(const KvAttendArgs& a, const TreeRow& t, const Sequence& s, int first) {
+  const int64_t rel = first - s.off;
+  const int left = s.len - first;
+  if (left <= 0 || rel >= 64 * a.tree_words) return 0;
+  uint32_t v = ~0u;
+  if (rel > -32) {
+    const int i = (int)(rel >> 5);
+    uint32_t lo, hi;
+    if (i < 1) {
+      lo = i < 0 ? ~0u : t.m0;
+      hi = i < 0 ? t.m0 : t.m1;
+    } else {
+      lo = t.mask[i];
+      hi = i + 1 < 2 * a.tree_words ? t.mask[i + 1] : 0u;
+    }
+    v = (uint32_t)(((uint64_t)hi << 32 | lo) >> (rel & 31));
+  }
+  return left < 32 ? v & ((1u << left) - 1) : v;
 }
 
 // Sum of x over this lane and the earlier ones.
@@ -236,6 +274,7 @@ __device__ inline Sequence of_lane(const Sequence& s, int l) {
   r.n = __builtin_amdgcn_readlane(s.n, l);
   r.len = __builtin_amdgcn_readlane(s.len, l);
   r.off = wide(s.off);
+  r.least = __builtin_amdgcn_readlane(s.least, l);
   return r;
 }
 
@@ -441,7 +480,7 @@ __device__ inline void load_values(RawValues<D>& r, __amdgpu_buffer_rsrc_t blk, 
   r.b = __builtin_bit_cast(uint4v, __builtin_amdgcn_raw_buffer_load_b128(blk, pair + 192, 32 * D, kNontemporal));
 }
 
-template <int D, int NT, bool F32>
+template <int D, int NT, bool F32, bool TREE>
 __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void kv_attend_few_kernel(KvAttendArgs a) {
   constexpr int MT = D / 16;
   constexpr int R = 16 * NT, LD = D + 4;  // rows of an item; a row's floats in LDS, padded off the same banks
@@ -504,7 +543,8 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   float4v o[NT][MT];  // O^T: row 4 quarter + i of tile m is channel (4 quarter + i) D / 16 + m
   float base[NT];     // m - kShift
   float sum[NT];      // of this lane's weights
-  int seen[NT];       // keys that the column's row sees
+  int seen[NT];       // keys that the column's row sees (without a tree)
+  TreeRow tree[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     // Columns past the last row repeat row 0: loads that some lanes leave out
@@ -514,13 +554,14 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
     const _Float16* src = a.q + (seq.row0 + i) * a.q_ts + (int64_t)(h * G + r - i * G) * a.q_hs + quarter * (D / 4);
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) q[n][x] = query_operand(src + 8 * x);
-    seen[n] = seq.seen(i);
+    if constexpr (TREE) tree[n] = tree_row(a, seq.row0 + i);
+    else seen[n] = seq.seen(i);
     base[n] = kNoMax;
     sum[n] = 0.f;
 #pragma unroll
     for (int m = 0; m < MT; ++m) o[n][m] = float4v{0.f, 0.f, 0.f, 0.f};
   }
-  const int whole = seq.seen(0) >> 5;  // blocks that every row sees whole
+  const int whole = TREE ? seq.below_tree() >> 5 : seq.seen(0) >> 5;  // blocks that every row sees whole
   const float factor = a.scale * kLog2e;
   float limit = kTop;  // of the exponents, the same in all lanes; -inf once some row's base is far
   const Bits bits;
@@ -552,15 +593,19 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
     for (int n = 0; n < NT; ++n) {
       float e[8];
       float top;
-      int left = (end > 0 ? seen[n] - j * 32 : 0) - (int)quarter * 4;
+      int left = TREE ? 0 : (end > 0 ? seen[n] - j * 32 : 0) - (int)quarter * 4;
+      uint32_t bits_seen = 0;
+      if constexpr (TREE)
+        if (hide && end > 0) bits_seen = tree_seen(a, tree[n], seq, j * 32) >> (quarter * 4);
       auto exponents = [&](float bs) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] = __builtin_fmaf(s[n][i >> 2][i & 3], factor, -bs);
         if (hide) {
-          asm volatile("" : "+v"(left));  // keeps the comparisons in this branch
+          asm volatile("" : "+v"(left), "+v"(bits_seen));  // keeps the comparisons in this branch
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if ((i >> 2) * 16 + (i & 3) >= left) e[i] = -__builtin_inff();
+            if (TREE ? !(bits_seen >> ((i >> 2) * 16 + (i & 3)) & 1) : (i >> 2) * 16 + (i & 3) >= left)
+              e[i] = -__builtin_inff();
         }
         top = max8(e);
       };
@@ -697,7 +742,7 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
 // vector units 50 % of the cycles, at 1.9 GHz of 2.4: power seems to hold the clock.
 // Binary32 out, which has twice the value products: 1394 us. D 64: 708 (binary32
 // 883), D 256 with half the heads: 1552 (1850), one block a tile there.
-template <int D, int W, bool F32>
+template <int D, int W, bool F32, bool TREE>
 __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel(KvAttendArgs a) {
   constexpr int KB = W * 64 / D;   // blocks of a tile
   constexpr int KS = D / 16;       // inner steps of the scores
@@ -742,9 +787,11 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
     for (int u = 0; u < KS; ++u) q[u] = live ? query_operand(src + 16 * u) : half8v{};
   }
   const int seen = live ? seq.seen(qi) : seq.len;
+  TreeRow tree;
+  if constexpr (TREE) tree = tree_row(a, seq.row0 + qi);
   // Wave-uniform: blocks below `whole` are seen whole by every row of the wave, none at or past `none`.
   const int w0 = r0 + wave * 32, w1 = (w0 + 31 < rows ? w0 + 31 : rows - 1);
-  const int whole = w0 < rows ? seq.seen(w0 / G) >> 5 : 0;
+  const int whole = w0 >= rows ? 0 : TREE ? seq.below_tree() >> 5 : seq.seen(w0 / G) >> 5;
   const int none = w0 < rows ? kv_blocks(seq.seen(w1 / G)) : 0;
   const float factor = a.scale * kLog2e;
   const Bits bits;
@@ -838,11 +885,19 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
     // A block without a page, or past the run, is hidden from every row.
     bool hide = j + NB > whole;
     int left[NB];
+    bool here[NB];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
-      const bool here = j + n < j1 && uniform(there[buf][kb + n]);
-      hide |= !here;
-      left[n] = here ? seen - ((j + n) * 32 + hh * 4) : 0;
+      here[n] = j + n < j1 && uniform(there[buf][kb + n]);
+      hide |= !here[n];
+      left[n] = !TREE && here[n] ? seen - ((j + n) * 32 + hh * 4) : 0;
+    }
+    if constexpr (TREE) {  // bits of the tokens seen, in left
+      if (hide) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+          if (here[n]) left[n] = (int)(tree_seen(a, tree, seq, (j + n) * 32) >> (hh * 4));
+      }
     }
     float e[NB][16];
     float top;
@@ -857,7 +912,8 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
           asm volatile("" : "+v"(left[n]));  // keeps the comparisons in this branch
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (8 * (i >> 2) + (i & 3) >= left[n]) e[n][i] = -__builtin_inff();
+            if (TREE ? !((uint32_t)left[n] >> (8 * (i >> 2) + (i & 3)) & 1) : 8 * (i >> 2) + (i & 3) >= left[n])
+              e[n][i] = -__builtin_inff();
         }
       }
       top = max3(max8(e[0]), max8(e[0] + 8), max8(e[NB - 1] + 8));
@@ -1063,34 +1119,40 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendAr
   if (a.lse && d == 0) a.lse[row] = sums[r] != 0.f ? (tops[r] + log2f(sums[r])) * kLn2 : kLowest;
 }
 
-template <int D, bool F32>
+template <int D, bool F32, bool TREE>
 hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
   const int64_t items = a.plan.many ? kv_many_items(a.plan, a.L, a.batch, a.tokens) : a.plan.items;
   const dim3 grid((unsigned)(a.plan.many ? items : a.plan.slots), (unsigned)a.plan.splits);
   hipError_t e = hipErrorInvalidValue;
   if (a.plan.many && a.plan.rows == 128) {
-    e = kv_launch(kv_attend_many_kernel<D, 4, F32>, grid, 256, s, a);
+    e = kv_launch(kv_attend_many_kernel<D, 4, F32, TREE>, grid, 256, s, a);
   } else if (a.plan.many) {
-    if constexpr (D == 128) e = kv_launch(kv_attend_many_kernel<D, 8, F32>, grid, 512, s, a);
+    if constexpr (D == 128) e = kv_launch(kv_attend_many_kernel<D, 8, F32, TREE>, grid, 512, s, a);
   } else if (a.plan.rows == 16) {
-    e = kv_launch(kv_attend_few_kernel<D, 1, F32>, grid, kWaves * 64, s, a);
+    e = kv_launch(kv_attend_few_kernel<D, 1, F32, TREE>, grid, kWaves * 64, s, a);
   } else if constexpr (D <= 128) {
-    e = kv_launch(kv_attend_few_kernel<D, 2, F32>, grid, kWaves * 64, s, a);
+    e = kv_launch(kv_attend_few_kernel<D, 2, F32, TREE>, grid, kWaves * 64, s, a);
   }
   if (a.plan.ws_bytes > 0 && e == hipSuccess)
     e = kv_launch(kv_attend_join_kernel<D, F32>, dim3((unsigned)items, (unsigned)a.plan.join_groups), kJoinThreads, s, a);
   return e;
 }
 
+template <bool F32, bool TREE>
+hipError_t launch_out(const KvAttendArgs& a, hipStream_t s) {
+  switch (a.L.D) {
+    case 64: return launch_d<64, F32, TREE>(a, s);
+    case 128: return launch_d<128, F32, TREE>(a, s);
+    case 256: return launch_d<256, F32, TREE>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
 }  // namespace
 
 hipError_t launch_kv_attend(const KvAttendArgs& a, bool out_f32, hipStream_t s) {
-  switch (a.L.D) {
-    case 64: return out_f32 ? launch_d<64, true>(a, s) : launch_d<64, false>(a, s);
-    case 128: return out_f32 ? launch_d<128, true>(a, s) : launch_d<128, false>(a, s);
-    case 256: return out_f32 ? launch_d<256, true>(a, s) : launch_d<256, false>(a, s);
-    default: return hipErrorInvalidValue;
-  }
+  if (a.tree) return out_f32 ? launch_out<true, true>(a, s) : launch_out<false, true>(a, s);
+  return out_f32 ? launch_out<true, false>(a, s) : launch_out<false, false>(a, s);
 }
 
 }  // namespace agemm

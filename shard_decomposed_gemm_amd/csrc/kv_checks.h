@@ -132,6 +132,96 @@ inline int kv_check_attend(const KvLayout& L, const void* pages, const kvc_atten
   return AGEMM_OK;
 }
 
+constexpr int64_t kKvMaxSequences = int64_t{1} << 20;  // of a call with trees: grids stay below 2^32 threads
+
+inline int kv_check_mask(const kvc_attend_args* p, const uint64_t* mask, int32_t words, char* why) {
+  if (!p) return kv_refuse(why, AGEMM_EINVAL, "args must be non-NULL");
+  if (words < 1 || words > kKvMaskWords) return kv_refuse(why, AGEMM_EINVAL, "mask_words must be 1 to %d", kKvMaskWords);
+  if (p->causal != 1) return kv_refuse(why, AGEMM_EINVAL, "causal must be 1 with a tree");
+  if (p->batch > 0 && p->tokens > 0 && (!mask || !kv_natural(mask)))
+    return kv_refuse(why, AGEMM_EINVAL, "mask must be non-NULL and aligned to its elements");
+  return AGEMM_OK;
+}
+
+// What the calls with trees have in common.
+inline int kv_check_nodes(int32_t batch, int32_t max_q, int64_t tokens, char* why) {
+  if (batch < 0 || tokens < 0) return kv_refuse(why, AGEMM_EINVAL, "batch and tokens must not be negative");
+  if (max_q < 1 || max_q > kKvNodes) return kv_refuse(why, AGEMM_EINVAL, "max_q must be 1 to %d", kKvNodes);
+  if (tokens > kKvMaxTokens || batch > kKvMaxSequences)
+    return kv_refuse(why, AGEMM_ESHAPE, "more than %lld rows or %lld sequences in a call", (long long)kKvMaxTokens,
+                     (long long)kKvMaxSequences);
+  return AGEMM_OK;
+}
+inline int kv_check_table(const int32_t* table, int64_t stride, int32_t width, char* why) {
+  if (!table || !kv_natural(table)) return kv_refuse(why, AGEMM_EINVAL, "page_table must be non-NULL and aligned to its elements");
+  if (width < 1 || stride < 0 || (stride > 0 && stride < width) || stride > kKvMaxStride)
+    return kv_refuse(why, AGEMM_EINVAL, "table_width must be positive and table_stride 0 or at least the width");
+  return AGEMM_OK;
+}
+
+inline int kv_check_tree(const kvc_tree_args* p, char* why) {
+  if (!p) return kv_refuse(why, AGEMM_EINVAL, "args must be non-NULL");
+  int rc = kv_check_nodes(p->batch, p->max_q, p->tokens, why);
+  if (rc) return rc;
+  if (p->mask_words < 1 || p->mask_words > kKvMaskWords || p->max_q > 64 * p->mask_words)
+    return kv_refuse(why, AGEMM_EINVAL, "mask_words must be 1 to %d and hold max_q nodes", kKvMaskWords);
+  if (p->tokens == 0 && (p->batch == 0 || !p->total_len)) return kKvNothing;
+  if (p->batch > 0 && (!p->q_start || !p->kv_len)) return kv_refuse(why, AGEMM_EINVAL, "q_start and kv_len must be non-NULL");
+  if (p->tokens > 0 && (!p->parent || !p->mask)) return kv_refuse(why, AGEMM_EINVAL, "parent and mask must be non-NULL");
+  for (const int32_t* x : {p->q_start, p->kv_len, p->parent, static_cast<const int32_t*>(p->total_len)})
+    if (!kv_natural(x)) return kv_refuse(why, AGEMM_EINVAL, "index arrays must be aligned to their elements");
+  if (!kv_natural(p->mask) || !kv_natural(p->positions) || !kv_natural(p->slots))
+    return kv_refuse(why, AGEMM_EINVAL, "mask, positions and slots must be aligned to their elements");
+  if (p->slots && p->batch > 0 && (rc = kv_check_table(p->page_table, p->table_stride, p->table_width, why))) return rc;
+  if (p->total_len && (p->total_len == p->kv_len || p->total_len == p->q_start))
+    return kv_refuse(why, AGEMM_EINVAL, "total_len must lie apart from the inputs");
+  return AGEMM_OK;
+}
+
+inline int kv_check_verify(const kvc_verify_args* p, int64_t need, const void* workspace, int64_t workspace_bytes, char* why) {
+  if (!p) return kv_refuse(why, AGEMM_EINVAL, "args must be non-NULL");
+  const int rc = kv_check_nodes(p->batch, p->max_q, p->tokens, why);
+  if (rc) return rc;
+  if (p->vocab < 1 || p->vocab > (int64_t{1} << 28)) return kv_refuse(why, AGEMM_ESHAPE, "vocab must be 1 to 2^28");
+  if (p->max_children < 1) return kv_refuse(why, AGEMM_EINVAL, "max_children must be positive");
+  if (p->batch == 0) return kKvNothing;
+  if (!p->q_start || !p->count || !p->next) return kv_refuse(why, AGEMM_EINVAL, "q_start, count and next must be non-NULL");
+  if (p->tokens > 0 && (!p->parent || !p->token || !p->p || !p->u || !p->path))
+    return kv_refuse(why, AGEMM_EINVAL, "parent, token, p, u and path must be non-NULL");
+  for (int64_t s : {p->p_stride, p->q ? p->q_stride : 0})
+    if (s < 0 || (s > 0 && s < p->vocab) || s > kKvMaxStride)
+      return kv_refuse(why, AGEMM_EINVAL, "strides of p and q must be 0 or at least vocab");
+  if (!kv_natural(p->q_start) || !kv_natural(p->parent) || !kv_natural(p->token) || !kv_natural(p->p) || !kv_natural(p->q) ||
+      !kv_natural(p->u) || !kv_natural(p->path) || !kv_natural(p->count) || !kv_natural(p->next))
+    return kv_refuse(why, AGEMM_EINVAL, "arrays must be aligned to their elements");
+  if (!kv_aligned16(workspace) || workspace_bytes < need)
+    return kv_refuse(why, AGEMM_EINVAL, "workspace must be 16-byte aligned and hold %lld bytes", (long long)need);
+  return AGEMM_OK;
+}
+
+inline int kv_check_commit(const KvLayout& L, void* const* pages, int32_t layers, const kvc_commit_args* p, char* why) {
+  if (!p) return kv_refuse(why, AGEMM_EINVAL, "args must be non-NULL");
+  int rc = kv_check_nodes(p->batch, p->max_q, p->tokens, why);
+  if (rc) return rc;
+  if (layers < 0 || layers > 4096) return kv_refuse(why, AGEMM_EINVAL, "layers must be 0 to 4096");
+  if ((int64_t)p->batch * L.Hkv > (int64_t{1} << 25)) return kv_refuse(why, AGEMM_ESHAPE, "more than 2^25 sequences' heads in a call");
+  if (p->batch == 0 || (layers == 0 && !p->new_len)) return kKvNothing;
+  if (layers > 0 && !pages) return kv_refuse(why, AGEMM_EINVAL, "pages must be non-NULL");
+  for (int i = 0; i < layers; ++i)
+    if (!kv_aligned16(pages[i])) return kv_refuse(why, AGEMM_EINVAL, "pages of every layer must be non-NULL and 16-byte aligned");
+  for (int i = 0; i < layers; ++i)
+    for (int j = 0; j < i; ++j)
+      if (pages[i] == pages[j]) return kv_refuse(why, AGEMM_EINVAL, "layers %d and %d have the same pages", j, i);
+  if (!p->q_start || !p->kv_len || !p->count || (p->tokens > 0 && !p->path))
+    return kv_refuse(why, AGEMM_EINVAL, "q_start, kv_len, path and count must be non-NULL");
+  for (const int32_t* x : {p->q_start, p->kv_len, p->path, p->count, static_cast<const int32_t*>(p->new_len)})
+    if (!kv_natural(x)) return kv_refuse(why, AGEMM_EINVAL, "index arrays must be aligned to their elements");
+  if ((rc = kv_check_table(p->page_table, p->table_stride, p->table_width, why))) return rc;
+  if (p->new_len && (p->new_len == p->kv_len || p->new_len == p->count || p->new_len == p->q_start))
+    return kv_refuse(why, AGEMM_EINVAL, "new_len must lie apart from the inputs");
+  return AGEMM_OK;
+}
+
 inline int kv_check_read(const void* pages, int64_t tokens, const int64_t* slots, const void* k_out, const void* v_out,
                          char* why) {
   if (tokens < 0) return kv_refuse(why, AGEMM_EINVAL, "tokens must not be negative");

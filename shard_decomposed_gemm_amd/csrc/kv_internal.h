@@ -1,5 +1,5 @@
 // Internal interface between the key/value cache's C-ABI host code (kvc.cpp)
-// and its gfx950 kernels (kv_append.hip, kv_attend.hip).
+// and its gfx950 kernels (kv_append.hip, kv_attend.hip, kv_tree.hip, kv_verify.hip).
 #pragma once
 
 #include "agemm_internal.h"
@@ -52,11 +52,58 @@ struct KvAttendArgs {
   float scale;
   void* out;
   float* lse;
+  const uint64_t* tree;  // masks of a tree's nodes, tree_words a row of q, or NULL
+  int32_t tree_words;
   KvPlan plan;
   float* ws;  // plan.ws_bytes of partials
   uint64_t* err;  // kv_report.h
 };
 
+struct KvTreeArgs {
+  KvLayout L;
+  int32_t batch, max_q;
+  int64_t tokens;
+  const int32_t *q_start, *kv_len, *parent, *table;
+  int64_t table_stride;
+  int32_t table_width, words;
+  uint64_t* mask;
+  int64_t *positions, *slots;
+  int32_t* total_len;
+  uint64_t* err;  // kv_report.h
+};
+
+struct KvVerifyArgs {
+  int32_t batch, max_q;
+  int64_t tokens;
+  const int32_t *q_start, *parent;
+  const int64_t* token;
+  const float *p, *q;
+  int64_t p_stride, q_stride;
+  int32_t vocab;
+  const float* u;
+  int32_t *path, *count;
+  int64_t* next;
+  KvVerifyPlan plan;
+  double* ws;     // batch x rounds x parts sums
+  uint64_t* err;  // kv_report.h
+};
+
+struct KvCommitArgs {
+  KvLayout L;
+  char* pages[kKvLayers];
+  int32_t batch, layers;
+  int32_t max_q;
+  int64_t tokens;
+  const int32_t *q_start, *kv_len, *path, *count, *table;
+  int64_t table_stride;
+  int32_t table_width;
+  int32_t* new_len;
+  uint64_t* err;  // kv_report.h
+};
+
+hipError_t launch_kv_tree(const KvTreeArgs& a, hipStream_t s);
+hipError_t launch_kv_verify(const KvVerifyArgs& a, hipStream_t s);
+hipError_t launch_kv_commit(const KvCommitArgs& a, hipStream_t s);
 hipError_t launch_kv_append(const KvAppendArgs& a, int num_cus, hipStream_t s);
 hipError_t launch_kv_read(const KvReadArgs& a, hipStream_t s);
 hipError_t launch_kv_attend(const KvAttendArgs& a, bool out_f32, hipStream_t s);

@@ -210,4 +210,42 @@ inline void kv_many_wide(KvPlan& p, const KvLayout& L, int64_t batch, int64_t ma
   if (kv_many_items(w, L, batch, tokens) >= 4 * num_cus) p = w;
 }
 
+constexpr int kKvNodes = 1024;       // of one tree
+constexpr int kKvMaskWords = kKvNodes / 64;
+constexpr int kKvLayers = 64;        // of one launch of the commit
+
+// Layers of one launch of the commit, a wave for each (layer, sequence, kv head).
+inline int kv_commit_piece(const KvLayout& L, int64_t batch) {
+  const int64_t fits = (int64_t{1} << 25) / (batch * L.Hkv);
+  return (int)(fits < 1 ? 1 : fits < kKvLayers ? fits : kKvLayers);
+}
+
+// How a verification's rows of probabilities are summed: in `parts` parts of
+// `part` tokens each, one workgroup a part, in `rounds` launches. A round sums
+// what the walk asks for next; what is left after the last round, the last
+// kernel sums alone.
+struct KvVerifyPlan {
+  int32_t parts, part, rounds;
+};
+constexpr int kKvParts = 64;  // at most: a wave adds them up
+constexpr int kKvRounds = 3;
+inline KvVerifyPlan kv_verify_plan(int64_t batch, int64_t vocab, bool drawn, int64_t max_children, int num_cus) {
+  KvVerifyPlan p{};
+  // Four workgroups a CU, of 2048 tokens at the least (two loads a thread).
+  int64_t parts = (4 * num_cus + batch - 1) / (batch > 0 ? batch : 1), most = (vocab + 2047) / 2048;
+  parts = parts < most ? parts : most;
+  parts = parts < kKvParts ? parts : kKvParts;
+  const int64_t part = ((vocab + parts - 1) / parts + 1023) / 1024 * 1024;
+  p.part = (int32_t)part;
+  p.parts = (int32_t)((vocab + part - 1) / part);
+  p.rounds = drawn && max_children > 1 ? kKvRounds : 1;
+  return p;
+}
+// Bytes for every verification of up to `batch` sequences and `vocab` tokens: batch x parts < batch + 4 num_cus.
+inline int64_t kv_verify_bound(int64_t batch, int64_t vocab, int num_cus) {
+  const int64_t most = (vocab + 2047) / 2048 < kKvParts ? (vocab + 2047) / 2048 : kKvParts;
+  const int64_t some = batch + 4 * num_cus, all = batch * most;
+  return (some < all ? some : all) * kKvRounds * 8;
+}
+
 }  // namespace agemm

@@ -18,6 +18,10 @@ enum KvErr : uint32_t {  // 0: nothing; the value that a report holds
   kKvPage = 4,      // page id outside the cache
   kKvLength = 5,    // length negative or beyond the page table
   kKvRows = 6,      // query rows beyond max_q or T, or not ascending: their number
+  kKvParent = 7,    // parent that is no earlier node
+  kKvToken = 8,     // drafted token outside the vocabulary
+  kKvWeight = 9,    // no probability to draw from
+  kKvPath = 10,     // accepted nodes not ascending or outside their tree: their number
 };
 
 // Case in bits 60..63, index of the token or sequence (a call has up to 2^23)
@@ -40,6 +44,10 @@ inline void kv_report_text(char* buf, size_t size, uint64_t word, int64_t slots,
     case kKvPage: snprintf(buf, size, "sequence %u: page id %lld outside the cache (%lld pages)", at, v, (long long)pages); break;
     case kKvLength: snprintf(buf, size, "sequence %u: length %lld negative or beyond its page table", at, v); break;
     case kKvRows: snprintf(buf, size, "sequence %u: %lld query rows, more than max_q, less than 0 or outside q", at, v); break;
+    case kKvParent: snprintf(buf, size, "row %u: parent %s%lld is no earlier node of its tree", at, end, v); break;
+    case kKvToken: snprintf(buf, size, "row %u: drafted token %s%lld outside the vocabulary", at, end, v); break;
+    case kKvWeight: snprintf(buf, size, "sequence %u: no probability to draw from", at); break;
+    case kKvPath: snprintf(buf, size, "sequence %u: a path of %lld nodes that does not ascend within its tree", at, v); break;
     default: snprintf(buf, size, "unknown case %u", code);
   }
 }

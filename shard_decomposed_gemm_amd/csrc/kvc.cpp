@@ -1,7 +1,8 @@
 // C-ABI of the 4-bit paged key/value cache (declared in include/kvcache.h).
 //
 // Host side only: validation, the context (its shape and the error word), and
-// the launches. The arithmetic runs in kv_append.hip and kv_attend.hip.
+// the launches. The arithmetic runs in kv_append.hip, kv_attend.hip, kv_tree.hip
+// and kv_verify.hip.
 #include "kvcache.h"
 
 #include <hip/hip_runtime.h>
@@ -53,6 +54,47 @@ struct OnDevice {
     if (before >= 0) (void)hipSetDevice(before);
   }
 };
+
+int attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, const uint64_t* mask, int32_t mask_words,
+           void* workspace, int64_t workspace_bytes, void* stream) {
+  KvPlan plan{};
+  if (p && p->batch >= 0 && p->batch <= kKvMaxTokens && p->max_q >= 1 && p->max_q <= kKvMaxTokens &&
+      p->max_kv >= 1)  // refused below otherwise
+    plan = kv_attend_plan(ctx->L, p->batch, p->max_q, p->max_kv, ctx->num_cus);
+  char why[kKvWhy];
+  const int rc = kv_check_attend(ctx->L, pages, p, plan, workspace, workspace_bytes, why);
+  if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);
+
+  KvAttendArgs a{};
+  a.L = ctx->L;
+  a.pages = static_cast<const char*>(pages);
+  a.batch = p->batch;
+  a.max_q = p->max_q;
+  a.tokens = p->tokens;
+  a.q = static_cast<const _Float16*>(p->q);
+  a.q_ts = p->q_token_stride;
+  a.q_hs = p->q_head_stride;
+  a.q_start = p->q_start;
+  a.kv_len = p->kv_len;
+  a.q_off = p->q_off;
+  a.table = p->page_table;
+  a.table_stride = p->table_stride;
+  a.table_width = p->table_width;
+  a.causal = p->causal;
+  a.scale = p->scale;
+  a.out = p->out;
+  a.lse = p->lse;
+  a.tree = mask;
+  a.tree_words = mask_words;
+  kv_many_wide(plan, ctx->L, p->batch, p->max_q, p->max_kv, p->tokens, ctx->num_cus);
+  a.plan = plan;
+  a.ws = static_cast<float*>(workspace);
+  a.err = ctx->err_dev;
+  OnDevice on(ctx->device);
+  if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");
+  const hipError_t e = launch_kv_attend(a, p->out_f32 != 0, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? AGEMM_OK : hip_fail(ctx, e, "attention launch");
+}
 
 }  // namespace
 
@@ -161,41 +203,122 @@ int kvc_attend_workspace(const kvc_ctx* ctx, int32_t batch, int32_t max_q, int64
 int kvc_attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, void* workspace, int64_t workspace_bytes,
                void* stream) {
   if (!ctx) return AGEMM_EINVAL;
-  KvPlan plan{};
-  if (p && p->batch >= 0 && p->batch <= kKvMaxTokens && p->max_q >= 1 && p->max_q <= kKvMaxTokens &&
-      p->max_kv >= 1)  // refused below otherwise
-    plan = kv_attend_plan(ctx->L, p->batch, p->max_q, p->max_kv, ctx->num_cus);
+  return attend(ctx, pages, p, nullptr, 0, workspace, workspace_bytes, stream);
+}
+
+int kvc_attend_tree(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, const uint64_t* mask, int32_t mask_words,
+                    void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!ctx) return AGEMM_EINVAL;
   char why[kKvWhy];
-  const int rc = kv_check_attend(ctx->L, pages, p, plan, workspace, workspace_bytes, why);
+  const int rc = kv_check_mask(p, mask, mask_words, why);
+  if (rc) return fail(ctx, rc, "%s", why);
+  return attend(ctx, pages, p, mask, mask_words, workspace, workspace_bytes, stream);
+}
+
+int kvc_tree(kvc_ctx* ctx, const kvc_tree_args* p, void* stream) {
+  if (!ctx) return AGEMM_EINVAL;
+  char why[kKvWhy];
+  const int rc = kv_check_tree(p, why);
   if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);
 
-  KvAttendArgs a{};
+  KvTreeArgs a{};
   a.L = ctx->L;
-  a.pages = static_cast<const char*>(pages);
   a.batch = p->batch;
   a.max_q = p->max_q;
   a.tokens = p->tokens;
-  a.q = static_cast<const _Float16*>(p->q);
-  a.q_ts = p->q_token_stride;
-  a.q_hs = p->q_head_stride;
   a.q_start = p->q_start;
   a.kv_len = p->kv_len;
-  a.q_off = p->q_off;
+  a.parent = p->parent;
   a.table = p->page_table;
   a.table_stride = p->table_stride;
   a.table_width = p->table_width;
-  a.causal = p->causal;
-  a.scale = p->scale;
-  a.out = p->out;
-  a.lse = p->lse;
-  kv_many_wide(plan, ctx->L, p->batch, p->max_q, p->max_kv, p->tokens, ctx->num_cus);
-  a.plan = plan;
-  a.ws = static_cast<float*>(workspace);
+  a.words = p->mask_words;
+  a.mask = p->mask;
+  a.positions = p->positions;
+  a.slots = p->slots;
+  a.total_len = p->total_len;
   a.err = ctx->err_dev;
   OnDevice on(ctx->device);
   if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");
-  const hipError_t e = launch_kv_attend(a, p->out_f32 != 0, static_cast<hipStream_t>(stream));
-  return e == hipSuccess ? AGEMM_OK : hip_fail(ctx, e, "attention launch");
+  const hipError_t e = launch_kv_tree(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? AGEMM_OK : hip_fail(ctx, e, "tree launch");
+}
+
+int kvc_verify_workspace(const kvc_ctx* ctx, int32_t batch, int64_t vocab, int64_t* bytes) {
+  if (!ctx || !bytes || batch < 0 || vocab < 1) return AGEMM_EINVAL;
+  if (batch > kKvMaxSequences || vocab > (int64_t{1} << 28)) return AGEMM_ESHAPE;
+  *bytes = kv_verify_bound(batch, vocab, ctx->num_cus);
+  return AGEMM_OK;
+}
+
+int kvc_verify(kvc_ctx* ctx, const kvc_verify_args* p, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!ctx) return AGEMM_EINVAL;
+  KvVerifyPlan plan{};
+  if (p && p->batch > 0 && p->batch <= kKvMaxSequences && p->vocab >= 1 && p->vocab <= (int64_t{1} << 28))  // refused below otherwise
+    plan = kv_verify_plan(p->batch, p->vocab, p->q != nullptr, p->max_children, ctx->num_cus);
+  char why[kKvWhy];
+  const int64_t need = p ? (int64_t)p->batch * plan.parts * plan.rounds * 8 : 0;
+  const int rc = kv_check_verify(p, need, workspace, workspace_bytes, why);
+  if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);
+
+  KvVerifyArgs a{};
+  a.batch = p->batch;
+  a.max_q = p->max_q;
+  a.tokens = p->tokens;
+  a.q_start = p->q_start;
+  a.parent = p->parent;
+  a.token = p->token;
+  a.p = p->p;
+  a.q = p->q;
+  a.p_stride = p->p_stride;
+  a.q_stride = p->q_stride;
+  a.vocab = (int32_t)p->vocab;
+  a.u = p->u;
+  a.path = p->path;
+  a.count = p->count;
+  a.next = p->next;
+  a.plan = plan;
+  a.ws = static_cast<double*>(workspace);
+  a.err = ctx->err_dev;
+  OnDevice on(ctx->device);
+  if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");
+  const hipError_t e = launch_kv_verify(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? AGEMM_OK : hip_fail(ctx, e, "verification launch");
+}
+
+int kvc_commit(kvc_ctx* ctx, void* const* pages, int32_t layers, const kvc_commit_args* p, void* stream) {
+  if (!ctx) return AGEMM_EINVAL;
+  char why[kKvWhy];
+  const int rc = kv_check_commit(ctx->L, pages, layers, p, why);
+  if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);
+
+  KvCommitArgs a{};
+  a.L = ctx->L;
+  a.batch = p->batch;
+  a.max_q = p->max_q;
+  a.tokens = p->tokens;
+  a.q_start = p->q_start;
+  a.kv_len = p->kv_len;
+  a.path = p->path;
+  a.count = p->count;
+  a.table = p->page_table;
+  a.table_stride = p->table_stride;
+  a.table_width = p->table_width;
+  a.new_len = p->new_len;
+  a.err = ctx->err_dev;
+  OnDevice on(ctx->device);
+  if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");
+  const int piece = kv_commit_piece(ctx->L, p->batch);
+  int i = 0;
+  do {  // once without layers, for the lengths
+    a.layers = layers - i < piece ? layers - i : piece;
+    for (int j = 0; j < a.layers; ++j) a.pages[j] = static_cast<char*>(pages[i + j]);
+    const hipError_t e = launch_kv_commit(a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(ctx, e, "commit launch");
+    a.new_len = nullptr;  // written by the first launch
+    i += piece;
+  } while (i < layers);
+  return AGEMM_OK;
 }
 
 int kvc_read(kvc_ctx* ctx, const void* pages, int64_t tokens, const int64_t* slots, void* k_out, void* v_out,

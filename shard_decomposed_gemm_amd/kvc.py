@@ -13,7 +13,7 @@ from .agemm import OK, AgemmError, status_string
 
 EXPORTED = (
     "kvc_create", "kvc_destroy", "kvc_page_bytes", "kvc_append", "kvc_attend", "kvc_attend_workspace", "kvc_read",
-    "kvc_check", "kvc_last_error",
+    "kvc_check", "kvc_last_error", "kvc_tree", "kvc_attend_tree", "kvc_verify", "kvc_verify_workspace", "kvc_commit",
 )
 
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
@@ -36,11 +36,32 @@ class AttendArgs(ctypes.Structure):
                 ("out_f32", _i32), ("out", _vp), ("lse", _vp)]
 
 
+class TreeArgs(ctypes.Structure):
+    """kvc_tree_args."""
+    _fields_ = [("batch", _i32), ("max_q", _i32), ("tokens", _i64), ("q_start", _vp), ("kv_len", _vp), ("parent", _vp),
+                ("page_table", _vp), ("table_stride", _i64), ("table_width", _i32), ("mask_words", _i32), ("mask", _vp),
+                ("positions", _vp), ("slots", _vp), ("total_len", _vp)]
+
+
+class VerifyArgs(ctypes.Structure):
+    """kvc_verify_args."""
+    _fields_ = [("batch", _i32), ("max_q", _i32), ("tokens", _i64), ("q_start", _vp), ("parent", _vp), ("token", _vp),
+                ("p", _vp), ("q", _vp), ("p_stride", _i64), ("q_stride", _i64), ("vocab", _i64), ("u", _vp),
+                ("max_children", _i32), ("path", _vp), ("count", _vp), ("next", _vp)]
+
+
+class CommitArgs(ctypes.Structure):
+    """kvc_commit_args."""
+    _fields_ = [("batch", _i32), ("max_q", _i32), ("tokens", _i64), ("q_start", _vp), ("kv_len", _vp), ("path", _vp),
+                ("count", _vp), ("page_table", _vp), ("table_stride", _i64), ("table_width", _i32), ("new_len", _vp)]
+
+
 # The same structs as bytes: packing them costs a third of filling a ctypes.Structure, and these calls are made for
 # every layer of a decode step. Null pointers are 0.
 _CODE = {_vp: "P", _i32: "i", _i64: "q", _f32: "f"}
-_pack_append, _pack_attend = (struct.Struct("@" + "".join(_CODE[t] for _, t in st._fields_)).pack
-                              for st in (AppendArgs, AttendArgs))
+_pack_append, _pack_attend, _pack_tree, _pack_verify, _pack_commit = (
+    struct.Struct("@" + "".join(_CODE[t] for _, t in st._fields_)).pack
+    for st in (AppendArgs, AttendArgs, TreeArgs, VerifyArgs, CommitArgs))
 
 _ready = False
 
@@ -56,6 +77,11 @@ def load() -> ctypes.CDLL:
         lib.kvc_append.argtypes = [_vp, _vp, _vp, _vp]  # a packed AppendArgs
         lib.kvc_attend.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp]  # a packed AttendArgs
         lib.kvc_attend_workspace.argtypes = [_vp, _i32, _i32, _i64, ctypes.POINTER(_i64)]
+        lib.kvc_attend_tree.argtypes = [_vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp]  # a packed AttendArgs
+        lib.kvc_tree.argtypes = [_vp, _vp, _vp]  # a packed TreeArgs
+        lib.kvc_verify.argtypes = [_vp, _vp, _vp, _i64, _vp]  # a packed VerifyArgs
+        lib.kvc_verify_workspace.argtypes = [_vp, _i32, _i64, ctypes.POINTER(_i64)]
+        lib.kvc_commit.argtypes = [_vp, _vp, _i32, _vp, _vp]  # page pointers, a packed CommitArgs
         lib.kvc_read.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp]
         lib.kvc_check.argtypes = [_vp]
         lib.kvc_last_error.argtypes = [_vp]
@@ -125,6 +151,35 @@ class KvCache:
             raise ValueError(f"{what} must have contiguous channels")
         return t.data_ptr(), st if T > 1 else H * self.D, sh if H > 1 else self.D
 
+    def _table(self, page_table, B):
+        """Pointer, row stride and width of a (B, width) int32 page table."""
+        if page_table.dtype is not self._i32 or page_table.get_device() != self._index or page_table.dim() != 2:
+            raise TypeError(f"page_table must be a two-dimensional int32 tensor on {self.device}")
+        rows, W = page_table.shape
+        if rows != B:
+            raise ValueError(f"page_table must have {B} rows, got {rows}")
+        ts, ws = page_table.stride()
+        if W > 1 and ws != 1:
+            raise ValueError("page_table must have contiguous rows")
+        return page_table.data_ptr(), ts if B > 1 else W, W
+
+    def _probabilities(self, t, what, T):
+        """Pointer, row stride and vocabulary of a (T, V) float32 tensor with contiguous rows."""
+        if t.dtype is not self._f32 or t.get_device() != self._index or t.dim() != 2:
+            raise TypeError(f"{what} must be a two-dimensional float32 tensor on {self.device}")
+        rows, V = t.shape
+        if rows != T:
+            raise ValueError(f"{what} must have {T} rows, got {rows}")
+        st, sv = t.stride()
+        if V > 1 and sv != 1:
+            raise ValueError(f"{what} must have contiguous rows")
+        return t.data_ptr(), st if T > 1 else V, V
+
+    def _bytes(self, workspace):
+        if workspace.dtype is not self._u8 or workspace.get_device() != self._index or not workspace.is_contiguous():
+            raise TypeError(f"workspace must be a contiguous uint8 tensor on {self.device}")
+        return workspace
+
     def _pages(self, pages):
         return self._plain(pages, "pages", self._u8, self._pages_shape)
 
@@ -183,9 +238,11 @@ class KvCache:
             self._raise(rc, "kvc_append")
 
     def attend(self, pages, q, kv_len, page_table, out, lse=None, q_start=None, max_q: int = 1, q_off=None,
-               causal: bool = True, scale: float | None = None, max_kv: int | None = None, workspace=None, stream=None):
+               causal: bool = True, scale: float | None = None, max_kv: int | None = None, workspace=None, stream=None,
+               tree=None):
         """kvc_attend: attention of q (T, Hq, D) over the cached tokens of each sequence into out (T, Hq, D)
-        float16 or float32 and lse (T, Hq) float32.
+        float16 or float32 and lse (T, Hq) float32. With tree (T, words) int64, the masks that ``tree`` makes,
+        kvc_attend_tree: each query sees the first q_off tokens and the tree's nodes that its mask names.
 
         kv_len (batch,), q_start (batch + 1,), q_off (batch,) and page_table (batch, width) int32. scale: 1 / sqrt(D)
         unless given. max_kv: the longest length to expect (the table's width unless given). Without a workspace one
@@ -197,14 +254,7 @@ class KvCache:
         f32 = out.dtype is self._f32
         outp = plain(out, "out", self._f32 if f32 else self._f16, (T, self.Hq, self.D))
         lsep = 0 if lse is None else plain(lse, "lse", self._f32, (T, self.Hq))
-        if page_table.dtype is not self._i32 or page_table.get_device() != self._index or page_table.dim() != 2:
-            raise TypeError(f"page_table must be a two-dimensional int32 tensor on {self.device}")
-        rows, W = page_table.shape
-        if rows != B:
-            raise ValueError(f"page_table must have {B} rows, got {rows}")
-        ts, ws = page_table.stride()
-        if W > 1 and ws != 1:
-            raise ValueError("page_table must have contiguous rows")
+        tp, ts, W = self._table(page_table, B)
         if max_kv is None:
             max_kv = max(1, W * self.page_tokens)
         handle = self._stream(stream)
@@ -212,17 +262,94 @@ class KvCache:
             import torch
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
                 workspace = self.workspace(B, max_q, max_kv)
-        elif workspace.dtype is not self._u8 or workspace.get_device() != self._index or not workspace.is_contiguous():
-            raise TypeError(f"workspace must be a contiguous uint8 tensor on {self.device}")
+        else:
+            self._bytes(workspace)
         args = _pack_attend(B, max_q, T, qp, qt, qh,
                             0 if q_start is None else plain(q_start, "q_start", self._i32, (B + 1,)),
                             plain(kv_len, "kv_len", self._i32, (B,)),
                             0 if q_off is None else plain(q_off, "q_off", self._i32, (B,)),
-                            page_table.data_ptr(), ts if B > 1 else W, W, bool(causal), max_kv,
-                            self.D ** -0.5 if scale is None else scale, f32, outp, lsep)
-        rc = self._lib.kvc_attend(self._h, self._pages(pages), args, workspace.data_ptr(), workspace.numel(), handle)
+                            tp, ts, W, bool(causal), max_kv, self.D ** -0.5 if scale is None else scale, f32, outp, lsep)
+        if tree is None:
+            rc = self._lib.kvc_attend(self._h, self._pages(pages), args, workspace.data_ptr(), workspace.numel(), handle)
+        else:
+            words = tree.shape[-1]
+            rc = self._lib.kvc_attend_tree(self._h, self._pages(pages), args, plain(tree, "tree", self._i64, (T, words)),
+                                           words, workspace.data_ptr(), workspace.numel(), handle)
         if rc != OK:
-            self._raise(rc, "kvc_attend")
+            self._raise(rc, "kvc_attend" if tree is None else "kvc_attend_tree")
+
+    def tree(self, parent, q_start, kv_len, page_table, max_q: int, mask, positions=None, slots=None, total_len=None,
+             stream=None):
+        """kvc_tree: lays out a step's drafted tokens. parent (T,) int32, q_start (batch + 1,), kv_len (batch,) and
+        page_table (batch, width) int32 give mask (T, words) int64, positions and slots (T,) int64 and total_len
+        (batch,) int32. page_table may be None without slots."""
+        T, B = parent.shape[0], kv_len.shape[0]
+        plain, i32, i64 = self._plain, self._i32, self._i64
+        words = mask.shape[-1]
+        tp, ts, W = (0, 0, 0) if page_table is None else self._table(page_table, B)
+        args = _pack_tree(B, max_q, T, plain(q_start, "q_start", i32, (B + 1,)), plain(kv_len, "kv_len", i32, (B,)),
+                          plain(parent, "parent", i32, (T,)), tp, ts, W, words, plain(mask, "mask", i64, (T, words)),
+                          0 if positions is None else plain(positions, "positions", i64, (T,)),
+                          0 if slots is None else plain(slots, "slots", i64, (T,)),
+                          0 if total_len is None else plain(total_len, "total_len", i32, (B,)))
+        rc = self._lib.kvc_tree(self._h, args, self._stream(stream))
+        if rc != OK:
+            self._raise(rc, "kvc_tree")
+
+    def verify_workspace(self, batch: int, vocab: int):
+        """Workspace for every ``verify`` call within these bounds: one for each call that may run at the same time."""
+        import torch
+        n = _i64()
+        rc = self._lib.kvc_verify_workspace(self._h, int(batch), int(vocab), ctypes.byref(n))
+        if rc != OK:
+            raise AgemmError(rc, f"kvc_verify_workspace: {status_string(rc)}")
+        return torch.empty(max(16, n.value), dtype=torch.uint8, device=self.device)
+
+    def verify(self, tokens, parent, q_start, p, u, path, count, next_token, max_q: int, q=None, max_children: int = 1,
+               workspace=None, stream=None):
+        """kvc_verify: the accepted path of each sequence's tree and the token that follows it.
+
+        tokens (T,) int64, parent (T,) int32 and u (T,) float32, q_start (batch + 1,) int32; p and q (T, V) float32, the
+        target's and the draft's probabilities after each node (q None: drafts are certain). path (T,) and count
+        (batch,) int32 and next_token (batch,) int64 are written. max_children: the most children of a node to
+        expect. Without a workspace one is allocated on the stream for this call."""
+        T, B = parent.shape[0], count.shape[0]
+        plain, i32, i64 = self._plain, self._i32, self._i64
+        pp, ps, V = self._probabilities(p, "p", T)
+        qp = qs = 0
+        if q is not None:
+            qp, qs, VQ = self._probabilities(q, "q", T)
+            if VQ != V:
+                raise ValueError(f"p and q must have the same vocabulary, got {V} and {VQ}")
+        handle = self._stream(stream)
+        if workspace is None:
+            import torch
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
+                workspace = self.verify_workspace(B, V)
+        else:
+            self._bytes(workspace)
+        args = _pack_verify(B, max_q, T, plain(q_start, "q_start", i32, (B + 1,)), plain(parent, "parent", i32, (T,)),
+                            plain(tokens, "tokens", i64, (T,)), pp, qp, ps, qs, V, plain(u, "u", self._f32, (T,)),
+                            max_children, plain(path, "path", i32, (T,)), plain(count, "count", i32, (B,)),
+                            plain(next_token, "next_token", i64, (B,)))
+        rc = self._lib.kvc_verify(self._h, args, workspace.data_ptr(), workspace.numel(), handle)
+        if rc != OK:
+            self._raise(rc, "kvc_verify")
+
+    def commit(self, pages, q_start, kv_len, path, count, page_table, max_q: int, new_len=None, stream=None):
+        """kvc_commit: moves the accepted nodes of ``verify`` to their places, in the pages of one layer or a list of
+        several with the same page table. new_len (batch,) int32: kv_len + count."""
+        layers = pages if isinstance(pages, (list, tuple)) else (pages,)
+        T, B = path.shape[0], kv_len.shape[0]
+        plain, i32 = self._plain, self._i32
+        tp, ts, W = self._table(page_table, B)
+        args = _pack_commit(B, max_q, T, plain(q_start, "q_start", i32, (B + 1,)), plain(kv_len, "kv_len", i32, (B,)),
+                            plain(path, "path", i32, (T,)), plain(count, "count", i32, (B,)), tp, ts, W,
+                            0 if new_len is None else plain(new_len, "new_len", i32, (B,)))
+        at = struct.pack(f"@{len(layers)}P", *[self._pages(p) for p in layers])
+        rc = self._lib.kvc_commit(self._h, at, len(layers), args, self._stream(stream))
+        if rc != OK:
+            self._raise(rc, "kvc_commit")
 
     def read(self, pages, slots, k_out, v_out, stream=None):
         """kvc_read: the binary16 keys and values of the tokens in slots (T,) int64 into k_out and v_out (T, Hkv, D)."""
