@@ -319,6 +319,112 @@ __device__ inline Runs find_runs(const KvAttendArgs& a, int64_t run, int b, int 
   return {chunk, -1, 0, Sequence{}};
 }
 
+// With a tree: the work of a call, (sequence, tile of its rows, kv head, run of
+// its blocks), kv heads innermost, so that the tiles of a head go to one XCD and
+// share its cache, then tiles, then runs. Runs are of the whole batch's lengths as
+// for few rows; only items of several runs leave partials. b < 0: none.
+struct Work {
+  int b, tile, h, run;
+  int chunk, runs;  // blocks of a run, runs of the item
+  int per;          // items of the sequence
+  int slot, join;   // the sequence's first partial and first item of several runs
+  Sequence seq;
+};
+__device__ inline int tiles_of(const KvAttendArgs& a, const Sequence& s) {
+  return (int)(((int64_t)s.n * a.plan.group + a.plan.rows - 1) >> a.plan.row_shift);
+}
+// Work `at` of the call, for a wave. Where runs are joined, the wave with work 0 of
+// several sequences leaves the number of items to join.
+__device__ inline Work find_work(const KvAttendArgs& a, int at, int lane, bool tell) {
+  Work w;
+  w.slot = w.join = 0;
+  auto split = [&](int rest) {  // `rest`: work of the sequence
+    w.run = (int)((uint32_t)rest / (uint32_t)w.per);
+    const int r = rest - w.run * w.per;
+    w.tile = (int)((uint32_t)r / (uint32_t)a.L.Hkv);
+    w.h = r - w.tile * a.L.Hkv;
+  };
+  if (a.plan.slots <= a.plan.items) {  // one run an item
+    w.per = a.plan.tiles * a.L.Hkv;
+    w.b = (int)((uint32_t)at / (uint32_t)w.per);
+    split(at - w.b * w.per);
+    w.chunk = kKvWhole;
+    w.runs = 1;
+    w.seq = sequence(a, w.b, tell && w.tile == 0 && w.h == 0);
+    return w;
+  }
+  if (a.batch == 1) {
+    w.seq = sequence(a, 0, tell && at == 0);
+    const int nblk = w.seq.blocks();
+    w.per = tiles_of(a, w.seq) * a.L.Hkv;
+    w.chunk = kv_tree_chunk_of_one(a.plan, w.per, nblk);
+    w.runs = kv_tree_runs(w.chunk, nblk);
+    w.b = at < w.per * w.runs ? 0 : -1;
+    if (w.b == 0) split(at);
+    return w;
+  }
+  auto load = [&](int b0, bool report) {
+    Sequence s{};
+    if (b0 + lane < a.batch) s = sequence<true>(a, b0 + lane, report);
+    return s;
+  };
+  auto sum = [](int x) { return __builtin_amdgcn_readlane(sum_up_to(x), 63); };
+  auto wide_sum = [&](int64_t x) { return ((int64_t)sum((int)(x >> 20)) << 20) + sum((int)(x & 0xfffff)); };
+  const Sequence group0 = load(0, tell && at == 0);
+  int64_t all = 0;
+  int items = 0, longest = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    const Sequence s = b0 == 0 ? group0 : load(b0, tell && at == 0);
+    const int x = s.blocks(), n = tiles_of(a, s), top = __builtin_amdgcn_readlane(largest_up_to(x), 63);
+    all += wide_sum((int64_t)x * n);
+    items += sum(n);
+    longest = longest > top ? longest : top;
+  }
+  w.chunk = kv_tree_chunk(a.plan, all * a.L.Hkv, longest);
+  if (a.batch <= 64 && items * a.L.Hkv <= a.plan.places) {
+    // Remainders make more runs than run at once: longer ones, until they fit or nearly so.
+    const int x = group0.blocks(), n = tiles_of(a, group0);
+    for (int turn = 0; turn < 4 && w.chunk < longest; ++turn) {
+      const int runs = sum(kv_tree_runs(w.chunk, x) * n) * a.L.Hkv;
+      if (runs <= a.plan.places) break;
+      w.chunk = kv_tree_longer(a.plan, w.chunk, runs);
+    }
+  }
+  int before = 0, slots = 0, joins = 0;  // of a head, of the groups of sequences before
+  w.b = -1;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    const Sequence s = b0 == 0 ? group0 : load(b0, false);
+    const int runs = kv_tree_runs(w.chunk, s.blocks()), tiles = tiles_of(a, s), mine = runs * tiles;
+    const int left = runs > 1 ? mine : 0, join = runs > 1 ? tiles : 0;
+    const int to_mine = sum_up_to(mine), to_left = sum_up_to(left), to_join = sum_up_to(join);
+    const uint64_t has = __ballot((before + to_mine) * a.L.Hkv > at);
+    if (has && w.b < 0) {
+      const int l = __builtin_ctzll(has);
+      w.b = b0 + l;
+      w.seq = of_lane(s, l);
+      w.runs = __builtin_amdgcn_readlane(runs, l);
+      w.per = __builtin_amdgcn_readlane(tiles, l) * a.L.Hkv;
+      w.slot = (slots + __builtin_amdgcn_readlane(to_left - left, l)) * a.L.Hkv;
+      w.join = (joins + __builtin_amdgcn_readlane(to_join - join, l)) * a.L.Hkv;
+      split(at - (before + __builtin_amdgcn_readlane(to_mine - mine, l)) * a.L.Hkv);
+      if (at > 0) return w;
+    }
+    before += __builtin_amdgcn_readlane(to_mine, 63);
+    slots += __builtin_amdgcn_readlane(to_left, 63);
+    joins += __builtin_amdgcn_readlane(to_join, 63);
+  }
+  if (at == 0 && tell && lane == 0) *a.joins = joins * a.L.Hkv;
+  return w;
+}
+// The partial of a run, and (its first run's first wave) what there is to join.
+__device__ inline int64_t partial_of(const KvAttendArgs& a, const Work& w, bool tell) {
+  const int i = w.tile * a.L.Hkv + w.h;
+  if (w.runs > 1 && w.run == 0 && tell && a.batch > 1)
+    reinterpret_cast<KvJoin*>(a.joins + 4)[w.join + i] =
+        KvJoin{w.seq.row0, w.h, w.tile << a.plan.row_shift, w.seq.n * a.plan.group, w.runs, w.slot + i, w.per};
+  return w.slot + (int64_t)w.run * w.per + i;
+}
+
 // Many rows: the tile (sequence, tile of its rows) that is k-th of the call's,
 // the last ones of all sequences first: those see the most keys. Every wave
 // works it out for itself, from tiles that each lane holds of up to eight
@@ -490,10 +596,21 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t col = lane & 15, quarter = lane >> 4;
   const int G = a.L.Hq / a.L.Hkv;
-  const int64_t slot_id = blockIdx.x;
-  int b, h, run = 0, chunk = kKvWhole;
+  int64_t slot_id = blockIdx.x;
+  int b, h, run = 0, runs = 1, chunk = kKvWhole, r0 = 0;  // r0: the item's first row
   Sequence seq;
-  if (a.plan.slots <= a.plan.items) {  // one run an item
+  if constexpr (TREE) {
+    const Work w = find_work(a, blockIdx.x, lane, wave == 0);
+    if (w.b < 0) return;
+    b = w.b;
+    h = w.h;
+    run = w.run;
+    runs = w.runs;
+    chunk = w.chunk;
+    seq = w.seq;
+    r0 = w.tile * R;
+    slot_id = partial_of(a, w, threadIdx.x == 0);
+  } else if (a.plan.slots <= a.plan.items) {  // one run an item
     b = (int)blockIdx.x / a.L.Hkv;
     h = (int)blockIdx.x - b * a.L.Hkv;
     seq = sequence(a, b, h == 0 && threadIdx.x == 0);
@@ -514,9 +631,10 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
     run = h / a.L.Hkv;
     h -= run * a.L.Hkv;
   }
-  const int rows = seq.n * G;
-  const int nblk = seq.blocks(), runs = kv_item_runs(chunk, nblk);
-  if (rows == 0 || run >= runs) return;
+  const int rows = TREE && seq.n * G - r0 > R ? R : seq.n * G - r0;
+  const int nblk = seq.blocks();
+  if constexpr (!TREE) runs = kv_item_runs(chunk, nblk);
+  if (rows <= 0 || run >= runs) return;
   const int j1 = nblk - run * chunk < chunk ? nblk : (run + 1) * chunk;
   int j = run * chunk + wave;
 
@@ -549,7 +667,7 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
   for (int n = 0; n < NT; ++n) {
     // Columns past the last row repeat row 0: loads that some lanes leave out
     // would make the loop's first waits those for everything.
-    const int r = n * 16 + (int)col < rows ? n * 16 + col : 0;
+    const int r = r0 + (n * 16 + (int)col < rows ? n * 16 + col : 0);
     const int i = r / G;
     const _Float16* src = a.q + (seq.row0 + i) * a.q_ts + (int64_t)(h * G + r - i * G) * a.q_hs + quarter * (D / 4);
 #pragma unroll
@@ -706,8 +824,8 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
       v4 += *reinterpret_cast<const float4v*>(&part[w][r][d]) * f;
     }
     if (runs == 1) {
-      const int i = r / G;
-      const int64_t row = (seq.row0 + i) * a.L.Hq + h * G + r - i * G;
+      const int i = (r0 + r) / G;
+      const int64_t row = (seq.row0 + i) * a.L.Hq + h * G + r0 + r - i * G;
       const float inv = all != 0.f ? 1.f / all : 0.f;
       store_out<F32, 4>(a.out, row * D + d, {v4.x * inv, v4.y * inv, v4.z * inv, v4.w * inv});
       if (a.lse && d == 0) a.lse[row] = all != 0.f ? (top + log2f(all)) * kLn2 : kLowest;
@@ -758,23 +876,39 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
   const int G = a.L.Hq / a.L.Hkv;
   // Heads innermost: workgroups of one head go to one XCD and share its cache;
   // later tiles, which see more keys, first.
-  const int item = blockIdx.x, run = a.plan.splits - 1 - blockIdx.y;
-  const int h = item % a.L.Hkv;
-  const bool tells = run == 0 && h == 0 && wave == 0;
-  const Tile at = find_tile(a, item / a.L.Hkv, lane, tells && item == 0);
-  const int b = at.b, tile = at.tile;
-  if (b < 0) return;
-  const Sequence seq = sequence(a, b, (a.batch == 1 || a.batch > kKvMaxBatch) && tells && tile == 0 && lane == 0);
+  const int item = blockIdx.x;
+  int run = a.plan.splits - 1 - blockIdx.y, h = item % a.L.Hkv, b, tile, chunk = 0, runs = 1;
+  int64_t slot_id = (int64_t)item * a.plan.splits + run;
+  Sequence seq;
+  if constexpr (TREE) {
+    const Work w = find_work(a, item, lane, wave == 0);
+    if (w.b < 0) return;
+    b = w.b;
+    tile = w.tile;
+    h = w.h;
+    run = w.run;
+    runs = w.runs;
+    chunk = w.chunk;
+    seq = w.seq;
+    slot_id = partial_of(a, w, tid == 0);
+  } else {
+    const bool tells = run == 0 && h == 0 && wave == 0;
+    const Tile at = find_tile(a, item / a.L.Hkv, lane, tells && item == 0);
+    b = at.b;
+    tile = at.tile;
+    if (b < 0) return;
+    seq = sequence(a, b, (a.batch == 1 || a.batch > kKvMaxBatch) && tells && tile == 0 && lane == 0);
+  }
   const int rows = seq.n * G;
   const int r0 = tile * (32 * W);
   if (r0 >= rows) return;
   const int r_last = (r0 + 32 * W - 1 < rows ? r0 + 32 * W - 1 : rows - 1);
   const int nblk = kv_blocks(seq.seen(r_last / G));
-  const int runs = kv_runs(a.plan.chunk, a.plan.splits, nblk);
+  if constexpr (!TREE) runs = kv_runs(a.plan.chunk, a.plan.splits, nblk);
   if (run >= runs) return;
-  const int chunk = kv_run_blocks(a.plan.chunk, a.plan.splits, nblk);
-  const int j0 = run * chunk;
-  const int j1 = nblk < j0 + chunk ? nblk : j0 + chunk;
+  if constexpr (!TREE) chunk = kv_run_blocks(a.plan.chunk, a.plan.splits, nblk);
+  const int j0 = TREE && runs == 1 ? 0 : run * chunk;
+  const int j1 = nblk - j0 < chunk ? nblk : j0 + chunk;
 
   const int r = r0 + wave * 32 + col;
   const bool live = r < rows;
@@ -984,7 +1118,7 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
   if (!live) return;
   // O^T: register i of tile m is row R = 8 (i / 4) + 4 hh + i % 4, channel (R % 16) D / 16 + 2 m + R / 16.
   const bool last = runs == 1;
-  float* slot = last ? nullptr : a.ws + ((int64_t)item * a.plan.splits + run) * a.plan.slot_floats;
+  float* slot = last ? nullptr : a.ws + slot_id * a.plan.slot_floats;
   const int lr = r - r0;
   const float inv = !last ? 1.f : sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
@@ -1020,57 +1154,18 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
 // workgroup of an item instead would need fences and counters to be cleared.
 constexpr int kJoinThreads = 512;
 
+// Joins R rows of an item, from row r0 + l0 of its kv head h on. RW: a power of two, R at the least.
 template <int D, bool F32>
-__global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendArgs a) {
+__device__ inline void join_rows(const KvAttendArgs& a, const float* part, int64_t step, int runs, int64_t row0, int h, int r0,
+                                 int l0, int R, int RW) {
   constexpr int C = D / 4;  // threads of a row
   __shared__ float weight[kJoinThreads / C][kKvMaxSplits];
   __shared__ float4v meet[kJoinThreads];
   __shared__ float sums[kJoinThreads / C], tops[kJoinThreads / C];
-  const int rpi = a.plan.rows, RW = a.plan.join_rows;
-  const int item = blockIdx.x, l0 = blockIdx.y * RW;
   const int G = a.L.Hq / a.L.Hkv;
   const int lane = threadIdx.x & 63;
-  int b = 0, h, r0 = 0, runs;
-  int64_t slot, step = 1;  // of the first partial, and to the next
-  Sequence seq;
-  if (a.plan.many) {
-    h = item % a.L.Hkv;
-    const Tile at = find_tile(a, item / a.L.Hkv, lane, false);
-    if (at.b < 0) return;
-    b = at.b;
-    seq = sequence(a, b, false);
-    r0 = at.tile * rpi;
-    const int rows = seq.n * G;
-    if (r0 >= rows) return;
-    const int r_last = r0 + rpi - 1 < rows ? r0 + rpi - 1 : rows - 1;
-    runs = kv_runs(a.plan.chunk, a.plan.splits, kv_blocks(seq.seen(r_last / G)));
-    slot = (int64_t)item * a.plan.splits;
-  } else {
-    b = item / a.L.Hkv;
-    h = item - b * a.L.Hkv;
-    slot = h;
-    int chunk;
-    if (a.batch == 1) {
-      seq = sequence(a, 0, false);
-      chunk = kv_chunk(a.plan, (int64_t)seq.blocks() * a.L.Hkv, seq.blocks());
-    } else {
-      const Runs r = find_runs(a, -1, b, lane, false);
-      seq = r.seq;
-      chunk = r.chunk;
-      slot += r.slot;
-    }
-    runs = kv_item_runs(chunk, seq.blocks());
-    step = a.L.Hkv;
-  }
-  const int rows = seq.n * G;
-  if (r0 + l0 >= rows) return;
-  if (runs == 1) return;  // written by its only run
-  const int R = rows - r0 - l0 < RW ? rows - r0 - l0 : RW;
-
-  const float* part = a.ws + slot * a.plan.slot_floats;
-  step *= a.plan.slot_floats;
   for (int r = uniform((int)threadIdx.x >> 6); r < R; r += kJoinThreads / 64) {
-    const float* head = part + rpi * D + 2 * (l0 + r);
+    const float* head = part + a.plan.rows * D + 2 * (l0 + r);
     float e[kKvMaxSplits / 64], n[kKvMaxSplits / 64], top = kNoMax, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kKvMaxSplits / 64; ++i) {
@@ -1113,16 +1208,151 @@ __global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendAr
   }
   if (r >= R) return;
   const int rr = r0 + l0 + r, i = rr / G;
-  const int64_t row = (seq.row0 + i) * a.L.Hq + h * G + rr - i * G;
+  const int64_t row = (row0 + i) * a.L.Hq + h * G + rr - i * G;
   const float inv = sums[r] != 0.f ? 1.f / sums[r] : 0.f;
   store_out<F32, 4>(a.out, row * D + d, {v.x * inv, v.y * inv, v.z * inv, v.w * inv});
   if (a.lse && d == 0) a.lse[row] = sums[r] != 0.f ? (tops[r] + log2f(sums[r])) * kLn2 : kLowest;
 }
 
+template <int D, bool F32>
+__global__ __launch_bounds__(kJoinThreads) void kv_attend_join_kernel(KvAttendArgs a) {
+  const int rpi = a.plan.rows, RW = a.plan.join_rows;
+  const int item = blockIdx.x, l0 = blockIdx.y * RW;
+  const int G = a.L.Hq / a.L.Hkv;
+  const int lane = threadIdx.x & 63;
+  int b = 0, h, r0 = 0, runs;
+  int64_t slot, step = 1;  // of the first partial, and to the next
+  Sequence seq;
+  if (a.plan.many) {
+    h = item % a.L.Hkv;
+    const Tile at = find_tile(a, item / a.L.Hkv, lane, false);
+    if (at.b < 0) return;
+    b = at.b;
+    seq = sequence(a, b, false);
+    r0 = at.tile * rpi;
+    const int rows = seq.n * G;
+    if (r0 >= rows) return;
+    const int r_last = r0 + rpi - 1 < rows ? r0 + rpi - 1 : rows - 1;
+    runs = kv_runs(a.plan.chunk, a.plan.splits, kv_blocks(seq.seen(r_last / G)));
+    slot = (int64_t)item * a.plan.splits;
+  } else {
+    b = item / a.L.Hkv;
+    h = item - b * a.L.Hkv;
+    slot = h;
+    int chunk;
+    if (a.batch == 1) {
+      seq = sequence(a, 0, false);
+      chunk = kv_chunk(a.plan, (int64_t)seq.blocks() * a.L.Hkv, seq.blocks());
+    } else {
+      const Runs r = find_runs(a, -1, b, lane, false);
+      seq = r.seq;
+      chunk = r.chunk;
+      slot += r.slot;
+    }
+    runs = kv_item_runs(chunk, seq.blocks());
+    step = a.L.Hkv;
+  }
+  const int rows = seq.n * G;
+  if (r0 + l0 >= rows) return;
+  if (runs == 1) return;  // written by its only run
+  const int R = rows - r0 - l0 < RW ? rows - r0 - l0 : RW;
+  join_rows<D, F32>(a, a.ws + slot * a.plan.slot_floats, step * a.plan.slot_floats, runs, seq.row0, h, r0, l0, R, RW);
+}
+
+// With a tree: the items that the attention left in a list (a single sequence's
+// follow from its lengths).
+struct Joins {
+  int count;
+  KvJoin one;
+  const KvJoin* list;
+
+  __device__ explicit Joins(const KvAttendArgs& a) : one{}, list(reinterpret_cast<const KvJoin*>(a.joins + 4)) {
+    if (a.batch > 1) {
+      count = *a.joins;
+      return;
+    }
+    const Sequence s = sequence(a, 0, false);
+    const int per = tiles_of(a, s) * a.L.Hkv;
+    one = KvJoin{s.row0, 0, 0, s.n * a.plan.group, kv_tree_runs(kv_tree_chunk_of_one(a.plan, per, s.blocks()), s.blocks()), 0, per};
+    count = one.runs > 1 ? per : 0;
+  }
+  __device__ KvJoin at(const KvAttendArgs& a, int i) const {
+    if (a.batch > 1) return list[i];
+    KvJoin j = one;
+    const int tile = (int)((uint32_t)i / (uint32_t)a.L.Hkv);
+    j.h = i - tile * a.L.Hkv;
+    j.r0 = tile << a.plan.row_shift;
+    j.slot = i;
+    return j;
+  }
+};
+
+// Few rows in all: a workgroup each, whose slices take every S-th run.
+template <int D, bool F32>
+__global__ __launch_bounds__(kJoinThreads) void kv_tree_join_few_kernel(KvAttendArgs a) {
+  const int groups = a.plan.join_groups;
+  const Joins joins(a);
+  for (int k = blockIdx.x, i; (i = (int)((uint32_t)k / (uint32_t)groups)) < joins.count; k += gridDim.x) {
+    const KvJoin j = joins.at(a, i);
+    const int l = k - i * groups;
+    if (l >= j.rows - j.r0) continue;
+    join_rows<D, F32>(a, a.ws + (int64_t)j.slot * a.plan.slot_floats, (int64_t)j.step * a.plan.slot_floats, j.runs, j.row0, j.h,
+                      j.r0, l, 1, 1);
+    __syncthreads();
+  }
+}
+
+// Many rows: D / 4 lanes a row, four runs' numbers on their way at a time, nothing
+// between the waves.
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void kv_tree_join_many_kernel(KvAttendArgs a) {
+  constexpr int C = D / 4, N = 64 / C;  // rows of a wave
+  const int lane = threadIdx.x & 63, d = 4 * (lane % C);
+  const int groups = a.plan.join_groups;
+  const Joins joins(a);
+  for (int k = uniform((int)(blockIdx.x * 4 + (threadIdx.x >> 6))), i; (i = (int)((uint32_t)k / (uint32_t)groups)) < joins.count;
+       k += gridDim.x * 4) {
+    const KvJoin j = joins.at(a, i);
+    const int l = (k - i * groups) * N + lane / C;
+    if (l >= j.rows - j.r0) continue;
+    const float* part = a.ws + (int64_t)j.slot * a.plan.slot_floats;
+    const int64_t step = (int64_t)j.step * a.plan.slot_floats;
+    float top = kNoMax, sum = 0.f;
+    float4v v = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < j.runs; s += 4) {
+      float e[4], n[4];
+      float4v p[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float* at = part + (s + x < j.runs ? s + x : s) * step;
+        e[x] = at[a.plan.rows * D + 2 * l];
+        n[x] = at[a.plan.rows * D + 2 * l + 1];
+        p[x] = *reinterpret_cast<const float4v*>(at + l * D + d);
+      }
+      const float m = fmaxf(max3(e[0], e[1], e[2]), fmaxf(e[3], top));
+      const float f = exp2_hw(top - m);
+      sum *= f;
+      v *= f;
+      top = m;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float w = s + x < j.runs ? exp2_hw(e[x] - m) : 0.f;
+        sum += w * n[x];
+        v += w * p[x];
+      }
+    }
+    const int r = j.r0 + l, q = (int)((uint32_t)r / (uint32_t)a.plan.group);
+    const int64_t row = (j.row0 + q) * a.L.Hq + j.h * a.plan.group + r - q * a.plan.group;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    store_out<F32, 4>(a.out, row * D + d, {v.x * inv, v.y * inv, v.z * inv, v.w * inv});
+    if (a.lse && d == 0) a.lse[row] = sum != 0.f ? (top + log2f(sum)) * kLn2 : kLowest;
+  }
+}
+
 template <int D, bool F32, bool TREE>
 hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
-  const int64_t items = a.plan.many ? kv_many_items(a.plan, a.L, a.batch, a.tokens) : a.plan.items;
-  const dim3 grid((unsigned)(a.plan.many ? items : a.plan.slots), (unsigned)a.plan.splits);
+  const int64_t items = a.plan.many && !TREE ? kv_many_items(a.plan, a.L, a.batch, a.tokens) : a.plan.items;
+  const dim3 grid((unsigned)(a.plan.many && !TREE ? items : a.plan.slots), (unsigned)a.plan.splits);
   hipError_t e = hipErrorInvalidValue;
   if (a.plan.many && a.plan.rows == 128) {
     e = kv_launch(kv_attend_many_kernel<D, 4, F32, TREE>, grid, 256, s, a);
@@ -1134,7 +1364,10 @@ hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
     e = kv_launch(kv_attend_few_kernel<D, 2, F32, TREE>, grid, kWaves * 64, s, a);
   }
   if (a.plan.ws_bytes > 0 && e == hipSuccess)
-    e = kv_launch(kv_attend_join_kernel<D, F32>, dim3((unsigned)items, (unsigned)a.plan.join_groups), kJoinThreads, s, a);
+    e = TREE ? a.plan.join_rows == 0
+                   ? kv_launch(kv_tree_join_few_kernel<D, F32>, dim3((unsigned)a.plan.join_grid), kJoinThreads, s, a)
+                   : kv_launch(kv_tree_join_many_kernel<D, F32>, dim3((unsigned)a.plan.join_grid), 256, s, a)
+             : kv_launch(kv_attend_join_kernel<D, F32>, dim3((unsigned)items, (unsigned)a.plan.join_groups), kJoinThreads, s, a);
   return e;
 }
 

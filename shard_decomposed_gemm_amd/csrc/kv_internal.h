@@ -56,7 +56,16 @@ struct KvAttendArgs {
   int32_t tree_words;
   KvPlan plan;
   float* ws;  // plan.ws_bytes of partials
+  int32_t* joins;  // with a tree, behind the partials: the number of KvJoin, and from 16 bytes on they themselves
   uint64_t* err;  // kv_report.h
+};
+
+// Rows of an item of several runs, for the join.
+struct KvJoin {
+  int64_t row0;        // its sequence's first row of q
+  int32_t h, r0;       // kv head, first row of the head's
+  int32_t rows, runs;  // rows of the head
+  int32_t slot, step;  // the first run's partial, and from one run's to the next
 };
 
 struct KvTreeArgs {

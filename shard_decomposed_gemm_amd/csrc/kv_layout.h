@@ -57,6 +57,10 @@ struct KvPlan {
   int32_t rows;    // rows of one item
   int32_t join_rows, join_groups;  // the join: rows of a workgroup (a power of two), workgroups of an item
   int32_t tiles;   // items of one sequence and kv head
+  int32_t group, row_shift;  // with a tree: query heads of a kv head, log2(rows),
+  int32_t join_grid;         // workgroups of the join (join_rows: of a wave; 0: one row a workgroup),
+  int32_t most_runs;         // of an item,
+  int64_t partials;          // partials that the workspace holds
   int32_t splits, chunk;   // many rows
   int32_t places, least, most;  // few rows: workgroups that run at once, the shortest and the longest run
   int64_t items, slots;    // slots: few rows, the call's runs at most
@@ -208,6 +212,148 @@ inline void kv_many_wide(KvPlan& p, const KvLayout& L, int64_t batch, int64_t ma
   w.tiles = (int32_t)((max_q * (L.Hq / L.Hkv) + 255) / 256);
   w.items = batch * L.Hkv * w.tiles;
   if (kv_many_items(w, L, batch, tokens) >= 4 * num_cus) p = w;
+}
+
+// With a tree: blocks of a run, from the batch's real lengths. U blocks in all
+// items, `longest` in one: `places` runs and a remainder of each item, none
+// shorter than the least, no item of more runs than it has partials for. (Items of
+// several runs, which have more than c blocks, then have 2 U / c <= 2 places runs.)
+KV_HD inline int kv_quotient_up(int x, int d) { return (int)(((uint32_t)x + (uint32_t)d - 1) / (uint32_t)d); }
+KV_HD inline int kv_tree_runs(int chunk, int nblk) { return nblk <= chunk ? 1 : kv_quotient_up(nblk, chunk); }
+KV_HD inline int kv_tree_chunk(const KvPlan& p, int64_t U, int longest) {
+  const int64_t many = U >> 31 ? (U + p.places - 1) / p.places : kv_quotient_up((int)U, p.places);
+  const int c = (int)(many < kKvWhole ? many : kKvWhole);
+  const int joined = kv_quotient_up(longest, p.most_runs);
+  const int least = p.least > joined ? p.least : joined;
+  return c < least ? least : c;
+}
+// A single sequence's, of `per` items: no more runs than run at once.
+KV_HD inline int kv_tree_chunk_of_one(const KvPlan& p, int per, int nblk) {
+  const int c = kv_tree_chunk(p, (int64_t)nblk * per, nblk);
+  if (per == 0 || per > p.places) return c;
+  const int even = kv_quotient_up(nblk, (int)((uint32_t)p.places / (uint32_t)per));
+  return c > even ? c : even;
+}
+// The next try where `runs` runs of c blocks are more than run at once.
+KV_HD inline int kv_tree_longer(const KvPlan& p, int c, int runs) {
+  return c + 1 + (int)((float)c * (float)(runs - p.places) / (float)runs);
+}
+
+// A call with a tree. Its items are (sequence, tile of rows, kv head), whose rows
+// all see nearly all of the sequence. Four forms take them: the kernel for few
+// rows with tiles of 16 or 32 rows, the one for many with 128 or 256. The
+// first two start fast and need no barrier, the others unpack a block once for
+// four or eight waves. Which is faster follows from the work of a place (a
+// workgroup that runs at once with others), by a model fitted to 390 shapes with 8
+// kv heads (1 to 32 sequences of 200 to 32000 tokens, 24 to 512 rows a kv head):
+//   us = first + round max(1, items / places) + (block + full F) B + J (join + runs N / places)
+// with B the blocks of a place, F the part of a tile's rows that exist, J whether
+// items of several runs are joined, N the runs. Its choice takes 1.02 times the
+// best form's time on average (1.3 at worst). In us, of D 128, tiles of 16, 32, 128
+// and 256 rows:
+//   8 sequences of 500 tokens,    64 rows    10.2   12.0   21.4   20.6
+//   8 of 16000,                   64         88.9   69.6   88.3    101
+//   32 of 1000,                  128         53.1   55.0   57.5   38.4
+//   8 of 16000,                  128          147    110    104    109
+//   32 of 2000,                  256          168    161   93.5   88.2
+struct KvForm {
+  int rows, places_per_cu, blocks;  // blocks: of a sequence that is one run for sure
+  double first, round, block, full, join, runs;
+};
+inline int kv_tree_forms(int D, const KvForm** forms) {
+  static const KvForm d64[] = {{16, 2, 64, 3.1, 3.7, .136, 0, 2.6, 7.0}, {32, 1, 32, 5.6, 1.8, .118, 0, 5.0, .3},
+                               {128, 2, 32, 0, 6.2, .528, .133, 4.2, 14.4}};
+  static const KvForm d128[] = {{16, 2, 64, .7, 5.5, .222, 0, .9, 12.9}, {32, 1, 32, 1.9, 6.5, .205, 0, 4.0, 3.0},
+                                {128, 2, 32, 0, 6.9, .775, .208, 4.2, 23.5}, {256, 1, 32, 0, 8.4, .499, .582, 4.5, 17.2}};
+  static const KvForm d256[] = {{16, 1, 64, 2.5, 6.2, .281, 0, 3.9, 3.8}, {128, 1, 32, 0, 11.8, 1.474, .316, 4.6, 16.4}};
+  *forms = D == 64 ? d64 : D == 128 ? d128 : d256;
+  return D == 64 ? 3 : D == 128 ? 4 : 2;
+}
+// The shortest run: four blocks a wave make up for what a run costs beside its
+// blocks; a tile for many rows has large partials, and short runs only where few
+// items leave most of the chip idle (64 rows x 8 heads of 2000 tokens, runs of 8
+// blocks or more 27.8 us, 16 29.2, 32 39.3; 384 rows x 64 heads of 1000 46.8, 46.5,
+// and 37.4 in one run).
+inline int kv_tree_least(int rows, int64_t items, int64_t places) { return rows < 128 ? 32 : items * 8 <= places ? 8 : 16; }
+
+// Runs of an item at most, and partials that items of several runs leave.
+inline int64_t kv_tree_most_runs(int64_t nblk, int64_t least) {
+  const int64_t runs = (nblk + least - 1) / least;
+  return runs < kKvMaxSplits ? runs : kKvMaxSplits;
+}
+inline int64_t kv_tree_partials(int64_t items, int64_t runs, int64_t places) {
+  return items < 2 * places && items * runs < 2 * places ? items * runs : 2 * places;
+}
+
+inline KvPlan kv_tree_plan_as(const KvForm& f, const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
+  KvPlan p{};
+  const int64_t rows = max_q * (L.Hq / L.Hkv), nblk = kv_expected_blocks(max_kv);
+  p.rows = f.rows;
+  p.many = p.rows >= 128;
+  p.group = L.Hq / L.Hkv;
+  p.row_shift = __builtin_ctz((unsigned)p.rows);
+  p.tiles = (int32_t)((rows + p.rows - 1) / p.rows);
+  p.items = batch * L.Hkv * p.tiles;
+  p.slot_floats = (int64_t)p.rows * (L.D + 2);
+  p.splits = 1;
+  p.slots = p.items;
+  p.places = num_cus * f.places_per_cu;
+  p.least = kv_tree_least(p.rows, p.items, p.places);
+  if (p.items == 0 || batch > kKvMaxBatch || nblk <= f.blocks) return p;
+  p.slots = p.items + p.places;
+  p.most_runs = (int32_t)kv_tree_most_runs(nblk, p.least);
+  p.partials = kv_tree_partials(p.items, p.most_runs, p.places);
+  const int64_t live = rows < p.rows ? rows : p.rows, joins = p.items < p.places ? p.items : p.places;
+  // The join: a workgroup a row for few rows, some rows a wave for many.
+  p.join_rows = joins * live <= 2 * num_cus ? 0 : 256 / L.D;
+  p.join_groups = (int32_t)(p.join_rows ? (live + p.join_rows - 1) / p.join_rows : live);
+  const int64_t grid = p.join_rows ? (joins * p.join_groups + 3) / 4 : joins * live;
+  p.join_grid = (int32_t)(grid < 4 * num_cus ? grid : 4 * num_cus);
+  p.ws_bytes = p.partials * p.slot_floats * 4 + 16 + joins * 32;
+  return p;
+}
+inline double kv_tree_us(const KvForm& f, const KvPlan& p, int64_t rows, int64_t nblk) {
+  const double per_place = (double)p.items / p.places;
+  const bool split = p.slots > p.items;
+  double chain = (double)(split && nblk > p.least ? p.least : nblk);
+  if (per_place * nblk > chain) chain = per_place * nblk;
+  double runs = chain > 0 ? per_place * nblk / chain : 0;
+  if (runs < per_place) runs = per_place;
+  const double fill = (double)rows / ((double)p.tiles * p.rows);
+  return f.first + f.round * (per_place > 1 ? per_place : 1) + (f.block + f.full * fill) * chain +
+         (split ? f.join + f.runs * (runs < 1 ? runs : 1) * fill : 0);
+}
+inline KvPlan kv_tree_plan(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
+  const KvForm* forms;
+  const int n = kv_tree_forms(L.D, &forms);
+  const int64_t rows = max_q * (L.Hq / L.Hkv), nblk = kv_expected_blocks(max_kv);
+  KvPlan best{};
+  double least = 0;
+  for (int i = 0; i < n; ++i) {
+    if (forms[i].rows >= 128 && rows <= 32) break;  // their partials would be the most of a decoder's workspace
+    const KvPlan p = kv_tree_plan_as(forms[i], L, batch, max_q, max_kv, num_cus);
+    const double us = kv_tree_us(forms[i], p, rows, nblk);
+    if (i == 0 || us < least) best = p, least = us;
+  }
+  return best;
+}
+// Workspace bytes for every call with a tree within these bounds: each form's need grows with each of them.
+inline int64_t kv_tree_bound(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
+  const KvForm* forms;
+  const int n = kv_tree_forms(L.D, &forms);
+  const int64_t rows = max_q * (L.Hq / L.Hkv), nblk = kv_expected_blocks(max_kv);
+  int64_t bytes = 0;
+  for (int i = 0; i < n; ++i) {
+    const KvForm& f = forms[i];
+    if (f.rows >= 128 && rows <= 32) break;
+    if (nblk <= f.blocks) continue;
+    const int64_t some = batch < kKvMaxBatch ? batch : kKvMaxBatch, places = (int64_t)num_cus * f.places_per_cu;
+    const int64_t items = some * L.Hkv * ((rows + f.rows - 1) / f.rows);
+    const int64_t need = kv_tree_partials(items, kv_tree_most_runs(nblk, f.rows < 128 ? 32 : 8), places) * f.rows * (L.D + 2) * 4 + 16 +
+                         (items < places ? items : places) * 32;
+    bytes = bytes > need ? bytes : need;
+  }
+  return bytes;
 }
 
 constexpr int kKvNodes = 1024;       // of one tree

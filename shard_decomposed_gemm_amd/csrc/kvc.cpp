@@ -60,7 +60,7 @@ int attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, const uint
   KvPlan plan{};
   if (p && p->batch >= 0 && p->batch <= kKvMaxTokens && p->max_q >= 1 && p->max_q <= kKvMaxTokens &&
       p->max_kv >= 1)  // refused below otherwise
-    plan = kv_attend_plan(ctx->L, p->batch, p->max_q, p->max_kv, ctx->num_cus);
+    plan = (mask ? kv_tree_plan : kv_attend_plan)(ctx->L, p->batch, p->max_q, p->max_kv, ctx->num_cus);
   char why[kKvWhy];
   const int rc = kv_check_attend(ctx->L, pages, p, plan, workspace, workspace_bytes, why);
   if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);
@@ -86,9 +86,10 @@ int attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, const uint
   a.lse = p->lse;
   a.tree = mask;
   a.tree_words = mask_words;
-  kv_many_wide(plan, ctx->L, p->batch, p->max_q, p->max_kv, p->tokens, ctx->num_cus);
+  if (!mask) kv_many_wide(plan, ctx->L, p->batch, p->max_q, p->max_kv, p->tokens, ctx->num_cus);
   a.plan = plan;
   a.ws = static_cast<float*>(workspace);
+  a.joins = reinterpret_cast<int32_t*>(a.ws + plan.partials * plan.slot_floats);
   a.err = ctx->err_dev;
   OnDevice on(ctx->device);
   if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");
@@ -197,6 +198,8 @@ int kvc_attend_workspace(const kvc_ctx* ctx, int32_t batch, int32_t max_q, int64
   if (!ctx || !bytes || batch < 0 || max_q < 1 || max_kv < 1) return AGEMM_EINVAL;
   if (batch > kKvMaxTokens || max_q > kKvMaxTokens) return AGEMM_ESHAPE;
   *bytes = kv_attend_bound(ctx->L, batch, max_q, max_kv, ctx->num_cus);
+  const int64_t tree = kv_tree_bound(ctx->L, batch, max_q, max_kv, ctx->num_cus);
+  if (*bytes < tree) *bytes = tree;
   return AGEMM_OK;
 }
 

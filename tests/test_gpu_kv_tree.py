@@ -279,9 +279,56 @@ def test_attend_a_tree(Hq, Hkv, D, page, shape, words, kind, q_off, f32):
     assert (got[starts[-1]:] == PAD).all() and (lse[starts[-1]:] == PAD).all()
 
 
+FORMS = [
+    # Hq, Hkv, D, page, [(queries, length)], max_kv: every kernel, one run an item and several, joined by rows and by
+    # workgroups, a batch of more sequences than lengths are looked through, lengths that max_kv does not say
+    (8, 1, 128, 64, [(2, 5000)], None),
+    (8, 1, 128, 64, [(4, 9000)], 1300),
+    (8, 1, 64, 32, [(4, 9000), (3, 100), (4, 5000)], 3000),
+    (4, 1, 256, 64, [(4, 6000), (2, 300)], None),
+    (8, 1, 256, 64, [(40, 6000), (20, 2500), (1, 40)], None),
+    (16, 1, 256, 64, [(64, 3000)], None),
+    (8, 2, 128, 64, [(16, 3500)] * 4, 3500),
+    (8, 2, 128, 64, [(13, 3000), (16, 20), (0, 900), (5, 2000)], 5000),
+    (8, 2, 64, 32, [(64, 4000), (30, 100), (9, 2000)], None),
+    (16, 2, 128, 64, [(40, 2500), (64, 1100), (33, 35)], None),
+    (16, 2, 128, 64, [(64, 6000)], 1100),
+    (24, 8, 128, 64, [(48, 1500)] * 6, None),
+    (4, 4, 128, 32, [(i % 3, i % 3 + 1400 if i == 300 else i % 40 + 3) for i in range(520)], 1400),
+    (2, 1, 128, 32, [(40 if i == 70 else i % 4, 1500 if i in (3, 70) else i % 90 + 40) for i in range(130)], 1500),
+    (8, 1, 64, 32, [(i % 9, 60 * i + 9) for i in range(70)], None),
+]
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,D,page,shape,max_kv", FORMS)
+def test_attend_a_tree_in_every_form(Hq, Hkv, D, page, shape, max_kv, f32):
+    print(f"[kv tree forms] {Hq} {Hkv} {D} {page} {shape[:4]} {len(shape)} {max_kv} {f32}", flush=True)
+    r = np.random.default_rng(len(shape) + D)
+    lens = [n for _, n in shape]
+    starts = _starts([n for n, _ in shape])
+    pages, table, K, V = _sequences(Hq + D, Hkv, D, page, lens)
+    kv = _cache(Hq, Hkv, D, page_tokens=page, num_pages=pages.shape[0])
+    mask = np.concatenate([okt.masks(_parents(r, n), 1) for n, _ in shape])
+    q = r.standard_normal((int(starts[-1]), Hq, D)).astype(np.float16)
+    most = max(n for n, _ in shape)
+    ws = kv.workspace(len(shape), most, max_kv or table.shape[1] * page)
+    ws.fill_(0xFF)
+    dp, dq = _dev(pages), _dev(q)
+    got, lse = _run_attend(kv, dp, table, lens, dq, starts, most, mask, f32=f32, max_kv=max_kv, workspace=ws)
+    kv.check()
+    for b, (n, L) in enumerate(shape):
+        rows = slice(starts[b], starts[b + 1])
+        if n:
+            _check_rows(got[rows], lse[rows], q[rows], K[b], V[b], okt.visible(mask[rows], L - n, L), D ** -0.5, f32)
+    again = _run_attend(kv, dp, table, lens, dq, starts, most, mask, f32=f32, max_kv=max_kv, with_lse=False)[0]
+    kv.check()
+    np.testing.assert_array_equal(got, again)
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,n,L", [(4, 2, 128, 3, 500), (8, 2, 64, 40, 200), (2, 2, 256, 20, 90), (8, 1, 128, 64, 3000)])
-def test_a_chain_gives_the_bits_of_the_causal_mask(Hq, Hkv, D, n, L):
-    """A tree without branches sees what a causal call sees."""
+def test_a_chain_sees_what_the_causal_mask_does(Hq, Hkv, D, n, L):
+    """A tree without branches: both calls are within the oracle's bounds, on the same tokens."""
     import torch
     pages, table, K, V = _sequences(5, Hkv, D, 64, [L])
     kv = _cache(Hq, Hkv, D, page_tokens=64, num_pages=pages.shape[0])
@@ -293,7 +340,9 @@ def test_a_chain_gives_the_bits_of_the_causal_mask(Hq, Hkv, D, n, L):
         kv.attend(_dev(pages), q, _i32([L]), _i32(table), out, q_start=_i32([0, n]), max_q=n, max_kv=L, workspace=ws, tree=tree)
         torch.cuda.synchronize()
     kv.check()
-    assert torch.equal(*outs)
+    seen = np.arange(L) <= L - n + np.arange(n)[:, None]
+    for out in outs:
+        _check_rows(out.cpu().numpy().astype(np.float64), None, q.cpu().numpy(), K[0], V[0], seen, D ** -0.5, True)
 
 
 @pytest.mark.parametrize("n", [2, 40])

@@ -39,6 +39,12 @@ def host(tmp_path_factory):
     lib.kvt_verify_plan.argtypes = [i64, i64, ctypes.c_int, i64, ctypes.c_int, ctypes.POINTER(i32)]
     lib.kvt_verify_bound.argtypes = [i64, i64, ctypes.c_int]
     lib.kvt_verify_bound.restype = i64
+    ints, longs = ctypes.POINTER(i32), ctypes.POINTER(i64)
+    lib.kvt_plan.argtypes = [ctypes.c_int] * 3 + [i64] * 3 + [ctypes.c_int, longs]
+    lib.kvt_plan.restype = None
+    lib.kvt_bound.argtypes = [ctypes.c_int] * 3 + [i64] * 3 + [ctypes.c_int]
+    lib.kvt_bound.restype = i64
+    lib.kvt_shared.argtypes = [ctypes.c_int, ctypes.c_int, ints, ints, longs, longs, longs]
     lib.kvt_report.argtypes = [ctypes.c_uint32, i64, i64, st]
     return lib
 
@@ -205,6 +211,71 @@ def test_verify_plans_cover_the_vocabulary_within_their_bound(host, cus):
                 need = batch * parts * rounds * 8
                 for more in ((batch, vocab), (batch + 1, vocab), (min(2 * batch, 1 << 20), min(1 << 28, 3 * vocab)), (1 << 20, 1 << 28)):
                     assert need <= host.kvt_verify_bound(*more, cus)
+
+
+PLAN = ("rows", "many", "tiles", "items", "slots", "places", "least", "most_runs", "partials", "join_rows", "join_groups",
+        "join_grid", "ws_bytes")
+
+
+def _plan(host, *shape):
+    out = (ctypes.c_int64 * len(PLAN))()
+    host.kvt_plan(*shape, out)
+    return dict(zip(PLAN, out))
+
+
+HEADS = [(64, 8), (96, 8), (8, 8), (1, 1), (1024, 1), (1024, 1024), (12, 4)]
+
+
+@pytest.mark.parametrize("cus", [32, 256, 304])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_tree_plans_hold_any_lengths(host, D, cus):
+    """What the kernels make of a batch's lengths - those of the bounds, shorter and longer ones - fits the grid, the
+    partials and the list of items to join."""
+    r = np.random.default_rng(D + cus)
+    for _ in range(1500):
+        Hq, Hkv = HEADS[r.integers(len(HEADS))]
+        batch, max_q, max_kv = (int(np.exp(r.uniform(0, np.log(top)))) for top in (600, 1100, 1 << 22))
+        p = _plan(host, Hq, Hkv, D, batch, max_q, max_kv, cus)
+        assert p["items"] == batch * Hkv * p["tiles"] and p["tiles"] * p["rows"] >= max_q * Hq // Hkv
+        assert p["rows"] in ((16, 128) if D == 256 else (16, 32, 128) if D == 64 else (16, 32, 128, 256))
+        if p["slots"] == p["items"]:
+            assert p["ws_bytes"] == 0 or batch > 512
+            continue
+        assert p["ws_bytes"] == p["partials"] * p["rows"] * (D + 2) * 4 + 16 + 32 * min(p["items"], p["places"])
+        assert (p["join_rows"] or 1) * p["join_groups"] >= min(p["rows"], max_q * Hq // Hkv)
+        for top in (max_kv, 1 << 12, (1 << 31) - 1, max(1, max_kv // 50)):
+            n = min(batch, 512)
+            lens = np.minimum(top, np.exp(r.uniform(0, np.log(top + 1), n))).astype(np.int64)
+            if r.random() < 0.4:
+                lens[:] = top
+            blocks = np.ascontiguousarray(-(-lens // 32), dtype=np.int32)
+            queries = np.ascontiguousarray(r.integers(0, max_q + 1, n) if r.random() < 0.5 else np.full(n, max_q), dtype=np.int32)
+            at = lambda x: x.ctypes.data_as(ctypes.POINTER(ctypes.c_int32))  # noqa: E731
+            got = [ctypes.c_int64() for _ in range(3)]
+            chunk = host.kvt_shared(Hkv, n, at(blocks), at(queries), *[ctypes.byref(x) for x in got])
+            work, partials, joins = (x.value for x in got)
+            assert work <= p["slots"] and partials <= p["partials"] and joins <= min(p["items"], p["places"])
+            assert -(-int(blocks.max()) // chunk) <= 256
+
+
+@pytest.mark.parametrize("cus", [32, 256, 304])
+def test_tree_workspace_of_bounds_holds_every_smaller_call(host, cus):
+    r = np.random.default_rng(cus)
+    for _ in range(4000):
+        Hq, Hkv = HEADS[r.integers(len(HEADS))]
+        D = (64, 128, 256)[r.integers(3)]
+        most = [int(np.exp(r.uniform(0, np.log(top)))) for top in (2000, 1100, 1 << 20)]
+        less = [int(np.exp(r.uniform(0, np.log(top)))) for top in most]
+        bound = host.kvt_bound(Hq, Hkv, D, *most, cus)
+        assert _plan(host, Hq, Hkv, D, *less, cus)["ws_bytes"] <= bound
+        assert _plan(host, Hq, Hkv, D, *most, cus)["ws_bytes"] <= bound
+
+
+def test_tree_plans_at_the_ends(host):
+    assert _plan(host, 64, 8, 128, 0, 5, 100, 256)["items"] == 0
+    p = _plan(host, 64, 8, 128, 1, 1, 1 << 40, 256)
+    assert p["partials"] <= 1024 and p["most_runs"] == 256
+    assert _plan(host, 1024, 1, 64, 1 << 20, 1024, 1 << 31, 256)["items"] >= 1 << 20  # refused for its items
 
 
 def test_reports(host):
