@@ -244,28 +244,29 @@ KV_HD inline int kv_tree_longer(const KvPlan& p, int c, int runs) {
 // rows with tiles of 16 or 32 rows, the one for many with 128 or 256. The
 // first two start fast and need no barrier, the others unpack a block once for
 // four or eight waves. Which is faster follows from the work of a place (a
-// workgroup that runs at once with others), by a model fitted to 390 shapes with 8
+// workgroup that runs at once with others), by a model fitted to 480 shapes with 8
 // kv heads (1 to 32 sequences of 200 to 32000 tokens, 24 to 512 rows a kv head):
 //   us = first + round max(1, items / places) + (block + full F) B + J (join + runs N / places)
 // with B the blocks of a place, F the part of a tile's rows that exist, J whether
 // items of several runs are joined, N the runs. Its choice takes 1.02 times the
-// best form's time on average (1.3 at worst). In us, of D 128, tiles of 16, 32, 128
+// best form's time on average (1.4 at worst). In us, of D 128, tiles of 16, 32, 128
 // and 256 rows:
 //   8 sequences of 500 tokens,    64 rows    10.2   12.0   21.4   20.6
 //   8 of 16000,                   64         88.9   69.6   88.3    101
 //   32 of 1000,                  128         53.1   55.0   57.5   38.4
 //   8 of 16000,                  128          147    110    104    109
-//   32 of 2000,                  256          168    161   93.5   88.2
+//   32 of 8000,                  128                 237    190    200
+//   8 of 16000,                  384                 324    311    261
 struct KvForm {
   int rows, places_per_cu, blocks;  // blocks: of a sequence that is one run for sure
   double first, round, block, full, join, runs;
 };
 inline int kv_tree_forms(int D, const KvForm** forms) {
-  static const KvForm d64[] = {{16, 2, 64, 3.1, 3.7, .136, 0, 2.6, 7.0}, {32, 1, 32, 5.6, 1.8, .118, 0, 5.0, .3},
-                               {128, 2, 32, 0, 6.2, .528, .133, 4.2, 14.4}};
-  static const KvForm d128[] = {{16, 2, 64, .7, 5.5, .222, 0, .9, 12.9}, {32, 1, 32, 1.9, 6.5, .205, 0, 4.0, 3.0},
-                                {128, 2, 32, 0, 6.9, .775, .208, 4.2, 23.5}, {256, 1, 32, 0, 8.4, .499, .582, 4.5, 17.2}};
-  static const KvForm d256[] = {{16, 1, 64, 2.5, 6.2, .281, 0, 3.9, 3.8}, {128, 1, 32, 0, 11.8, 1.474, .316, 4.6, 16.4}};
+  static const KvForm d64[] = {{16, 2, 64, 3.2, 3.3, .148, 0, 2.6, 6.9}, {32, 1, 32, 5.6, 1.9, .117, 0, 5.1, .4},
+                               {128, 2, 32, 0, 5.1, .572, .187, 4.9, 13.1}};
+  static const KvForm d128[] = {{16, 2, 64, 1.0, 4.6, .248, 0, .9, 12.7}, {32, 1, 32, 2.0, 6.4, .203, 0, 4.0, 3.1},
+                                {128, 2, 32, 0, 4.9, .864, .319, 5.4, 20.9}, {256, 1, 32, 0, 8.6, .525, .523, 4.1, 17.1}};
+  static const KvForm d256[] = {{16, 1, 64, 3.1, 6.2, .264, 0, 3.6, 6.4}, {128, 1, 32, 0, 13.1, 1.55, .125, 2.9, 19.0}};
   *forms = D == 64 ? d64 : D == 128 ? d128 : d256;
   return D == 64 ? 3 : D == 128 ? 4 : 2;
 }
