@@ -81,6 +81,22 @@ struct KvTreeArgs {
   uint64_t* err;  // kv_report.h
 };
 
+// How far a sequence's verification has come (kv_verify.hip says what A, S and Z are).
+struct KvWalk {
+  double A, S, Z;
+  int32_t node, last;      // where it is, the child tried last
+  int32_t count, rejects;  // accepted nodes, tokens rejected at the last of them (without q)
+  int32_t pending, wants;  // Z is out of date; the walk needs it to go on (else it has ended)
+  int32_t done, unused;
+};
+// A line of its own: workgroups of all XCDs count in it.
+struct KvVerifyState {
+  KvWalk walk;
+  uint32_t arrived[kKvRounds];  // parts that are summed, of each round
+  uint8_t rest[kKvStateBytes - sizeof(KvWalk) - 4 * kKvRounds];
+};
+static_assert(sizeof(KvVerifyState) == kKvStateBytes, "the workspace's bound counts them");
+
 struct KvVerifyArgs {
   int32_t batch, max_q;
   int64_t tokens;
@@ -93,7 +109,8 @@ struct KvVerifyArgs {
   int32_t *path, *count;
   int64_t* next;
   KvVerifyPlan plan;
-  double* ws;     // batch x rounds x parts sums
+  KvVerifyState* states;  // batch
+  double* sums;           // batch x segments of all parts
   uint64_t* err;  // kv_report.h
 };
 

@@ -369,30 +369,40 @@ inline int kv_commit_piece(const KvLayout& L, int64_t batch) {
 
 // How a verification's rows of probabilities are summed: in `parts` parts of
 // `part` tokens each, one workgroup a part, in `rounds` launches. A round sums
-// what the walk asks for next; what is left after the last round, the last
-// kernel sums alone.
+// what the walk asks for next; what is left after the last round, its last
+// workgroup sums alone.
 struct KvVerifyPlan {
   int32_t parts, part, rounds;
 };
-constexpr int kKvParts = 64;  // at most: a wave adds them up
-constexpr int kKvRounds = 3;
+constexpr int kKvParts = 64;   // at most
+constexpr int kKvRounds = 8;   // for siblings drawn from q
+constexpr int kKvStateBytes = 128;  // of a sequence: how far it has come, parts that are summed
+inline int64_t kv_verify_parts(int64_t batch, int64_t vocab, int num_cus) {
+  // Four workgroups a CU, of 2048 tokens at the least and 16384 at the most (the
+  // draw looks through a quarter of a part).
+  int64_t parts = (4 * num_cus + batch - 1) / (batch > 0 ? batch : 1), most = (vocab + 2047) / 2048;
+  const int64_t least = (vocab + 16383) / 16384;
+  parts = parts > least ? parts : least;
+  parts = parts < most ? parts : most;
+  return parts < kKvParts ? parts : kKvParts;
+}
 inline KvVerifyPlan kv_verify_plan(int64_t batch, int64_t vocab, bool drawn, int64_t max_children, int num_cus) {
   KvVerifyPlan p{};
-  // Four workgroups a CU, of 2048 tokens at the least (two loads a thread).
-  int64_t parts = (4 * num_cus + batch - 1) / (batch > 0 ? batch : 1), most = (vocab + 2047) / 2048;
-  parts = parts < most ? parts : most;
-  parts = parts < kKvParts ? parts : kKvParts;
+  int64_t parts = kv_verify_parts(batch, vocab, num_cus);
+  const int64_t fits = (int64_t{1} << 23) / (batch > 0 ? batch : 1);  // grids stay below 2^32 threads
+  parts = parts < fits ? parts : fits;
   const int64_t part = ((vocab + parts - 1) / parts + 1023) / 1024 * 1024;
   p.part = (int32_t)part;
   p.parts = (int32_t)((vocab + part - 1) / part);
   p.rounds = drawn && max_children > 1 ? kKvRounds : 1;
   return p;
 }
-// Bytes for every verification of up to `batch` sequences and `vocab` tokens: batch x parts < batch + 4 num_cus.
+inline int64_t kv_verify_bytes(const KvVerifyPlan& p, int64_t batch) { return batch * ((int64_t)p.parts * 32 + kKvStateBytes); }
+// Bytes for every verification of up to `batch` sequences and `vocab` tokens.
 inline int64_t kv_verify_bound(int64_t batch, int64_t vocab, int num_cus) {
-  const int64_t most = (vocab + 2047) / 2048 < kKvParts ? (vocab + 2047) / 2048 : kKvParts;
-  const int64_t some = batch + 4 * num_cus, all = batch * most;
-  return (some < all ? some : all) * kKvRounds * 8;
+  const int64_t most = (vocab + 2047) / 2048 < kKvParts ? (vocab + 2047) / 2048 : kKvParts, all = batch * most;
+  const int64_t some = batch * ((vocab + 16383) / 16384 + 1) + 4 * num_cus;
+  return (some < all ? some : all) * 32 + batch * kKvStateBytes;
 }
 
 }  // namespace agemm

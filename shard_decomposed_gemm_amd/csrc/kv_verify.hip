@@ -14,10 +14,11 @@
 // neighbours lie that far apart), so that sums in binary64 are exact up to 8 and
 // do not depend on how the vocabulary is split.
 //
-// Bytes: the row of p (and q) that the last token is drawn from. The walk is
-// latency: parents, tokens and numbers, then p and q of every draft, then some
-// 0.2 us a level. Every workgroup of a part walks by itself, which costs no
-// launch; the sums of the parts it stores are read by the next launch.
+// One workgroup a sequence begins the walk (parents, tokens and numbers, then p
+// and q of every draft, then some 0.2 us a level). A round then sums the row that
+// the walk has come to, by `parts` workgroups a sequence; the one that is done
+// last goes on with it: to the next node that wants a sum, which is the next
+// round's, or to the end, where it draws. The last round goes on alone.
 #include "kv_internal.h"
 
 namespace agemm {
@@ -31,19 +32,18 @@ struct __attribute__((packed, aligned(4))) Quad {  // rows of odd vocabularies a
 constexpr double kGrid = 4.0;
 constexpr float kBelowOne = 0x1.fffffep-1f;
 
+__device__ inline float number(float u) { return u > 0.f ? fminf(u, kBelowOne) : 0.f; }
 __device__ inline float unit(float x) { return fminf(fmaxf(x, 0.f), 1.f); }  // NaN: 0
+
+constexpr int kThreads = 256;
+constexpr int kSegments = kThreads / 64;  // of a part, a wave each
 
 struct Shared {
   int32_t token[kKvNodes];  // -1: outside the vocabulary
   float p[kKvNodes], q[kKvNodes], u[kKvNodes];
   int16_t parent[kKvNodes];
-  int16_t path[kKvNodes];
-  int32_t rejected[kKvNodes];  // tokens, at the current node, without q
-  // what the walk left
-  int32_t node, count, rejects, wants;  // wants: 1 if it needs a sum to go on, 0 at its end
-  int32_t last;                         // the child tried last
-  double A, S, Z;
-  bool pending;  // Z is out of date
+  int32_t path[kKvNodes];  // accepted nodes, then (without q) the tokens rejected at the last of them
+  KvWalk walk;
 };
 
 template <bool DRAWN>
@@ -69,7 +69,7 @@ __device__ inline Rows rows_of(const KvVerifyArgs& a, int b) {
 // The tree, and p and q of every draft at its parent, to LDS.
 template <bool DRAWN>
 __device__ inline void load_tree(const KvVerifyArgs& a, const Rows& r, Shared& s, bool tell) {
-  for (int i = threadIdx.x; i < r.n; i += blockDim.x) {
+  for (int i = threadIdx.x; i < r.n; i += kThreads) {
     const int64_t row = r.row0 + i;
     const int parent = a.parent[row];
     const int64_t token = a.token[row];
@@ -80,7 +80,7 @@ __device__ inline void load_tree(const KvVerifyArgs& a, const Rows& r, Shared& s
     if (tell && i > 0 && !known) kv_report(a.err, kKvToken, row, token);
     s.parent[i] = (int16_t)(ok ? parent : -1);
     s.token[i] = known ? (int)token : -1;
-    s.u[i] = u > 0.f ? fminf(u, kBelowOne) : 0.f;
+    s.u[i] = number(u);
     if (ok && known && parent >= 0) {
       s.p[i] = unit(a.p[(r.row0 + parent) * a.p_stride + token]);
       if constexpr (DRAWN) s.q[i] = unit(a.q[(r.row0 + parent) * a.q_stride + token]);
@@ -88,85 +88,62 @@ __device__ inline void load_tree(const KvVerifyArgs& a, const Rows& r, Shared& s
   }
 }
 
-// Goes on with the walk, by one wave, until it needs a sum or ends.
+// Goes on with the walk from w, by one wave, until it needs a sum or ends.
 template <bool DRAWN>
-__device__ inline void walk(Shared& s, int n, int lane) {
-  int cur = s.node, last = s.last, count = s.count, rejects = s.rejects;
-  double A = s.A, S = s.S, Z = s.Z;
-  bool pending = s.pending;
-  int wants = 0;
+__device__ inline void go_on(Shared& s, KvWalk w, int n, int lane) {
+  w.wants = 0;
   for (;;) {
-    // the next child of cur, and whether an earlier one had its token
+    // the next child of the node, and whether an earlier one had its token
     int c = -1;
-    for (int i0 = last & ~63; i0 < n && c < 0; i0 += 64) {
+    for (int i0 = w.last & ~63; i0 < n && c < 0; i0 += 64) {
       const int i = i0 + lane;
-      const uint64_t is = __ballot(i > last && i < n && s.parent[i] == cur);
+      const uint64_t is = __ballot(i > w.last && i < n && s.parent[i] == w.node);
       if (is) c = i0 + __builtin_ctzll(is);
     }
     if (c < 0) break;
     const int x = s.token[c];
     bool again = x < 0;
-    for (int i0 = cur & ~63; i0 < c && !again; i0 += 64) {
+    for (int i0 = w.node & ~63; i0 < c && !again; i0 += 64) {
       const int i = i0 + lane;
-      again = __any(i > cur && i < c && s.parent[i] == cur && s.token[i] == x);
+      again = __any(i > w.node && i < c && s.parent[i] == w.node && s.token[i] == x);
     }
-    if (again || (DRAWN && !(S < 1.0)) || (!pending && !(Z > 0.0))) {
-      last = c;
+    if (again || (DRAWN && !(w.S < 1.0)) || (!w.pending && !(w.Z > 0.0))) {
+      w.last = c;
       continue;
     }
-    if (pending) {
-      wants = 1;
+    if (w.pending) {
+      w.wants = 1;
       break;
     }
-    last = c;
+    w.last = c;
     const double p = s.p[c], u = s.u[c];
     bool take;
     if constexpr (DRAWN) {
-      const double q = s.q[c], w = __builtin_fma(-A, q, p);
-      take = u * q * Z < (w > 0.0 ? w : 0.0) * (1.0 - S);
+      const double q = s.q[c], left = __builtin_fma(-w.A, q, p);
+      take = u * q * w.Z < (left > 0.0 ? left : 0.0) * (1.0 - w.S);
       if (!take) {
-        A += Z / (1.0 - S);
-        S += q;
-        pending = true;
+        w.A += w.Z / (1.0 - w.S);
+        w.S += q;
+        w.pending = 1;
       }
     } else {
-      take = u * Z < p;
+      take = u * w.Z < p;
       if (!take) {
-        Z -= p;
-        if (lane == 0) s.rejected[rejects] = x;
-        ++rejects;
+        w.Z -= p;
+        if (lane == 0) s.path[w.count + w.rejects] = x;
+        ++w.rejects;
       }
     }
     if (take) {
-      if (lane == 0) s.path[count] = (int16_t)c;
-      ++count;
-      cur = c;
-      rejects = 0;
-      A = S = 0.0;
-      Z = 1.0;
-      pending = false;
+      if (lane == 0) s.path[w.count] = c;
+      ++w.count;
+      w.node = c;
+      w.rejects = w.pending = 0;
+      w.A = w.S = 0.0;
+      w.Z = 1.0;
     }
   }
-  if (lane == 0) {
-    s.node = cur;
-    s.last = last;
-    s.count = count;
-    s.rejects = rejects;
-    s.A = A;
-    s.S = S;
-    s.Z = Z;
-    s.pending = pending;
-    s.wants = wants;
-  }
-}
-
-__device__ inline void start_walk(Shared& s) {
-  s.node = s.last = s.rejects = 0;
-  s.count = 1;
-  s.path[0] = 0;
-  s.A = s.S = 0.0;
-  s.Z = 1.0;
-  s.pending = false;
+  if (lane == 0) s.walk = w;
 }
 
 __device__ inline double wave_sum(double x) {
@@ -175,232 +152,349 @@ __device__ inline double wave_sum(double x) {
   return x;
 }
 
-// Sum of the weights of tokens t0 .. t1 - 1 over a workgroup, valid in thread 0.
-template <bool DRAWN, int THREADS>
-__device__ inline double sum_part(const KvVerifyArgs& a, const Rows& r, const Shared& s, int t0, int t1, double* meet) {
-  const float* p = a.p + (r.row0 + s.node) * a.p_stride;
-  const float* q = DRAWN ? a.q + (r.row0 + s.node) * a.q_stride : p;
-  const double A = s.A;
+// Begins the walk of a sequence; `keeps`: and leaves how far it has come. False if there is nothing to walk.
+template <bool DRAWN>
+__device__ inline bool begin(const KvVerifyArgs& a, int b, Shared& s, bool keeps, int64_t& row0) {
+  const int tid = threadIdx.x;
+  const Rows r = rows_of(a, b);
+  row0 = r.row0;
+  if (r.n == 0) {
+    if (keeps && tid == 0) {
+      a.count[b] = 0;
+      a.next[b] = -1;
+      a.states[b].walk.done = 1;
+      if (!r.usable) kv_report(a.err, kKvRows, b, (int64_t)a.q_start[b + 1] - a.q_start[b]);
+    }
+    return false;
+  }
+  load_tree<DRAWN>(a, r, s, keeps);
+  if (tid == 0) s.path[0] = 0;
+  __syncthreads();
+  if (tid < 64) go_on<DRAWN>(s, KvWalk{0.0, 0.0, 1.0, 0, 0, 1, 0, 0, 0, 0, 0}, r.n, tid);
+  __syncthreads();
+  if (keeps) {
+    const KvWalk w = s.walk;
+    for (int i = tid; i < r.n; i += kThreads) a.path[r.row0 + i] = i < w.count + w.rejects ? s.path[i] : -1;
+    if (tid == 0) a.states[b].walk = w;
+  }
+  return true;
+}
+
+// A wave's sum of the weights of tokens t0 .. t1 - 1 of a row.
+template <bool DRAWN>
+__device__ inline double sum_segment(const float* p, const float* q, double A, int t0, int t1, int lane) {
   double sum = 0.0;
-  int t = t0 + 4 * (int)threadIdx.x;
+  int t = t0 + 4 * lane;
 #pragma unroll 4
-  for (; t + 4 <= t1; t += 4 * THREADS) {
+  for (; t + 4 <= t1; t += 256) {
     const float4v x = reinterpret_cast<const Quad*>(p + t)->x, y = DRAWN ? reinterpret_cast<const Quad*>(q + t)->x : x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum += weight<DRAWN>(A, x[i], y[i]);
   }
   for (; t < t1; ++t) sum += weight<DRAWN>(A, p[t], q[t]);
-  if constexpr (!DRAWN)  // rejected tokens have no weight
-    for (int i = threadIdx.x; i < s.rejects; i += THREADS) {
-      const int x = s.rejected[i];
-      if (x >= t0 && x < t1) sum -= weight<false>(0.0, p[x], 0.f);
-    }
-  sum = wave_sum(sum);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) meet[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  sum = 0.0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) sum += meet[w];
-  return sum;
+  return wave_sum(sum);
 }
 
-// Round k: walks with the sums of the rounds before it, and sums this
-// workgroup's part of what the walk asks for then, or of the last draw.
-constexpr int kRoundThreads = 256;
-template <bool DRAWN>
-__global__ __launch_bounds__(kRoundThreads) void kv_verify_round_kernel(KvVerifyArgs a, int round) {
-  __shared__ Shared s;
-  __shared__ double meet[kRoundThreads / 64];
-  const int b = blockIdx.x / a.plan.parts, part = blockIdx.x - b * a.plan.parts, lane = threadIdx.x & 63;
-  const Rows r = rows_of(a, b);
-  if (r.n == 0) return;
-  load_tree<DRAWN>(a, r, s, part == 0 && round == 0);
-  if (threadIdx.x == 0) start_walk(s);
-  double* sums = a.ws + (int64_t)b * a.plan.rounds * a.plan.parts;
-  __syncthreads();
-  bool done = false;
-  for (int k = 0; k <= round && !done; ++k) {
-    if (threadIdx.x < 64) {
-      if (k > 0) {
-        const double z = wave_sum(lane < a.plan.parts ? sums[(k - 1) * a.plan.parts + lane] : 0.0);
-        if (lane == 0) {
-          s.Z = z;
-          s.pending = false;
-        }
-      }
-      walk<DRAWN>(s, r.n, lane);
-    }
-    __syncthreads();
-    done = !s.wants;
-    if (done && k < round) return;  // an earlier round summed the last draw
-    __syncthreads();
-  }
-  const int t0 = part * a.plan.part, t1 = t0 + a.plan.part < a.vocab ? t0 + a.plan.part : a.vocab;
-  const double sum = sum_part<DRAWN, kRoundThreads>(a, r, s, t0, t1, meet);
-  if (threadIdx.x == 0) sums[round * a.plan.parts + part] = sum;
+__device__ inline double load_sum(const double* p) {
+  return __builtin_bit_cast(double, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+}
+__device__ inline void store_sum(double* p, double x) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, x), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Walks with the sums of all rounds and sums what they left, then draws: the
-// part that holds the number, and in it the token.
-constexpr int kPickThreads = 1024;
+// The row that a walk has come to, and its sums.
 template <bool DRAWN>
-__global__ __launch_bounds__(kPickThreads) void kv_verify_pick_kernel(KvVerifyArgs a) {
-  __shared__ Shared s;
-  __shared__ double meet[kPickThreads / 64];
-  __shared__ double parts[kKvParts];
-  __shared__ int found;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const Rows r = rows_of(a, b);
-  if (r.n == 0) {
-    if (tid == 0) {
-      a.count[b] = 0;
-      a.next[b] = -1;
-      if (!r.usable) kv_report(a.err, kKvRows, b, (int64_t)a.q_start[b + 1] - a.q_start[b]);
-    }
-    return;
+struct Row {
+  const float *p, *q;
+  double A;
+  int segment, vocab;
+
+  __device__ Row(const KvVerifyArgs& a, int64_t row0, const KvWalk& w)
+      : p(a.p + (row0 + w.node) * a.p_stride), q(DRAWN ? a.q + (row0 + w.node) * a.q_stride : p), A(w.A),
+        segment(a.plan.part / kSegments), vocab(a.vocab) {}
+  __device__ int first(int i) const {  // token of segment i
+    const int64_t t = (int64_t)i * segment;
+    return t < vocab ? (int)t : vocab;
   }
-  load_tree<DRAWN>(a, r, s, false);
-  if (tid == 0) start_walk(s);
-  const double* sums = a.ws + (int64_t)b * a.plan.rounds * a.plan.parts;
-  __syncthreads();
-  // `parts` has the sums that the walk asks for next.
-  auto fetch = [&](int k) {
-    if (k < a.plan.rounds) {
-      if (tid < a.plan.parts) parts[tid] = sums[k * a.plan.parts + tid];
-    } else {
-      for (int i = 0; i < a.plan.parts; ++i) {
-        const int t0 = i * a.plan.part, t1 = t0 + a.plan.part < a.vocab ? t0 + a.plan.part : a.vocab;
-        const double sum = sum_part<DRAWN, kPickThreads>(a, r, s, t0, t1, meet);
-        if (tid == 0) parts[i] = sum;
-      }
+  __device__ double sum(int i, int lane) const { return sum_segment<DRAWN>(p, q, A, first(i), first(i + 1), lane); }
+};
+
+// What goes on with a walk needs beside the sums: the tree where it wants one, else the rejected tokens and their p.
+template <bool DRAWN>
+__device__ inline void load_rest(const KvVerifyArgs& a, Shared& s, const KvWalk& w, const Row<DRAWN>& row, int64_t row0, int n) {
+  if (w.wants) {
+    load_tree<DRAWN>(a, Rows{row0, n, true}, s, false);
+    for (int i = threadIdx.x; i < w.count; i += kThreads) s.path[i] = a.path[row0 + i];
+  } else if (!DRAWN) {
+    for (int i = threadIdx.x; i < w.rejects; i += kThreads) {
+      const int x = a.path[row0 + w.count + i];
+      s.token[i] = x;
+      s.p[i] = row.p[x];
+    }
+  }
+}
+
+// Goes on from the sums that the walk w asked for: to what the next round is to
+// sum, or (`last`) to the end by itself, and draws.
+struct Meeting {
+  double sums[kKvParts * kSegments];  // of the segments of all parts
+  double waves[kSegments];
+  int found;
+};
+template <bool DRAWN>
+__device__ inline void finish(const KvVerifyArgs& a, int b, Shared& s, Meeting& m, KvWalk w, Row<DRAWN> row, int64_t row0, int n,
+                              float u0, bool last) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, segments = a.plan.parts * kSegments;
+  const bool walked = w.wants;
+  auto total = [&] {  // the same in all waves; exact, so in any order
+    double x = 0.0;
+    for (int i = lane; i < segments; i += 64) x += m.sums[i];
+    return wave_sum(x);
+  };
+  auto sum_all = [&] {
+    row = Row<DRAWN>(a, row0, w);
+    for (int i = wave; i < segments; i += kSegments) {
+      const double x = row.sum(i, lane);
+      if (lane == 0) m.sums[i] = x;
     }
     __syncthreads();
   };
-  for (int k = 0;; ++k) {
-    if (wave == 0) walk<DRAWN>(s, r.n, lane);
+  while (w.wants) {
+    w.Z = total();
+    w.pending = 0;
     __syncthreads();
-    fetch(k);
-    if (!s.wants) break;
-    if (wave == 0) {
-      const double z = wave_sum(lane < a.plan.parts ? parts[lane] : 0.0);
-      if (lane == 0) {
-        s.Z = z;
-        s.pending = false;
-      }
+    if (wave == 0) go_on<DRAWN>(s, w, n, lane);
+    __syncthreads();
+    w = s.walk;
+    if (!last) {  // the next round's
+      for (int i = tid; i < w.count; i += kThreads) a.path[row0 + i] = s.path[i];
+      if (tid == 0) a.states[b].walk = w;
+      return;
     }
+    sum_all();
+  }
+  if constexpr (!DRAWN) {  // rejected tokens have no weight
+    if (tid < segments)
+      for (int i = 0; i < w.rejects; ++i)
+        if (s.token[i] >= row.first(tid) && s.token[i] < row.first(tid + 1))
+          m.sums[tid] -= weight<false>(0.0, s.p[i], 0.f);
     __syncthreads();
   }
-  auto total = [&] { return wave_sum(lane < a.plan.parts ? parts[lane] : 0.0); };  // the same in all waves
   double all = total();
+  int rejects = w.rejects;
   if (!(all > 0.0)) {  // nothing left: p itself
+    w.A = 0.0;
+    rejects = 0;
     __syncthreads();
-    if (tid == 0) {
-      s.A = 0.0;
-      s.rejects = 0;
-    }
-    __syncthreads();
-    fetch(a.plan.rounds);
+    sum_all();
     all = total();
   }
-  for (int i = tid; i < r.n; i += kPickThreads) a.path[r.row0 + i] = i < s.count ? s.path[i] : -1;
-  if (tid == 0) a.count[b] = s.count;
-  if (!(all > 0.0)) {
-    if (tid == 0) {
-      a.next[b] = -1;
-      kv_report(a.err, kKvWeight, b, 0);
-    }
-    return;
-  }
-
-  // The first part whose sum with those before it passes the number.
-  const double x = (double)s.u[0] * all;
-  double below = 0.0;
-  int part = 0;
-  for (int last = 0;; ++part) {
-    if (parts[part] > 0.0) last = part;
-    if (below + parts[part] > x) break;
-    if (part == a.plan.parts - 1) {  // only by rounding, where sums are not exact
-      part = last;
-      break;
-    }
-    below += parts[part];
-  }
-  const int t0 = part * a.plan.part, t1 = t0 + a.plan.part < a.vocab ? t0 + a.plan.part : a.vocab;
-  const float* p = a.p + (r.row0 + s.node) * a.p_stride;
-  const float* q = DRAWN ? a.q + (r.row0 + s.node) * a.q_stride : p;
-  const double A = s.A;
-  int best = -1;  // the last token with a weight so far, should none pass
-  for (int tile = t0; tile < t1; tile += 4 * kPickThreads) {
-    const int t = tile + 4 * tid;
-    double w[4], mine = 0.0;
+  int token = -1;
+  if (all > 0.0) {
+    // The first segment whose sum with those before it passes the number, then the first token.
+    const double x = (double)number(u0) * all;
+    auto search = [&](const double (&v)[8], int per, double below, double& before) {
+      // v: this thread's numbers. The index (tid per + i) of the first whose running sum passes x, or -1, and the sum
+      // before it.
+      double own = 0.0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = t + i < t1 ? weight<DRAWN>(A, p[t + i], q[t + i]) : 0.0;
-      if constexpr (!DRAWN)
-        for (int j = 0; j < s.rejects; ++j)
-          if (s.rejected[j] == t + i) w[i] = 0.0;
-      mine += w[i];
-    }
-    double upto = mine;  // over the lanes before and this one
+      for (int i = 0; i < 8; ++i) own += v[i];
+      double upto = own;  // over the lanes before and this one
 #pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const double y = __shfl_up(upto, m);
-      if (lane >= m) upto += y;
-    }
-    __syncthreads();
-    if (lane == 63) meet[wave] = upto;
-    if (tid == 0) found = 0x7fffffff;
-    __syncthreads();
-    double before = below, whole = 0.0;
+      for (int m = 1; m < 64; m <<= 1) {
+        const double y = __shfl_up(upto, m);
+        if (lane >= m) upto += y;
+      }
+      __syncthreads();
+      if (lane == 63) m.waves[wave] = upto;
+      if (tid == 0) m.found = 0x7fffffff;
+      __syncthreads();
+      double run = below + (upto - own);
 #pragma unroll
-    for (int i = 0; i < kPickThreads / 64; ++i) {
-      if (i < wave) before += meet[i];
-      whole += meet[i];
-    }
-    double sum = before + (upto - mine);
-    int hit = 0x7fffffff, any = -1;
+      for (int i = 0; i < kSegments; ++i)
+        if (i < wave) run += m.waves[i];
+      int hit = 0x7fffffff;
+      double at = 0.0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sum += w[i];
-      if (w[i] > 0.0) {
-        any = t + i;
-        if (sum > x && hit == 0x7fffffff) hit = t + i;
+      for (int i = 0; i < 8; ++i) {
+        if (hit == 0x7fffffff && v[i] > 0.0 && run + v[i] > x) {
+          hit = tid * per + i;
+          at = run;
+        }
+        run += v[i];
+      }
+      if (hit != 0x7fffffff) atomicMin(&m.found, hit);
+      __syncthreads();
+      const int first = m.found;
+      if (hit == first && hit != 0x7fffffff) m.waves[0] = at;
+      __syncthreads();
+      before = m.waves[0];
+      __syncthreads();
+      return first == 0x7fffffff ? -1 : first;
+    };
+    double v[8] = {};
+    if (tid < segments) v[0] = m.sums[tid];
+    double below = 0.0;
+    int at = search(v, 1, 0.0, below);
+    if (at < 0) {  // only by rounding, where sums are not exact: the last one with a weight
+      below = 0.0;
+      for (int i = 0; i < segments; ++i)
+        if (m.sums[i] > 0.0) at = i;
+      for (int i = 0; i < at; ++i) below += m.sums[i];
+    }
+    const int t1 = row.first(at + 1);
+    int end = -1;
+    for (int t0 = row.first(at); t0 < t1 && token < 0; t0 += 8 * kThreads) {
+      const int t = t0 + 8 * tid;
+      float x4[8] = {}, y4[8] = {};
+      if (t + 8 <= t1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4v xx = reinterpret_cast<const Quad*>(row.p + t + 4 * i)->x;
+          const float4v yy = DRAWN ? reinterpret_cast<const Quad*>(row.q + t + 4 * i)->x : xx;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x4[4 * i + k] = xx[k], y4[4 * i + k] = yy[k];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (t + i < t1) x4[i] = row.p[t + i], y4[i] = row.q[t + i];
+      }
+      double whole = 0.0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = weight<DRAWN>(w.A, x4[i], y4[i]);
+        if constexpr (!DRAWN)
+          for (int k = 0; k < rejects; ++k)
+            if (s.token[k] == t + i) v[i] = 0.0;
+        if (v[i] > 0.0) end = t + i > end ? t + i : end;
+        whole += v[i];
+      }
+      double before;
+      const int hit = search(v, 8, below, before);
+      if (hit >= 0) {
+        token = t0 + hit;
+      } else {
+        whole = wave_sum(whole);
+        if (lane == 0) m.waves[wave] = whole;
+        __syncthreads();
+        for (int i = 0; i < kSegments; ++i) below += m.waves[i];
+        __syncthreads();
       }
     }
-    if (hit != 0x7fffffff) atomicMin(&found, hit);
-    __syncthreads();
-    if (found != 0x7fffffff) {
-      best = found;
-      break;
+    if (token < 0) {  // see above
+      if (tid == 0) m.found = -1;
+      __syncthreads();
+      atomicMax(&m.found, end);
+      __syncthreads();
+      token = m.found;
     }
-    best = any > best ? any : best;
-    below += whole;
-    __syncthreads();
+  } else if (tid == 0) {
+    kv_report(a.err, kKvWeight, b, 0);
   }
-  if (found == 0x7fffffff) {  // see above
-    __syncthreads();
-    if (tid == 0) found = -1;
-    __syncthreads();
-    atomicMax(&found, best);
-    __syncthreads();
-    best = found;
+  __syncthreads();
+  for (int i = tid; i < n; i += kThreads)
+    if (i >= w.count) a.path[row0 + i] = -1;
+    else if (walked) a.path[row0 + i] = s.path[i];
+  if (tid == 0) {
+    a.count[b] = w.count;
+    a.next[b] = token;
+    a.states[b].walk.done = 1;
   }
-  if (tid == 0) a.next[b] = best;
+}
+
+// A round: sums a part of the row; the last of a sequence goes on.
+template <bool DRAWN>
+__global__ __launch_bounds__(kThreads) void kv_verify_round_kernel(KvVerifyArgs a, int round) {
+  __shared__ Shared s;
+  __shared__ Meeting m;
+  const int b = blockIdx.x / a.plan.parts, part = blockIdx.x - b * a.plan.parts;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const KvWalk w = a.states[b].walk;
+  if (w.done) return;
+  const int64_t row0 = a.q_start[b];
+  const int n = a.q_start[b + 1] - (int)row0;
+  const Row<DRAWN> row(a, row0, w);
+  const float u0 = a.u[row0];
+  load_rest<DRAWN>(a, s, w, row, row0, n);  // on its way during the sum
+  const double mine = row.sum(part * kSegments + wave, lane);
+  if (lane == 0) m.waves[wave] = mine;
+  __syncthreads();
+  const int segments = a.plan.parts * kSegments;
+  double* sums = a.sums + (int64_t)b * segments;
+  if (wave == 0) {
+    // The sums go past the caches of this XCD, and are there before they are
+    // counted: one wave stores and waits, which a release (the write-back of
+    // all of the cache, 20 us a call of 1024 workgroups) would do too.
+    if (lane < kSegments) store_sum(sums + part * kSegments + lane, m.waves[lane]);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    asm volatile("" ::: "memory");
+    if (lane == 0)
+      m.found = (int)__hip_atomic_fetch_add(&a.states[b].arrived[round], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (m.found != a.plan.parts - 1) return;
+  if (tid < segments) m.sums[tid] = load_sum(sums + tid);
+  __syncthreads();
+  finish<DRAWN>(a, b, s, m, w, row, row0, n, u0, round + 1 == a.plan.rounds);
+}
+
+// The rounds' beginning.
+template <bool DRAWN>
+__global__ __launch_bounds__(kThreads) void kv_verify_begin_kernel(KvVerifyArgs a) {
+  __shared__ Shared s;
+  int64_t row0;
+  if (threadIdx.x < kKvRounds) a.states[blockIdx.x].arrived[threadIdx.x] = 0;
+  begin<DRAWN>(a, blockIdx.x, s, true, row0);
+}
+
+// Where the walk is expected to need no sum but the last: every part walks for
+// itself and sums, and a second kernel draws. 64 chains of 6, 131072 tokens: XX us
+// (with the kernels of the rounds 26).
+template <bool DRAWN>
+__global__ __launch_bounds__(kThreads) void kv_verify_sum_kernel(KvVerifyArgs a) {
+  __shared__ Shared s;
+  const int b = blockIdx.x / a.plan.parts, part = blockIdx.x - b * a.plan.parts;
+  const int lane = threadIdx.x & 63, i = part * kSegments + (threadIdx.x >> 6);
+  int64_t row0;
+  if (!begin<DRAWN>(a, b, s, part == 0, row0)) return;
+  const double mine = Row<DRAWN>(a, row0, s.walk).sum(i, lane);
+  if (lane == 0) a.sums[(int64_t)b * a.plan.parts * kSegments + i] = mine;
+}
+template <bool DRAWN>
+__global__ __launch_bounds__(kThreads) void kv_verify_draw_kernel(KvVerifyArgs a) {
+  __shared__ Shared s;
+  __shared__ Meeting m;
+  const int b = blockIdx.x, tid = threadIdx.x, segments = a.plan.parts * kSegments;
+  const KvWalk w = a.states[b].walk;
+  const int64_t row0 = a.q_start[b];
+  const int n = a.q_start[b + 1] - (int)row0;
+  if (tid < segments) m.sums[tid] = a.sums[(int64_t)b * segments + tid];
+  if (w.done) return;
+  const Row<DRAWN> row(a, row0, w);
+  const float u0 = a.u[row0];
+  load_rest<DRAWN>(a, s, w, row, row0, n);
+  __syncthreads();
+  finish<DRAWN>(a, b, s, m, w, row, row0, n, u0, true);
 }
 
 template <class A>
 hipError_t launch_round(void (*kernel)(A, int), dim3 grid, hipStream_t s, A a, int round) {
   void* args[] = {&a, &round};
-  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kRoundThreads), args, 0, s);
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kThreads), args, 0, s);
 }
 
 template <bool DRAWN>
 hipError_t launch(const KvVerifyArgs& a, hipStream_t s) {
-  hipError_t e = hipSuccess;
+  const dim3 sequences((unsigned)a.batch), parts((unsigned)(a.batch * a.plan.parts));
+  if (a.plan.rounds == 1) {
+    const hipError_t e = kv_launch(kv_verify_sum_kernel<DRAWN>, parts, kThreads, s, a);
+    return e == hipSuccess ? kv_launch(kv_verify_draw_kernel<DRAWN>, sequences, kThreads, s, a) : e;
+  }
+  hipError_t e = kv_launch(kv_verify_begin_kernel<DRAWN>, sequences, kThreads, s, a);
   for (int k = 0; k < a.plan.rounds && e == hipSuccess; ++k)
-    e = launch_round(kv_verify_round_kernel<DRAWN>, dim3((unsigned)(a.batch * a.plan.parts)), s, a, k);
-  if (e == hipSuccess) e = kv_launch(kv_verify_pick_kernel<DRAWN>, dim3((unsigned)a.batch), kPickThreads, s, a);
+    e = launch_round(kv_verify_round_kernel<DRAWN>, parts, s, a, k);
   return e;
 }
 

@@ -260,7 +260,7 @@ int kvc_verify(kvc_ctx* ctx, const kvc_verify_args* p, void* workspace, int64_t 
   if (p && p->batch > 0 && p->batch <= kKvMaxSequences && p->vocab >= 1 && p->vocab <= (int64_t{1} << 28))  // refused below otherwise
     plan = kv_verify_plan(p->batch, p->vocab, p->q != nullptr, p->max_children, ctx->num_cus);
   char why[kKvWhy];
-  const int64_t need = p ? (int64_t)p->batch * plan.parts * plan.rounds * 8 : 0;
+  const int64_t need = p ? kv_verify_bytes(plan, p->batch) : 0;
   const int rc = kv_check_verify(p, need, workspace, workspace_bytes, why);
   if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);
 
@@ -281,7 +281,9 @@ int kvc_verify(kvc_ctx* ctx, const kvc_verify_args* p, void* workspace, int64_t 
   a.count = p->count;
   a.next = p->next;
   a.plan = plan;
-  a.ws = static_cast<double*>(workspace);
+  // The states first, on lines of their own, as far as the workspace is aligned to lines.
+  a.states = static_cast<KvVerifyState*>(workspace);
+  a.sums = reinterpret_cast<double*>(a.states + p->batch);
   a.err = ctx->err_dev;
   OnDevice on(ctx->device);
   if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");
