@@ -92,8 +92,9 @@ struct KvWalk {
 // A line of its own: workgroups of all XCDs count in it.
 struct KvVerifyState {
   KvWalk walk;
-  uint32_t arrived[kKvRounds];  // parts that are summed, of each round
-  uint8_t rest[kKvStateBytes - sizeof(KvWalk) - 4 * kKvRounds];
+  uint32_t arrived;  // parts that are summed, over all rounds
+  uint32_t turn;     // rounds after which the walk has gone on
+  uint8_t rest[kKvStateBytes - sizeof(KvWalk) - 8];
 };
 static_assert(sizeof(KvVerifyState) == kKvStateBytes, "the workspace's bound counts them");
 
@@ -111,6 +112,7 @@ struct KvVerifyArgs {
   KvVerifyPlan plan;
   KvVerifyState* states;  // batch
   double* sums;           // batch x segments of all parts
+  int64_t patience;       // ticks of the wall clock that a workgroup of the rounds waits for the others
   uint64_t* err;  // kv_report.h
 };
 

@@ -368,14 +368,12 @@ inline int kv_commit_piece(const KvLayout& L, int64_t batch) {
 }
 
 // How a verification's rows of probabilities are summed: in `parts` parts of
-// `part` tokens each, one workgroup a part, in `rounds` launches. A round sums
-// what the walk asks for next; what is left after the last round, its last
-// workgroup sums alone.
+// `part` tokens each, one workgroup a part; with rounds, again and again as the
+// walk asks for sums, else once, for the last draw.
 struct KvVerifyPlan {
   int32_t parts, part, rounds;
 };
 constexpr int kKvParts = 64;   // at most
-constexpr int kKvRounds = 8;   // for siblings drawn from q
 constexpr int kKvStateBytes = 128;  // of a sequence: how far it has come, parts that are summed
 inline int64_t kv_verify_parts(int64_t batch, int64_t vocab, int num_cus) {
   // Four workgroups a CU, of 2048 tokens at the least and 16384 at the most (the
@@ -394,7 +392,7 @@ inline KvVerifyPlan kv_verify_plan(int64_t batch, int64_t vocab, bool drawn, int
   const int64_t part = ((vocab + parts - 1) / parts + 1023) / 1024 * 1024;
   p.part = (int32_t)part;
   p.parts = (int32_t)((vocab + part - 1) / part);
-  p.rounds = drawn && max_children > 1 ? kKvRounds : 1;
+  p.rounds = drawn && max_children > 1;
   return p;
 }
 inline int64_t kv_verify_bytes(const KvVerifyPlan& p, int64_t batch) { return batch * ((int64_t)p.parts * 32 + kKvStateBytes); }

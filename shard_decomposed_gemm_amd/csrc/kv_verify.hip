@@ -14,11 +14,13 @@
 // neighbours lie that far apart), so that sums in binary64 are exact up to 8 and
 // do not depend on how the vocabulary is split.
 //
-// One workgroup a sequence begins the walk (parents, tokens and numbers, then p
-// and q of every draft, then some 0.2 us a level). A round then sums the row that
-// the walk has come to, by `parts` workgroups a sequence; the one that is done
-// last goes on with it: to the next node that wants a sum, which is the next
-// round's, or to the end, where it draws. The last round goes on alone.
+// Where no sum but the last is expected, the workgroups of a row's parts each walk
+// by themselves and sum, and a second kernel draws. Else one workgroup a sequence
+// begins the walk, and the parts' workgroups then take turns: they sum the row
+// that the walk has come to, and the one that is done last goes on with the walk
+// and tells the others, which wait for that. A wait is bounded: what is not
+// finished when one gives up, the last kernel finishes, a workgroup a sequence.
+// As the sums are exact, who makes them does not matter.
 #include "kv_internal.h"
 
 namespace agemm {
@@ -38,12 +40,18 @@ __device__ inline float unit(float x) { return fminf(fmaxf(x, 0.f), 1.f); }  // 
 constexpr int kThreads = 256;
 constexpr int kSegments = kThreads / 64;  // of a part, a wave each
 
+// A walk as the words that go between workgroups.
+constexpr int kWords = sizeof(KvWalk) / 8;
+struct KvWalkWords {
+  uint64_t x[kWords];
+};
+
 struct Shared {
   int32_t token[kKvNodes];  // -1: outside the vocabulary
   float p[kKvNodes], q[kKvNodes], u[kKvNodes];
   int16_t parent[kKvNodes];
   int32_t path[kKvNodes];  // accepted nodes, then (without q) the tokens rejected at the last of them
-  KvWalk walk;
+  KvWalkWords walk;
 };
 
 template <bool DRAWN>
@@ -143,13 +151,31 @@ __device__ inline void go_on(Shared& s, KvWalk w, int n, int lane) {
       w.Z = 1.0;
     }
   }
-  if (lane == 0) s.walk = w;
+  if (lane == 0) s.walk = __builtin_bit_cast(KvWalkWords, w);
 }
 
-__device__ inline double wave_sum(double x) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
+// x of another lane as the DPP control says, 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ inline double moved(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sum over this lane and the earlier ones.
+__device__ inline double sum_up_to(double x) {
+  x += moved<0x111, 0xf>(x);  // row_shr:1
+  x += moved<0x112, 0xf>(x);  // row_shr:2
+  x += moved<0x114, 0xf>(x);  // row_shr:4
+  x += moved<0x118, 0xf>(x);  // row_shr:8
+  x += moved<0x142, 0xa>(x);  // row_bcast:15
+  x += moved<0x143, 0xc>(x);  // row_bcast:31
   return x;
+}
+__device__ inline double wave_sum(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, sum_up_to(x));
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
 // Begins the walk of a sequence; `keeps`: and leaves how far it has come. False if there is nothing to walk.
@@ -173,7 +199,7 @@ __device__ inline bool begin(const KvVerifyArgs& a, int b, Shared& s, bool keeps
   if (tid < 64) go_on<DRAWN>(s, KvWalk{0.0, 0.0, 1.0, 0, 0, 1, 0, 0, 0, 0, 0}, r.n, tid);
   __syncthreads();
   if (keeps) {
-    const KvWalk w = s.walk;
+    const KvWalk w = __builtin_bit_cast(KvWalk, s.walk);
     for (int i = tid; i < r.n; i += kThreads) a.path[r.row0 + i] = i < w.count + w.rejects ? s.path[i] : -1;
     if (tid == 0) a.states[b].walk = w;
   }
@@ -219,60 +245,33 @@ struct Row {
   __device__ double sum(int i, int lane) const { return sum_segment<DRAWN>(p, q, A, first(i), first(i + 1), lane); }
 };
 
-// What goes on with a walk needs beside the sums: the tree where it wants one, else the rejected tokens and their p.
-template <bool DRAWN>
-__device__ inline void load_rest(const KvVerifyArgs& a, Shared& s, const KvWalk& w, const Row<DRAWN>& row, int64_t row0, int n) {
-  if (w.wants) {
-    load_tree<DRAWN>(a, Rows{row0, n, true}, s, false);
-    for (int i = threadIdx.x; i < w.count; i += kThreads) s.path[i] = a.path[row0 + i];
-  } else if (!DRAWN) {
-    for (int i = threadIdx.x; i < w.rejects; i += kThreads) {
-      const int x = a.path[row0 + w.count + i];
-      s.token[i] = x;
-      s.p[i] = row.p[x];
-    }
-  }
-}
-
-// Goes on from the sums that the walk w asked for: to what the next round is to
-// sum, or (`last`) to the end by itself, and draws.
 struct Meeting {
   double sums[kKvParts * kSegments];  // of the segments of all parts
   double waves[kSegments];
-  int found;
+  int found, told;
 };
+__device__ inline double total_of(const Meeting& m, int segments) {  // the same in all waves
+  double x = 0.0;
+  for (int i = threadIdx.x & 63; i < segments; i += 64) x += m.sums[i];
+  return wave_sum(x);
+}
 template <bool DRAWN>
-__device__ inline void finish(const KvVerifyArgs& a, int b, Shared& s, Meeting& m, KvWalk w, Row<DRAWN> row, int64_t row0, int n,
-                              float u0, bool last) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, segments = a.plan.parts * kSegments;
-  const bool walked = w.wants;
-  auto total = [&] {  // the same in all waves; exact, so in any order
-    double x = 0.0;
-    for (int i = lane; i < segments; i += 64) x += m.sums[i];
-    return wave_sum(x);
-  };
-  auto sum_all = [&] {
-    row = Row<DRAWN>(a, row0, w);
-    for (int i = wave; i < segments; i += kSegments) {
-      const double x = row.sum(i, lane);
-      if (lane == 0) m.sums[i] = x;
-    }
-    __syncthreads();
-  };
-  while (w.wants) {
-    w.Z = total();
-    w.pending = 0;
-    __syncthreads();
-    if (wave == 0) go_on<DRAWN>(s, w, n, lane);
-    __syncthreads();
-    w = s.walk;
-    if (!last) {  // the next round's
-      for (int i = tid; i < w.count; i += kThreads) a.path[row0 + i] = s.path[i];
-      if (tid == 0) a.states[b].walk = w;
-      return;
-    }
-    sum_all();
+__device__ inline void sum_all(Meeting& m, const Row<DRAWN>& row, int segments) {
+  const int lane = threadIdx.x & 63;
+  for (int i = threadIdx.x >> 6; i < segments; i += kSegments) {
+    const double x = row.sum(i, lane);
+    if (lane == 0) m.sums[i] = x;
   }
+  __syncthreads();
+}
+
+// Draws from the row that the walk w has ended at, whose sums are there, and
+// writes the sequence's results. `tree`: s has the tree, which the path follows
+// from; else the path is written, and s has the rejected tokens and their p.
+template <bool DRAWN>
+__device__ inline void draw(const KvVerifyArgs& a, int b, Shared& s, Meeting& m, KvWalk w, Row<DRAWN> row, int64_t row0, int n,
+                            float u0, bool tree) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, segments = a.plan.parts * kSegments;
   if constexpr (!DRAWN) {  // rejected tokens have no weight
     if (tid < segments)
       for (int i = 0; i < w.rejects; ++i)
@@ -280,14 +279,15 @@ __device__ inline void finish(const KvVerifyArgs& a, int b, Shared& s, Meeting& 
           m.sums[tid] -= weight<false>(0.0, s.p[i], 0.f);
     __syncthreads();
   }
-  double all = total();
+  double all = total_of(m, segments);
   int rejects = w.rejects;
   if (!(all > 0.0)) {  // nothing left: p itself
     w.A = 0.0;
     rejects = 0;
     __syncthreads();
-    sum_all();
-    all = total();
+    row = Row<DRAWN>(a, row0, w);
+    sum_all(m, row, segments);
+    all = total_of(m, segments);
   }
   int token = -1;
   if (all > 0.0) {
@@ -299,12 +299,7 @@ __device__ inline void finish(const KvVerifyArgs& a, int b, Shared& s, Meeting& 
       double own = 0.0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) own += v[i];
-      double upto = own;  // over the lanes before and this one
-#pragma unroll
-      for (int m = 1; m < 64; m <<= 1) {
-        const double y = __shfl_up(upto, m);
-        if (lane >= m) upto += y;
-      }
+      const double upto = sum_up_to(own);
       __syncthreads();
       if (lane == 63) m.waves[wave] = upto;
       if (tid == 0) m.found = 0x7fffffff;
@@ -393,9 +388,12 @@ __device__ inline void finish(const KvVerifyArgs& a, int b, Shared& s, Meeting& 
     kv_report(a.err, kKvWeight, b, 0);
   }
   __syncthreads();
+  if (tree && tid == 0)
+    for (int i = w.count - 1, node = w.node; i >= 0; node = s.parent[node], --i) s.path[i] = node;
+  __syncthreads();
   for (int i = tid; i < n; i += kThreads)
     if (i >= w.count) a.path[row0 + i] = -1;
-    else if (walked) a.path[row0 + i] = s.path[i];
+    else if (tree) a.path[row0 + i] = s.path[i];
   if (tid == 0) {
     a.count[b] = w.count;
     a.next[b] = token;
@@ -403,50 +401,85 @@ __device__ inline void finish(const KvVerifyArgs& a, int b, Shared& s, Meeting& 
   }
 }
 
-// A round: sums a part of the row; the last of a sequence goes on.
-template <bool DRAWN>
-__global__ __launch_bounds__(kThreads) void kv_verify_round_kernel(KvVerifyArgs a, int round) {
-  __shared__ Shared s;
-  __shared__ Meeting m;
-  const int b = blockIdx.x / a.plan.parts, part = blockIdx.x - b * a.plan.parts;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const KvWalk w = a.states[b].walk;
-  if (w.done) return;
-  const int64_t row0 = a.q_start[b];
-  const int n = a.q_start[b + 1] - (int)row0;
-  const Row<DRAWN> row(a, row0, w);
-  const float u0 = a.u[row0];
-  load_rest<DRAWN>(a, s, w, row, row0, n);  // on its way during the sum
-  const double mine = row.sum(part * kSegments + wave, lane);
-  if (lane == 0) m.waves[wave] = mine;
-  __syncthreads();
-  const int segments = a.plan.parts * kSegments;
-  double* sums = a.sums + (int64_t)b * segments;
-  if (wave == 0) {
-    // The sums go past the caches of this XCD, and are there before they are
-    // counted: one wave stores and waits, which a release (the write-back of
-    // all of the cache, 20 us a call of 1024 workgroups) would do too.
-    if (lane < kSegments) store_sum(sums + part * kSegments + lane, m.waves[lane]);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0);
-    asm volatile("" ::: "memory");
-    if (lane == 0)
-      m.found = (int)__hip_atomic_fetch_add(&a.states[b].arrived[round], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  if (m.found != a.plan.parts - 1) return;
-  if (tid < segments) m.sums[tid] = load_sum(sums + tid);
-  __syncthreads();
-  finish<DRAWN>(a, b, s, m, w, row, row0, n, u0, round + 1 == a.plan.rounds);
-}
-
 // The rounds' beginning.
 template <bool DRAWN>
 __global__ __launch_bounds__(kThreads) void kv_verify_begin_kernel(KvVerifyArgs a) {
   __shared__ Shared s;
   int64_t row0;
-  if (threadIdx.x < kKvRounds) a.states[blockIdx.x].arrived[threadIdx.x] = 0;
+  if (threadIdx.x == 0) a.states[blockIdx.x].arrived = a.states[blockIdx.x].turn = 0;
   begin<DRAWN>(a, blockIdx.x, s, true, row0);
+}
+
+// The rounds. What workgroups tell each other goes past the caches of their XCDs
+// (relaxed accesses at the device's scope), and is there before the counter or
+// turn that announces it: one wave stores and waits, which a release (the
+// write-back of all of the cache, 20 us a call of 1024 workgroups) would do too.
+__device__ inline void stores_are_there() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0);
+  asm volatile("" ::: "memory");
+}
+template <bool DRAWN>
+__global__ __launch_bounds__(kThreads) void kv_verify_rounds_kernel(KvVerifyArgs a) {
+  __shared__ Shared s;
+  __shared__ Meeting m;
+  const int b = blockIdx.x / a.plan.parts, part = blockIdx.x - b * a.plan.parts, segments = a.plan.parts * kSegments;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  KvVerifyState& state = a.states[b];
+  KvWalk w = state.walk;
+  if (w.done) return;
+  const int64_t row0 = a.q_start[b];
+  const int n = a.q_start[b + 1] - (int)row0;
+  const float u0 = a.u[row0];
+  load_tree<DRAWN>(a, Rows{row0, n, true}, s, false);
+  double* sums = a.sums + (int64_t)b * segments;
+  for (uint32_t turn = 1;; ++turn) {
+    const Row<DRAWN> row(a, row0, w);
+    const double mine = row.sum(part * kSegments + wave, lane);
+    if (lane == 0) m.waves[wave] = mine;
+    __syncthreads();
+    if (wave == 0) {
+      if (lane < kSegments) store_sum(sums + part * kSegments + lane, m.waves[lane]);
+      stores_are_there();
+      if (lane == 0) m.found = __hip_atomic_fetch_add(&state.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == a.plan.parts * turn;
+    }
+    __syncthreads();
+    if (m.found) {  // the last one
+      if (tid < segments) m.sums[tid] = load_sum(sums + tid);
+      __syncthreads();
+      if (!w.wants) {
+        draw<DRAWN>(a, b, s, m, w, row, row0, n, u0, true);
+        return;
+      }
+      w.Z = total_of(m, segments);
+      w.pending = 0;
+      if (wave == 0) {
+        go_on<DRAWN>(s, w, n, lane);
+        if (lane < kWords)
+          __hip_atomic_store(reinterpret_cast<uint64_t*>(&state.walk) + lane, s.walk.x[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        stores_are_there();
+        if (lane == 0) __hip_atomic_store(&state.turn, turn, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    } else {
+      if (!w.wants) return;  // the last one draws
+      if (wave == 0) {
+        const uint64_t t0 = wall_clock64();
+        bool told;
+        while (!(told = __hip_atomic_load(&state.turn, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= turn) &&
+               wall_clock64() - t0 < (uint64_t)a.patience)
+          __builtin_amdgcn_s_sleep(1);
+        asm volatile("" ::: "memory");
+        if (told && lane < kWords)
+          s.walk.x[lane] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(&state.walk) + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lane == 0) m.told = told;
+      }
+      __syncthreads();
+      if (!m.told) return;  // the last kernel finishes it
+    }
+    __syncthreads();
+    w = __builtin_bit_cast(KvWalk, s.walk);
+    __syncthreads();
+  }
 }
 
 // Where the walk is expected to need no sum but the last: every part walks for
@@ -459,43 +492,59 @@ __global__ __launch_bounds__(kThreads) void kv_verify_sum_kernel(KvVerifyArgs a)
   const int lane = threadIdx.x & 63, i = part * kSegments + (threadIdx.x >> 6);
   int64_t row0;
   if (!begin<DRAWN>(a, b, s, part == 0, row0)) return;
-  const double mine = Row<DRAWN>(a, row0, s.walk).sum(i, lane);
+  const double mine = Row<DRAWN>(a, row0, __builtin_bit_cast(KvWalk, s.walk)).sum(i, lane);
   if (lane == 0) a.sums[(int64_t)b * a.plan.parts * kSegments + i] = mine;
 }
-template <bool DRAWN>
+// SUMMED: the sums that the walk wants are there; else only what the rounds left is to do.
+template <bool DRAWN, bool SUMMED>
 __global__ __launch_bounds__(kThreads) void kv_verify_draw_kernel(KvVerifyArgs a) {
   __shared__ Shared s;
   __shared__ Meeting m;
   const int b = blockIdx.x, tid = threadIdx.x, segments = a.plan.parts * kSegments;
-  const KvWalk w = a.states[b].walk;
+  KvWalk w = a.states[b].walk;
   const int64_t row0 = a.q_start[b];
   const int n = a.q_start[b + 1] - (int)row0;
-  if (tid < segments) m.sums[tid] = a.sums[(int64_t)b * segments + tid];
+  if (SUMMED && tid < segments) m.sums[tid] = a.sums[(int64_t)b * segments + tid];
   if (w.done) return;
-  const Row<DRAWN> row(a, row0, w);
+  Row<DRAWN> row(a, row0, w);
   const float u0 = a.u[row0];
-  load_rest<DRAWN>(a, s, w, row, row0, n);
+  const bool tree = !SUMMED || w.wants;
+  if (tree) {
+    load_tree<DRAWN>(a, Rows{row0, n, true}, s, false);
+  } else if (!DRAWN) {
+    for (int i = tid; i < w.rejects; i += kThreads) {
+      const int x = a.path[row0 + w.count + i];
+      s.token[i] = x;
+      s.p[i] = row.p[x];
+    }
+  }
   __syncthreads();
-  finish<DRAWN>(a, b, s, m, w, row, row0, n, u0, true);
-}
-
-template <class A>
-hipError_t launch_round(void (*kernel)(A, int), dim3 grid, hipStream_t s, A a, int round) {
-  void* args[] = {&a, &round};
-  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kThreads), args, 0, s);
+  if (!SUMMED) sum_all(m, row, segments);
+  while (w.wants) {
+    w.Z = total_of(m, segments);
+    w.pending = 0;
+    __syncthreads();
+    if (tid < 64) go_on<DRAWN>(s, w, n, tid);
+    __syncthreads();
+    w = __builtin_bit_cast(KvWalk, s.walk);
+    row = Row<DRAWN>(a, row0, w);
+    sum_all(m, row, segments);
+  }
+  draw<DRAWN>(a, b, s, m, w, row, row0, n, u0, tree);
 }
 
 template <bool DRAWN>
 hipError_t launch(const KvVerifyArgs& a, hipStream_t s) {
   const dim3 sequences((unsigned)a.batch), parts((unsigned)(a.batch * a.plan.parts));
-  if (a.plan.rounds == 1) {
-    const hipError_t e = kv_launch(kv_verify_sum_kernel<DRAWN>, parts, kThreads, s, a);
-    return e == hipSuccess ? kv_launch(kv_verify_draw_kernel<DRAWN>, sequences, kThreads, s, a) : e;
-  }
-  hipError_t e = kv_launch(kv_verify_begin_kernel<DRAWN>, sequences, kThreads, s, a);
-  for (int k = 0; k < a.plan.rounds && e == hipSuccess; ++k)
-    e = launch_round(kv_verify_round_kernel<DRAWN>, parts, s, a, k);
-  return e;
+  hipError_t e;
+  if constexpr (DRAWN)
+    if (a.plan.rounds) {
+      e = kv_launch(kv_verify_begin_kernel<true>, sequences, kThreads, s, a);
+      if (e == hipSuccess) e = kv_launch(kv_verify_rounds_kernel<true>, parts, kThreads, s, a);
+      return e == hipSuccess ? kv_launch(kv_verify_draw_kernel<true, false>, sequences, kThreads, s, a) : e;
+    }
+  e = kv_launch(kv_verify_sum_kernel<DRAWN>, parts, kThreads, s, a);
+  return e == hipSuccess ? kv_launch(kv_verify_draw_kernel<DRAWN, true>, sequences, kThreads, s, a) : e;
 }
 
 }  // namespace

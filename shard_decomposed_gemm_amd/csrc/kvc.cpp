@@ -9,6 +9,7 @@
 
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <new>
 #include <string>
 
@@ -22,6 +23,7 @@ struct kvc_ctx {
   KvLayout L{};
   int device = 0;
   int num_cus = 0;
+  int64_t patience = 0;  // ticks that a workgroup of a verification waits for the others
   uint64_t* err_host = nullptr;  // the last report (kv_report.h), 0: none
   uint64_t* err_dev = nullptr;
   std::string last_error;
@@ -111,6 +113,12 @@ int kvc_create(kvc_ctx** out, int Hq, int Hkv, int D, int page_tokens, int64_t n
   c->L = kv_layout(Hq, Hkv, D, page_tokens, num_pages);
   hipError_t e = hipGetDevice(&c->device);
   if (e == hipSuccess) e = hipDeviceGetAttribute(&c->num_cus, hipDeviceAttributeMultiprocessorCount, c->device);
+  int khz = 0;
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&khz, hipDeviceAttributeWallClockRate, c->device);
+  // Some ten times what a round takes. AGEMM_VERIFY_WAIT_US: a testing hook (0: no wait, the last kernel does it all).
+  const char* wait = std::getenv("AGEMM_VERIFY_WAIT_US");
+  const long us = wait ? std::strtol(wait, nullptr, 10) : 200;
+  c->patience = (int64_t)(us < 0 ? 0 : us < 100000 ? us : 100000) * khz / 1000;
   void* hp = nullptr;
   if (e == hipSuccess) e = hipHostMalloc(&hp, sizeof(uint64_t), hipHostMallocMapped | hipHostMallocCoherent);
   if (e == hipSuccess) {
@@ -284,6 +292,7 @@ int kvc_verify(kvc_ctx* ctx, const kvc_verify_args* p, void* workspace, int64_t 
   // The states first, on lines of their own, as far as the workspace is aligned to lines.
   a.states = static_cast<KvVerifyState*>(workspace);
   a.sums = reinterpret_cast<double*>(a.states + p->batch);
+  a.patience = ctx->patience;
   a.err = ctx->err_dev;
   OnDevice on(ctx->device);
   if (on.e != hipSuccess) return hip_fail(ctx, on.e, "hipSetDevice");

@@ -456,7 +456,7 @@ VERIFIES = [
     ([5, 0, 3, 9, 1], 4099, True, "chain", 1),
     ([5, 0, 3, 9, 1], 4099, False, "chain", 1),
     ([12, 20, 7], 2000, True, "mixed", 20),
-    ([12, 20, 7], 2000, True, "mixed", 1),   # more children than said: the last kernel sums alone
+    ([12, 20, 7], 2000, True, "mixed", 1),   # more children than said: the last kernel sums them
     ([12, 20, 7], 2001, False, "mixed", 20),
     ([64, 63], 777, True, "star", 64),
     ([65, 130], 512, True, "mixed", 200),
@@ -495,6 +495,18 @@ def test_verify_near_and_far_drafts(gap):
         accepted = _check_verify(got, c)
         if gap == 0.0 and kind == "chain":
             assert accepted == 8 * 8
+
+
+@pytest.mark.parametrize("wait", ["0", "1"])
+def test_verify_without_waiting_for_other_workgroups(wait, monkeypatch):
+    """Workgroups that give up waiting leave the rest to the last kernel: the same results."""
+    monkeypatch.setenv("AGEMM_VERIFY_WAIT_US", wait)
+    kv = _cache(1, 1, 64)
+    for kind, sizes, vocab in (("star", [20] * 8, 500), ("mixed", [30] * 40, 9000), ("mixed", [12], 70001)):
+        c = _verify_problem(7, sizes, vocab, True, kind, gap=2.0, sharp=1.5)
+        got = _run_verify(kv, c, max_children=9)
+        kv.check()
+        _check_verify(got, c)
 
 
 def test_verify_borders_exactly():

@@ -206,7 +206,7 @@ def test_verify_plans_cover_the_vocabulary_within_their_bound(host, cus):
                 host.kvt_verify_plan(batch, vocab, drawn, children, cus, out)
                 parts, part, rounds = out
                 assert 1 <= parts <= 64 and part % 1024 == 0 and (parts - 1) * part < vocab <= parts * part
-                assert rounds == (8 if drawn and children > 1 else 1)
+                assert rounds == (1 if drawn and children > 1 else 0)
                 assert batch * parts * 256 <= 1 << 31
                 need = batch * (parts * 32 + 128)
                 for more in ((batch, vocab), (batch + 1, vocab), (min(2 * batch, 1 << 20), min(1 << 28, 3 * vocab)), (1 << 20, 1 << 28)):
