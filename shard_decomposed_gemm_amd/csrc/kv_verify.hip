@@ -50,7 +50,7 @@ struct Shared {
   int32_t token[kKvNodes];  // -1: outside the vocabulary
   float p[kKvNodes], q[kKvNodes], u[kKvNodes];
   int16_t parent[kKvNodes];
-  int32_t path[kKvNodes];  // accepted nodes, then (without q) the tokens rejected at the last of them
+  int32_t path[kKvNodes];  // accepted nodes, then (without q) those rejected at the last of them
   KvWalkWords walk;
 };
 
@@ -100,21 +100,32 @@ __device__ inline void load_tree(const KvVerifyArgs& a, const Rows& r, Shared& s
 template <bool DRAWN>
 __device__ inline void go_on(Shared& s, KvWalk w, int n, int lane) {
   w.wants = 0;
+  // Node `base` + lane, in registers: most trees are one such group.
+  int base = -1, parent, token;
+  float np, nq = 0.f, nu;
+  auto group = [&](int i0) {
+    if (base == i0) return;
+    base = i0;
+    const int i = i0 + lane < n ? i0 + lane : n - 1;
+    parent = i0 + lane < n ? s.parent[i] : -2;
+    token = s.token[i];
+    np = s.p[i];
+    if constexpr (DRAWN) nq = s.q[i];
+    nu = s.u[i];
+  };
+  auto number_of = [](float x, int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l)); };
   for (;;) {
     // the next child of the node, and whether an earlier one had its token
     int c = -1;
     for (int i0 = w.last & ~63; i0 < n && c < 0; i0 += 64) {
-      const int i = i0 + lane;
-      const uint64_t is = __ballot(i > w.last && i < n && s.parent[i] == w.node);
+      group(i0);
+      const uint64_t is = __ballot(i0 + lane > w.last && parent == w.node);
       if (is) c = i0 + __builtin_ctzll(is);
     }
     if (c < 0) break;
-    const int x = s.token[c];
-    bool again = x < 0;
-    for (int i0 = w.node & ~63; i0 < c && !again; i0 += 64) {
-      const int i = i0 + lane;
-      again = __any(i > w.node && i < c && s.parent[i] == w.node && s.token[i] == x);
-    }
+    const int l = c & 63, x = __builtin_amdgcn_readlane(token, l);
+    bool again = x < 0 || __any(lane < l && parent == w.node && token == x);
+    for (int i = (w.node & ~63) + lane; i < base && !again; i += 64) again = __any(s.parent[i] == w.node && s.token[i] == x);
     if (again || (DRAWN && !(w.S < 1.0)) || (!w.pending && !(w.Z > 0.0))) {
       w.last = c;
       continue;
@@ -124,10 +135,10 @@ __device__ inline void go_on(Shared& s, KvWalk w, int n, int lane) {
       break;
     }
     w.last = c;
-    const double p = s.p[c], u = s.u[c];
+    const double p = number_of(np, l), u = number_of(nu, l);
     bool take;
     if constexpr (DRAWN) {
-      const double q = s.q[c], left = __builtin_fma(-w.A, q, p);
+      const double q = number_of(nq, l), left = __builtin_fma(-w.A, q, p);
       take = u * q * w.Z < (left > 0.0 ? left : 0.0) * (1.0 - w.S);
       if (!take) {
         w.A += w.Z / (1.0 - w.S);
@@ -138,7 +149,7 @@ __device__ inline void go_on(Shared& s, KvWalk w, int n, int lane) {
       take = u * w.Z < p;
       if (!take) {
         w.Z -= p;
-        if (lane == 0) s.path[w.count + w.rejects] = x;
+        if (lane == 0) s.path[w.count + w.rejects] = c;
         ++w.rejects;
       }
     }
@@ -172,11 +183,12 @@ __device__ inline double sum_up_to(double x) {
   x += moved<0x143, 0xc>(x);  // row_bcast:31
   return x;
 }
-__device__ inline double wave_sum(double x) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, sum_up_to(x));
-  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+__device__ inline double lane_of(double x, int l) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, l), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+__device__ inline double wave_sum(double x) { return lane_of(sum_up_to(x), 63); }
 
 // Begins the walk of a sequence; `keeps`: and leaves how far it has come. False if there is nothing to walk.
 template <bool DRAWN>
@@ -200,16 +212,17 @@ __device__ inline bool begin(const KvVerifyArgs& a, int b, Shared& s, bool keeps
   __syncthreads();
   if (keeps) {
     const KvWalk w = __builtin_bit_cast(KvWalk, s.walk);
-    for (int i = tid; i < r.n; i += kThreads) a.path[r.row0 + i] = i < w.count + w.rejects ? s.path[i] : -1;
+    // rejected ones as their tokens, which the draw leaves out
+    for (int i = tid; i < r.n; i += kThreads)
+      a.path[r.row0 + i] = i < w.count ? s.path[i] : i < w.count + w.rejects ? s.token[s.path[i]] : -1;
     if (tid == 0) a.states[b].walk = w;
   }
   return true;
 }
 
-// A wave's sum of the weights of tokens t0 .. t1 - 1 of a row.
+// A wave's sum of the weights of tokens t0 .. t1 - 1 of a row, and of the lanes' `sum`.
 template <bool DRAWN>
-__device__ inline double sum_segment(const float* p, const float* q, double A, int t0, int t1, int lane) {
-  double sum = 0.0;
+__device__ inline double sum_segment(const float* p, const float* q, double A, int t0, int t1, int lane, double sum) {
   int t = t0 + 4 * lane;
 #pragma unroll 4
   for (; t + 4 <= t1; t += 256) {
@@ -242,7 +255,7 @@ struct Row {
     const int64_t t = (int64_t)i * segment;
     return t < vocab ? (int)t : vocab;
   }
-  __device__ double sum(int i, int lane) const { return sum_segment<DRAWN>(p, q, A, first(i), first(i + 1), lane); }
+  __device__ double sum(int i, int lane, double start = 0.0) const { return sum_segment<DRAWN>(p, q, A, first(i), first(i + 1), lane, start); }
 };
 
 struct Meeting {
@@ -267,18 +280,11 @@ __device__ inline void sum_all(Meeting& m, const Row<DRAWN>& row, int segments) 
 
 // Draws from the row that the walk w has ended at, whose sums are there, and
 // writes the sequence's results. `tree`: s has the tree, which the path follows
-// from; else the path is written, and s has the rejected tokens and their p.
+// from; else the path is written, and s.token has the rejected tokens.
 template <bool DRAWN>
 __device__ inline void draw(const KvVerifyArgs& a, int b, Shared& s, Meeting& m, KvWalk w, Row<DRAWN> row, int64_t row0, int n,
                             float u0, bool tree) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, segments = a.plan.parts * kSegments;
-  if constexpr (!DRAWN) {  // rejected tokens have no weight
-    if (tid < segments)
-      for (int i = 0; i < w.rejects; ++i)
-        if (s.token[i] >= row.first(tid) && s.token[i] < row.first(tid + 1))
-          m.sums[tid] -= weight<false>(0.0, s.p[i], 0.f);
-    __syncthreads();
-  }
   double all = total_of(m, segments);
   int rejects = w.rejects;
   if (!(all > 0.0)) {  // nothing left: p itself
@@ -289,93 +295,107 @@ __device__ inline void draw(const KvVerifyArgs& a, int b, Shared& s, Meeting& m,
     sum_all(m, row, segments);
     all = total_of(m, segments);
   }
+  constexpr int kNone = 0x7fffffff;
   int token = -1;
   if (all > 0.0) {
-    // The first segment whose sum with those before it passes the number, then the first token.
     const double x = (double)number(u0) * all;
-    auto search = [&](const double (&v)[8], int per, double below, double& before) {
-      // v: this thread's numbers. The index (tid per + i) of the first whose running sum passes x, or -1, and the sum
-      // before it.
+    // The first segment whose sum with those before it passes the number, in every wave: four segments a lane.
+    static_assert(kKvParts * kSegments == 4 * 64, "all segments in a wave");
+    double v[8], below = 0.0;
+    int at = -1;
+    {
       double own = 0.0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) own += v[i];
-      const double upto = sum_up_to(own);
-      __syncthreads();
-      if (lane == 63) m.waves[wave] = upto;
-      if (tid == 0) m.found = 0x7fffffff;
-      __syncthreads();
-      double run = below + (upto - own);
+      for (int i = 0; i < 4; ++i) {
+        v[i] = 4 * lane + i < segments ? m.sums[4 * lane + i] : 0.0;
+        own += v[i];
+      }
+      double run = sum_up_to(own) - own, before = 0.0;  // exact where all sums are
+      int hit = -1;
 #pragma unroll
-      for (int i = 0; i < kSegments; ++i)
-        if (i < wave) run += m.waves[i];
-      int hit = 0x7fffffff;
-      double at = 0.0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (hit == 0x7fffffff && v[i] > 0.0 && run + v[i] > x) {
-          hit = tid * per + i;
-          at = run;
+      for (int i = 0; i < 4; ++i) {
+        if (hit < 0 && v[i] > 0.0 && run + v[i] > x) {
+          hit = 4 * lane + i;
+          before = run;
         }
         run += v[i];
       }
-      if (hit != 0x7fffffff) atomicMin(&m.found, hit);
-      __syncthreads();
-      const int first = m.found;
-      if (hit == first && hit != 0x7fffffff) m.waves[0] = at;
-      __syncthreads();
-      before = m.waves[0];
-      __syncthreads();
-      return first == 0x7fffffff ? -1 : first;
-    };
-    double v[8] = {};
-    if (tid < segments) v[0] = m.sums[tid];
-    double below = 0.0;
-    int at = search(v, 1, 0.0, below);
-    if (at < 0) {  // only by rounding, where sums are not exact: the last one with a weight
-      below = 0.0;
-      for (int i = 0; i < segments; ++i)
-        if (m.sums[i] > 0.0) at = i;
-      for (int i = 0; i < at; ++i) below += m.sums[i];
+      const uint64_t hits = __ballot(hit >= 0);
+      if (hits) {
+        const int l = __builtin_ctzll(hits);
+        at = __builtin_amdgcn_readlane(hit, l);
+        below = lane_of(before, l);
+      } else {  // only by rounding, where sums are not exact: the last one with a weight
+        for (int i = 0; i < segments; ++i)
+          if (m.sums[i] > 0.0) at = i;
+        for (int i = 0; i < at; ++i) below += m.sums[i];
+      }
     }
+    // Then the first token. Rejected ones of the segment are left out.
     const int t1 = row.first(at + 1);
+    __syncthreads();
+    if (tid == 0) m.told = 0;
+    __syncthreads();
+    if constexpr (!DRAWN) {
+      for (int k = tid; k < rejects; k += kThreads) {
+        const int t = s.token[k];
+        if (t >= row.first(at) && t < t1) s.path[atomicAdd(&m.told, 1)] = t;
+      }
+      __syncthreads();
+    }
+    const int out = m.told;
     int end = -1;
     for (int t0 = row.first(at); t0 < t1 && token < 0; t0 += 8 * kThreads) {
       const int t = t0 + 8 * tid;
-      float x4[8] = {}, y4[8] = {};
+      float px[8] = {}, qx[8] = {};
       if (t + 8 <= t1) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float4v xx = reinterpret_cast<const Quad*>(row.p + t + 4 * i)->x;
-          const float4v yy = DRAWN ? reinterpret_cast<const Quad*>(row.q + t + 4 * i)->x : xx;
+          const float4v p4 = reinterpret_cast<const Quad*>(row.p + t + 4 * i)->x;
+          const float4v q4 = DRAWN ? reinterpret_cast<const Quad*>(row.q + t + 4 * i)->x : p4;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x4[4 * i + k] = xx[k], y4[4 * i + k] = yy[k];
+          for (int k = 0; k < 4; ++k) px[4 * i + k] = p4[k], qx[4 * i + k] = q4[k];
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (t + i < t1) x4[i] = row.p[t + i], y4[i] = row.q[t + i];
+          if (t + i < t1) px[i] = row.p[t + i], qx[i] = row.q[t + i];
       }
-      double whole = 0.0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = weight<DRAWN>(w.A, px[i], qx[i]);
+      if constexpr (!DRAWN)
+        for (int k = 0; k < out; ++k) {
+          const int z = s.path[k] - t;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (z == i) v[i] = 0.0;
+        }
+      double own = 0.0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] = weight<DRAWN>(w.A, x4[i], y4[i]);
-        if constexpr (!DRAWN)
-          for (int k = 0; k < rejects; ++k)
-            if (s.token[k] == t + i) v[i] = 0.0;
-        if (v[i] > 0.0) end = t + i > end ? t + i : end;
-        whole += v[i];
+        if (v[i] > 0.0) end = t + i;
+        own += v[i];
       }
-      double before;
-      const int hit = search(v, 8, below, before);
-      if (hit >= 0) {
-        token = t0 + hit;
-      } else {
-        whole = wave_sum(whole);
-        if (lane == 0) m.waves[wave] = whole;
-        __syncthreads();
-        for (int i = 0; i < kSegments; ++i) below += m.waves[i];
-        __syncthreads();
+      const double upto = sum_up_to(own);
+      if (lane == 63) m.waves[wave] = upto;
+      if (tid == 0) m.found = kNone;
+      __syncthreads();
+      double run = below + (upto - own);
+#pragma unroll
+      for (int i = 0; i < kSegments; ++i) {
+        if (i < wave) run += m.waves[i];
+        below += m.waves[i];
       }
+      int hit = kNone;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (hit == kNone && v[i] > 0.0 && run + v[i] > x) hit = t + i;
+        run += v[i];
+      }
+      if (hit != kNone) atomicMin(&m.found, hit);
+      __syncthreads();
+      if (m.found != kNone) token = m.found;
+      __syncthreads();
     }
     if (token < 0) {  // see above
       if (tid == 0) m.found = -1;
@@ -492,7 +512,15 @@ __global__ __launch_bounds__(kThreads) void kv_verify_sum_kernel(KvVerifyArgs a)
   const int lane = threadIdx.x & 63, i = part * kSegments + (threadIdx.x >> 6);
   int64_t row0;
   if (!begin<DRAWN>(a, b, s, part == 0, row0)) return;
-  const double mine = Row<DRAWN>(a, row0, __builtin_bit_cast(KvWalk, s.walk)).sum(i, lane);
+  const KvWalk w = __builtin_bit_cast(KvWalk, s.walk);
+  const Row<DRAWN> row(a, row0, w);
+  double start = 0.0;
+  if constexpr (!DRAWN)  // rejected tokens have no weight
+    for (int k = lane; k < w.rejects; k += 64) {
+      const int node = s.path[w.count + k], t = s.token[node];
+      if (t >= row.first(i) && t < row.first(i + 1)) start -= weight<false>(0.0, s.p[node], 0.f);
+    }
+  const double mine = row.sum(i, lane, start);
   if (lane == 0) a.sums[(int64_t)b * a.plan.parts * kSegments + i] = mine;
 }
 // SUMMED: the sums that the walk wants are there; else only what the rounds left is to do.
@@ -502,20 +530,27 @@ __global__ __launch_bounds__(kThreads) void kv_verify_draw_kernel(KvVerifyArgs a
   __shared__ Meeting m;
   const int b = blockIdx.x, tid = threadIdx.x, segments = a.plan.parts * kSegments;
   KvWalk w = a.states[b].walk;
-  const int64_t row0 = a.q_start[b];
-  const int n = a.q_start[b + 1] - (int)row0;
+  const Rows r = rows_of(a, b);
+  const int64_t row0 = r.row0;
+  const int n = r.n;
   if (SUMMED && tid < segments) m.sums[tid] = a.sums[(int64_t)b * segments + tid];
+  int known[kKvNodes / kThreads];
+  if constexpr (!DRAWN) {
+#pragma unroll
+    for (int i = 0; i < kKvNodes / kThreads; ++i)
+      if (tid + i * kThreads < n) known[i] = a.path[row0 + tid + i * kThreads];
+  }
   if (w.done) return;
   Row<DRAWN> row(a, row0, w);
   const float u0 = a.u[row0];
   const bool tree = !SUMMED || w.wants;
   if (tree) {
     load_tree<DRAWN>(a, Rows{row0, n, true}, s, false);
-  } else if (!DRAWN) {
-    for (int i = tid; i < w.rejects; i += kThreads) {
-      const int x = a.path[row0 + w.count + i];
-      s.token[i] = x;
-      s.p[i] = row.p[x];
+  } else if constexpr (!DRAWN) {
+#pragma unroll
+    for (int i = 0; i < kKvNodes / kThreads; ++i) {
+      const int k = tid + i * kThreads - w.count;
+      if (k >= 0 && k < w.rejects) s.token[k] = known[i];
     }
   }
   __syncthreads();
