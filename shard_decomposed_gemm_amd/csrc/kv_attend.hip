@@ -590,7 +590,13 @@ template <int D, int NT, bool F32, bool TREE>
 __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void kv_attend_few_kernel(KvAttendArgs a) {
   constexpr int MT = D / 16;
   constexpr int R = 16 * NT, LD = D + 4;  // rows of an item; a row's floats in LDS, padded off the same banks
-  __shared__ __attribute__((aligned(16))) float part[kWaves][R][LD];
+  // From three tiles on the queries lie in LDS, for want of registers, and the
+  // waves join two tiles at a time, for want of LDS.
+  constexpr bool QL = NT > 2;
+  constexpr int PN = QL ? 2 : NT;
+  __shared__ __attribute__((aligned(16))) float part[kWaves][16 * PN][LD];
+  __shared__ half8v ql[QL ? NT : 1][QL ? D / 32 : 1][64];
+  __shared__ TreeRow tl[QL ? R : 1];
   __shared__ float heads[kWaves][R][2];
   const uint32_t lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -657,12 +663,12 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
     load_values<D>(v, block_buffer<D>(blk), 16 * lane, 16 * quarter);
   }
 
-  half8v q[NT][D / 32];
+  half8v q[QL ? 1 : NT][D / 32];
   float4v o[NT][MT];  // O^T: row 4 quarter + i of tile m is channel (4 quarter + i) D / 16 + m
   float base[NT];     // m - kShift
   float sum[NT];      // of this lane's weights
   int seen[NT];       // keys that the column's row sees (without a tree)
-  TreeRow tree[NT];
+  TreeRow tree[QL ? 1 : NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     // Columns past the last row repeat row 0: loads that some lanes leave out
@@ -671,14 +677,19 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
     const int i = r / G;
     const _Float16* src = a.q + (seq.row0 + i) * a.q_ts + (int64_t)(h * G + r - i * G) * a.q_hs + quarter * (D / 4);
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) q[n][x] = query_operand(src + 8 * x);
-    if constexpr (TREE) tree[n] = tree_row(a, seq.row0 + i);
-    else seen[n] = seq.seen(i);
+    for (int x = 0; x < D / 32; ++x)
+      if constexpr (!QL) q[n][x] = query_operand(src + 8 * x);
+      else if ((n * (D / 32) + x) % kWaves == wave) ql[n][x][lane] = query_operand(src + 8 * x);
+    if constexpr (TREE) {
+      if constexpr (!QL) tree[n] = tree_row(a, seq.row0 + i);
+      else if (wave == n % kWaves && quarter == 0) tl[n * 16 + col] = tree_row(a, seq.row0 + i);
+    } else seen[n] = seq.seen(i);
     base[n] = kNoMax;
     sum[n] = 0.f;
 #pragma unroll
     for (int m = 0; m < MT; ++m) o[n][m] = float4v{0.f, 0.f, 0.f, 0.f};
   }
+  if constexpr (QL) __syncthreads();
   const int whole = TREE ? seq.below_tree() >> 5 : seq.seen(0) >> 5;  // blocks that every row sees whole
   const float factor = a.scale * kLog2e;
   float limit = kTop;  // of the exponents, the same in all lanes; -inf once some row's base is far
@@ -692,15 +703,20 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
     if constexpr (more) find(j + kWaves);
 
     float4v s[NT][2];
+    half8v qi[QL ? NT : 1];
 #pragma unroll
     for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
+      if constexpr (QL) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) qi[n] = ql[n][i][lane];
+      }
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const half8v kk = key_operand(bits, k.w[t][i], half2v{k.pair[t].x, k.pair[t].x}, half2v{k.pair[t].y, k.pair[t].y});
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, q[n][i], s[n][t], 0, 0, 0);
+        for (int n = 0; n < NT; ++n) s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kk, QL ? qi[n] : q[n][i], s[n][t], 0, 0, 0);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -714,7 +730,7 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
       int left = TREE ? 0 : (end > 0 ? seen[n] - j * 32 : 0) - (int)quarter * 4;
       uint32_t bits_seen = 0;
       if constexpr (TREE)
-        if (hide && end > 0) bits_seen = tree_seen(a, tree[n], seq, j * 32) >> (quarter * 4);
+        if (hide && end > 0) bits_seen = tree_seen(a, QL ? tl[n * 16 + col] : tree[QL ? 0 : n], seq, j * 32) >> (quarter * 4);
       auto exponents = [&](float bs) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) e[i] = __builtin_fmaf(s[n][i >> 2][i & 3], factor, -bs);
@@ -797,43 +813,56 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
     sum[n] += __shfl_xor(sum[n], 16);
     sum[n] += __shfl_xor(sum[n], 32);
     const int r = n * 16 + col;
-    if (r >= rows) continue;
-    if (quarter == 0) {
+    if (r < rows && quarter == 0) {
       heads[wave][r][0] = base[n];
       heads[wave][r][1] = sum[n];
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int m = 0; m < MT; m += 4)
-        *reinterpret_cast<float4v*>(&part[wave][r][(quarter * 4 + i) * MT + m]) =
-            float4v{o[n][m][i], o[n][m + 1][i], o[n][m + 2][i], o[n][m + 3][i]};
   }
-  __syncthreads();
   float* slot = a.ws + slot_id * a.plan.slot_floats;
-  for (int x = threadIdx.x; x < rows * (D / 4); x += kWaves * 64) {
-    const int r = x / (D / 4), d = 4 * (x % (D / 4));
-    float top = kNoMax, all = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, heads[w][r][0]);
-    float4v v4 = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = exp2_hw(heads[w][r][0] - top);
-      all += heads[w][r][1] * f;
-      v4 += *reinterpret_cast<const float4v*>(&part[w][r][d]) * f;
+  for (int n0 = 0; n0 < NT; n0 += PN) {
+    const int p0 = 16 * n0;
+    if (QL && n0 > 0) {
+      if (p0 >= rows) break;
+      __syncthreads();
     }
-    if (runs == 1) {
-      const int i = (r0 + r) / G;
-      const int64_t row = (seq.row0 + i) * a.L.Hq + h * G + r0 + r - i * G;
-      const float inv = all != 0.f ? 1.f / all : 0.f;
-      store_out<F32, 4>(a.out, row * D + d, {v4.x * inv, v4.y * inv, v4.z * inv, v4.w * inv});
-      if (a.lse && d == 0) a.lse[row] = all != 0.f ? (top + log2f(all)) * kLn2 : kLowest;
-    } else {
-      *reinterpret_cast<float4v*>(slot + r * D + d) = v4;
-      if (d == 0) {
-        slot[a.plan.rows * D + 2 * r] = top;
-        slot[a.plan.rows * D + 2 * r + 1] = all;
+#pragma unroll
+    for (int n = n0; n < n0 + PN && n < NT; ++n) {
+      const int r = n * 16 + col;
+      if (r >= rows) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int m = 0; m < MT; m += 4)
+          *reinterpret_cast<float4v*>(&part[wave][r - p0][(quarter * 4 + i) * MT + m]) =
+              float4v{o[n][m][i], o[n][m + 1][i], o[n][m + 2][i], o[n][m + 3][i]};
+    }
+    __syncthreads();
+    const int here = rows - p0 < 16 * PN ? rows - p0 : 16 * PN;
+    for (int x = threadIdx.x; x < here * (D / 4); x += kWaves * 64) {
+      const int l = x / (D / 4), r = p0 + l, d = 4 * (x % (D / 4));
+      float top = kNoMax, all = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, heads[w][r][0]);
+      float4v v4 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = exp2_hw(heads[w][r][0] - top);
+        all += heads[w][r][1] * f;
+        v4 += *reinterpret_cast<const float4v*>(&part[w][l][d]) * f;
+      }
+      if (runs == 1) {
+        const int i = (r0 + r) / G;
+        const int64_t row = (seq.row0 + i) * a.L.Hq + h * G + r0 + r - i * G;
+        const float inv = all != 0.f ? 1.f / all : 0.f;
+        store_out<F32, 4>(a.out, row * D + d, {v4.x * inv, v4.y * inv, v4.z * inv, v4.w * inv});
+        if (a.lse && d == 0) a.lse[row] = all != 0.f ? (top + log2f(all)) * kLn2 : kLowest;
+      } else {
+        *reinterpret_cast<float4v*>(slot + r * D + d) = v4;
+        if (d == 0) {
+          slot[a.plan.rows * D + 2 * r] = top;
+          slot[a.plan.rows * D + 2 * r + 1] = all;
+        }
       }
     }
   }
@@ -1361,7 +1390,10 @@ hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
   } else if (a.plan.rows == 16) {
     e = kv_launch(kv_attend_few_kernel<D, 1, F32, TREE>, grid, kWaves * 64, s, a);
   } else if constexpr (D <= 128) {
-    e = kv_launch(kv_attend_few_kernel<D, 2, F32, TREE>, grid, kWaves * 64, s, a);
+    e = hipErrorInvalidValue;
+    if (a.plan.rows == 32) e = kv_launch(kv_attend_few_kernel<D, 2, F32, TREE>, grid, kWaves * 64, s, a);
+    if constexpr (TREE && !(D == 128 && F32))
+      if (a.plan.rows == 64) e = kv_launch(kv_attend_few_kernel<D, 4, F32, true>, grid, kWaves * 64, s, a);
   }
   if (a.plan.ws_bytes > 0 && e == hipSuccess)
     e = TREE ? a.plan.join_rows == 0

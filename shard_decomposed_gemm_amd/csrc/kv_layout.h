@@ -240,35 +240,39 @@ KV_HD inline int kv_tree_longer(const KvPlan& p, int c, int runs) {
 }
 
 // A call with a tree. Its items are (sequence, tile of rows, kv head), whose rows
-// all see nearly all of the sequence. Four forms take them: the kernel for few
-// rows with tiles of 16 or 32 rows, the one for many with 128 or 256. The
-// first two start fast and need no barrier, the others unpack a block once for
-// four or eight waves. Which is faster follows from the work of a place (a
-// workgroup that runs at once with others), by a model fitted to 480 shapes with 8
-// kv heads (1 to 32 sequences of 200 to 32000 tokens, 24 to 512 rows a kv head):
+// all see nearly all of the sequence. Five forms take them: the kernel for few
+// rows with tiles of 16, 32 or 64 rows, the one for many with 128 or 256. The
+// former start fast and need no barrier, and the more rows unpack a block once
+// the better; the latter unpack it once for four or eight waves. Which is faster
+// follows from the work of a place (a workgroup that runs at once with others), by
+// a model fitted to 560 shapes with 8 kv heads (1 to 32 sequences of 200 to 32000
+// tokens, 24 to 512 rows a kv head):
 //   us = first + round max(1, items / places) + (block + full F) B + J (join + runs N / places)
 // with B the blocks of a place, F the part of a tile's rows that exist, J whether
-// items of several runs are joined, N the runs. Its choice takes 1.02 times the
-// best form's time on average (1.4 at worst). In us, of D 128, tiles of 16, 32, 128
-// and 256 rows:
-//   8 sequences of 500 tokens,    64 rows    10.2   12.0   21.4   20.6
-//   8 of 16000,                   64         88.9   69.6   88.3    101
-//   32 of 1000,                  128         53.1   55.0   57.5   38.4
-//   8 of 16000,                  128          147    110    104    109
-//   32 of 8000,                  128                 237    190    200
-//   8 of 16000,                  384                 324    311    261
+// items of several runs are joined, N the runs. Its choice takes 1.03 times the
+// best form's time on average (1.4 at worst). In us, of D 128, tiles of 16, 32,
+// 64, 128 and 256 rows:
+//   8 sequences of 500 tokens,    64 rows     9.8   12.2   16.0   19.5   17.4
+//   8 of 16000,                   64         87.7   70.1   61.4   88.7   99.0
+//   32 of 2000,                   64         47.7   48.2   37.7   53.1   55.3
+//   8 of 16000,                  104          150    114   95.2    102    107
+//   32 of 2000,                  200          131    145    125   89.1   80.0
+//   8 of 16000,                  384                 324           311    261
+// A binary32 output of D 128 does not fit 64 rows' registers (8 of 16000, 64 rows:
+// 85.9 us spilling, 76.0 with 32).
 struct KvForm {
   int rows, places_per_cu, blocks;  // blocks: of a sequence that is one run for sure
   double first, round, block, full, join, runs;
 };
 inline int kv_tree_forms(int D, const KvForm** forms) {
-  static const KvForm d64[] = {{16, 2, 64, 3.2, 3.3, .148, 0, 2.6, 6.9}, {32, 1, 32, 5.6, 1.9, .117, 0, 5.1, .4},
-                               {128, 2, 32, 0, 5.1, .572, .187, 4.9, 13.1}};
-  static const KvForm d128[] = {{16, 2, 64, 1.0, 4.6, .248, 0, .9, 12.7}, {32, 1, 32, 2.0, 6.4, .203, 0, 4.0, 3.1},
-                                {128, 2, 32, 0, 4.9, .864, .319, 5.4, 20.9}, {256, 1, 32, 0, 8.6, .525, .523, 4.1, 17.1}};
+  static const KvForm d64[] = {{16, 2, 64, 3.1, 3.4, .149, 0, 2.5, 7.0}, {32, 1, 32, 5.8, 1.8, .120, 0, 5.0, 0},
+                               {64, 1, 32, 1.6, 7.4, .213, 0, 4.1, 2.9}, {128, 2, 32, 0, 5.2, .563, .186, 4.8, 12.7}};
+  static const KvForm d128[] = {{16, 2, 64, 1.0, 4.6, .249, 0, .8, 12.8}, {32, 1, 32, 2.1, 6.3, .208, 0, 4.2, 2.7},
+                                {64, 1, 32, 1.1, 9.7, .318, 0, 2.9, 5.6}, {128, 2, 32, 0, 4.8, .868, .342, 5.7, 19.6},
+                                {256, 1, 32, 0, 8.5, .519, .555, 4.4, 15.6}};
   static const KvForm d256[] = {{16, 1, 64, 3.1, 6.2, .264, 0, 3.6, 6.4}, {128, 1, 32, 0, 13.1, 1.55, .125, 2.9, 19.0}};
   *forms = D == 64 ? d64 : D == 128 ? d128 : d256;
-  return D == 64 ? 3 : D == 128 ? 4 : 2;
+  return D == 64 ? 4 : D == 128 ? 5 : 2;
 }
 // The shortest run: four blocks a wave make up for what a run costs beside its
 // blocks; a tile for many rows has large partials, and short runs only where few
@@ -324,7 +328,7 @@ inline double kv_tree_us(const KvForm& f, const KvPlan& p, int64_t rows, int64_t
   return f.first + f.round * (per_place > 1 ? per_place : 1) + (f.block + f.full * fill) * chain +
          (split ? f.join + f.runs * (runs < 1 ? runs : 1) * fill : 0);
 }
-inline KvPlan kv_tree_plan(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
+inline KvPlan kv_tree_plan(const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, bool out_f32, int num_cus) {
   const KvForm* forms;
   const int n = kv_tree_forms(L.D, &forms);
   const int64_t rows = max_q * (L.Hq / L.Hkv), nblk = kv_expected_blocks(max_kv);
@@ -332,6 +336,7 @@ inline KvPlan kv_tree_plan(const KvLayout& L, int64_t batch, int64_t max_q, int6
   double least = 0;
   for (int i = 0; i < n; ++i) {
     if (forms[i].rows >= 128 && rows <= 32) break;  // their partials would be the most of a decoder's workspace
+    if (forms[i].rows == 64 && L.D == 128 && out_f32) continue;
     const KvPlan p = kv_tree_plan_as(forms[i], L, batch, max_q, max_kv, num_cus);
     const double us = kv_tree_us(forms[i], p, rows, nblk);
     if (i == 0 || us < least) best = p, least = us;

@@ -62,7 +62,8 @@ int attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, const uint
   KvPlan plan{};
   if (p && p->batch >= 0 && p->batch <= kKvMaxTokens && p->max_q >= 1 && p->max_q <= kKvMaxTokens &&
       p->max_kv >= 1)  // refused below otherwise
-    plan = (mask ? kv_tree_plan : kv_attend_plan)(ctx->L, p->batch, p->max_q, p->max_kv, ctx->num_cus);
+    plan = mask ? kv_tree_plan(ctx->L, p->batch, p->max_q, p->max_kv, p->out_f32 != 0, ctx->num_cus)
+                : kv_attend_plan(ctx->L, p->batch, p->max_q, p->max_kv, ctx->num_cus);
   char why[kKvWhy];
   const int rc = kv_check_attend(ctx->L, pages, p, plan, workspace, workspace_bytes, why);
   if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);

@@ -33,8 +33,8 @@ static KvPlan tree_plan;
 extern "C" {
 
 // rows, many, tiles, items, slots, places, least, most_runs, partials, join_rows, join_groups, join_grid, ws_bytes
-void kvt_plan(int Hq, int Hkv, int D, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus, int64_t* out) {
-  const KvPlan p = tree_plan = kv_tree_plan(kv_layout(Hq, Hkv, D, 64, 1000), batch, max_q, max_kv, num_cus);
+void kvt_plan(int Hq, int Hkv, int D, int64_t batch, int64_t max_q, int64_t max_kv, int f32, int num_cus, int64_t* out) {
+  const KvPlan p = tree_plan = kv_tree_plan(kv_layout(Hq, Hkv, D, 64, 1000), batch, max_q, max_kv, f32 != 0, num_cus);
   const int64_t v[13] = {p.rows,      p.many,     p.tiles,     p.items,       p.slots,     p.places,  p.least,
                          p.most_runs, p.partials, p.join_rows, p.join_groups, p.join_grid, p.ws_bytes};
   for (int i = 0; i < 13; ++i) out[i] = v[i];

@@ -279,21 +279,42 @@ def test_attend_a_tree(Hq, Hkv, D, page, shape, words, kind, q_off, f32):
     assert (got[starts[-1]:] == PAD).all() and (lse[starts[-1]:] == PAD).all()
 
 
+def _batch(b, n, L):
+    """b sequences of up to n queries and L tokens, the first of most."""
+    return [(n - i % 3 if n > 3 else n, L - 37 * i % (L // 2)) for i in range(b)]
+
+
 FORMS = [
     # Hq, Hkv, D, page, [(queries, length)], max_kv: every kernel, one run an item and several, joined by rows and by
-    # workgroups, a batch of more sequences than lengths are looked through, lengths that max_kv does not say
-    (8, 1, 128, 64, [(2, 5000)], None),
+    # workgroups (tests/test_kv_tree_host.py sees to it), a batch of more sequences than lengths are looked through,
+    # lengths that max_kv does not say
+    (32, 8, 128, 32, _batch(12, 25, 64), None),
+    (2, 1, 128, 64, [(1, 60)], None),
+    (2, 1, 128, 64, [(1, 2100)], None),
+    (16, 2, 128, 64, _batch(6, 5, 2100), None),
+    (16, 8, 128, 64, _batch(32, 40, 500), 500),
+    (32, 8, 128, 64, _batch(32, 25, 1100), 1100),
+    (16, 4, 128, 64, _batch(2, 32, 4000), None),
+    (16, 8, 128, 64, _batch(16, 60, 200), None),
+    (8, 8, 128, 64, _batch(16, 40, 2100), None),
+    (8, 4, 256, 32, _batch(32, 25, 64), None),
+    (8, 4, 256, 64, _batch(32, 60, 1100), 1100),
+    (1, 1, 256, 32, [(1, 64)], None),
+    (1, 1, 256, 64, [(1, 2100)], None),
+    (8, 1, 256, 64, _batch(12, 5, 2100), None),
+    (2, 1, 64, 32, [(20, 64)], None),
+    (32, 8, 64, 64, _batch(32, 25, 1100), 1100),
+    (4, 1, 64, 32, [(1, 64)], None),
+    (4, 1, 64, 32, [(1, 2100)], None),
+    (32, 4, 64, 32, _batch(3, 5, 2100), None),
+    (16, 8, 64, 64, _batch(12, 60, 200), None),
+    (8, 1, 64, 64, _batch(4, 48, 2100), None),
+    (16, 8, 64, 64, _batch(32, 25, 500), 500),
+    (8, 8, 64, 64, _batch(32, 40, 2100), None),
     (8, 1, 128, 64, [(4, 9000)], 1300),
     (8, 1, 64, 32, [(4, 9000), (3, 100), (4, 5000)], 3000),
-    (4, 1, 256, 64, [(4, 6000), (2, 300)], None),
-    (8, 1, 256, 64, [(40, 6000), (20, 2500), (1, 40)], None),
-    (16, 1, 256, 64, [(64, 3000)], None),
-    (8, 2, 128, 64, [(16, 3500)] * 4, 3500),
     (8, 2, 128, 64, [(13, 3000), (16, 20), (0, 900), (5, 2000)], 5000),
-    (8, 2, 64, 32, [(64, 4000), (30, 100), (9, 2000)], None),
-    (16, 2, 128, 64, [(40, 2500), (64, 1100), (33, 35)], None),
     (16, 2, 128, 64, [(64, 6000)], 1100),
-    (24, 8, 128, 64, [(48, 1500)] * 6, None),
     (4, 4, 128, 32, [(i % 3, i % 3 + 1400 if i == 300 else i % 40 + 3) for i in range(520)], 1400),
     (2, 1, 128, 32, [(40 if i == 70 else i % 4, 1500 if i in (3, 70) else i % 90 + 40) for i in range(130)], 1500),
     (8, 1, 64, 32, [(i % 9, 60 * i + 9) for i in range(70)], None),

@@ -40,7 +40,7 @@ def host(tmp_path_factory):
     lib.kvt_verify_bound.argtypes = [i64, i64, ctypes.c_int]
     lib.kvt_verify_bound.restype = i64
     ints, longs = ctypes.POINTER(i32), ctypes.POINTER(i64)
-    lib.kvt_plan.argtypes = [ctypes.c_int] * 3 + [i64] * 3 + [ctypes.c_int, longs]
+    lib.kvt_plan.argtypes = [ctypes.c_int] * 3 + [i64] * 3 + [ctypes.c_int] * 2 + [longs]
     lib.kvt_plan.restype = None
     lib.kvt_bound.argtypes = [ctypes.c_int] * 3 + [i64] * 3 + [ctypes.c_int]
     lib.kvt_bound.restype = i64
@@ -235,9 +235,10 @@ def test_tree_plans_hold_any_lengths(host, D, cus):
     for _ in range(1500):
         Hq, Hkv = HEADS[r.integers(len(HEADS))]
         batch, max_q, max_kv = (int(np.exp(r.uniform(0, np.log(top)))) for top in (600, 1100, 1 << 22))
-        p = _plan(host, Hq, Hkv, D, batch, max_q, max_kv, cus)
+        f32 = int(r.integers(2))
+        p = _plan(host, Hq, Hkv, D, batch, max_q, max_kv, f32, cus)
         assert p["items"] == batch * Hkv * p["tiles"] and p["tiles"] * p["rows"] >= max_q * Hq // Hkv
-        assert p["rows"] in ((16, 128) if D == 256 else (16, 32, 128) if D == 64 else (16, 32, 128, 256))
+        assert p["rows"] in {64: (16, 32, 64, 128), 128: (16, 32, 128, 256) if f32 else (16, 32, 64, 128, 256), 256: (16, 128)}[D]
         if p["slots"] == p["items"]:
             assert p["ws_bytes"] == 0 or batch > 512
             continue
@@ -267,15 +268,30 @@ def test_tree_workspace_of_bounds_holds_every_smaller_call(host, cus):
         most = [int(np.exp(r.uniform(0, np.log(top)))) for top in (2000, 1100, 1 << 20)]
         less = [int(np.exp(r.uniform(0, np.log(top)))) for top in most]
         bound = host.kvt_bound(Hq, Hkv, D, *most, cus)
-        assert _plan(host, Hq, Hkv, D, *less, cus)["ws_bytes"] <= bound
-        assert _plan(host, Hq, Hkv, D, *most, cus)["ws_bytes"] <= bound
+        for f32 in (0, 1):
+            assert _plan(host, Hq, Hkv, D, *less, f32, cus)["ws_bytes"] <= bound
+            assert _plan(host, Hq, Hkv, D, *most, f32, cus)["ws_bytes"] <= bound
+
+
+def test_gpu_tests_reach_every_form(host):
+    from tests import test_gpu_kv_tree as t
+    seen = set()
+    for Hq, Hkv, D, page, shape, max_kv in t.FORMS:
+        width = max(1, max(-(-n // page) for _, n in shape)) * page
+        for f32 in (0, 1):
+            p = _plan(host, Hq, Hkv, D, len(shape), max(n for n, _ in shape), max_kv or width, f32, 256)
+            seen.add((D, p["rows"], p["slots"] > p["items"], p["join_rows"] > 0 if p["slots"] > p["items"] else None))
+    several = {(D, n, True) for D, rows in ((64, (16, 32, 64, 128)), (128, (16, 32, 64, 128, 256)), (256, (16, 128))) for n in rows}
+    one = {(D, n, False) for D, n, _ in several} - {(128, 32, False)}
+    assert {x[:3] for x in seen} >= one | several - {(128, 128, True)}  # one run of 32, several of 128: only larger calls
+    assert {x[3] for x in seen} == {None, False, True}
 
 
 def test_tree_plans_at_the_ends(host):
-    assert _plan(host, 64, 8, 128, 0, 5, 100, 256)["items"] == 0
-    p = _plan(host, 64, 8, 128, 1, 1, 1 << 40, 256)
+    assert _plan(host, 64, 8, 128, 0, 5, 100, 0, 256)["items"] == 0
+    p = _plan(host, 64, 8, 128, 1, 1, 1 << 40, 0, 256)
     assert p["partials"] <= 1024 and p["most_runs"] == 256
-    assert _plan(host, 1024, 1, 64, 1 << 20, 1024, 1 << 31, 256)["items"] >= 1 << 20  # refused for its items
+    assert _plan(host, 1024, 1, 64, 1 << 20, 1024, 1 << 31, 1, 256)["items"] >= 1 << 20  # refused for its items
 
 
 def test_reports(host):
