@@ -165,7 +165,7 @@ typedef struct {
 int kvc_attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* args, void* workspace,
                int64_t workspace_bytes, void* stream);
 
-/* Workspace that holds every kvc_attend call of up to `batch` sequences, max_q
+/* Workspace that holds every kvc_attend and kvc_attend_tree call of up to `batch` sequences, max_q
  * queries and max_kv tokens (any out type): one made for a server's largest
  * batch, chunk and length serves its smaller calls too, which may need more
  * than the largest one does. */
@@ -292,7 +292,7 @@ typedef struct {
 } kvc_commit_args;
 
 /* Moves the key and value of node path[i] of each sequence to place kv_len + i of
- * it, bit for bit, in each of `layers` caches of the context's shape (pages: a
+ * it, bit for bit, in each of `layers` (0 .. 1024) caches of the context's shape (pages: a
  * host array of as many device pointers, no two of them equal), with the same
  * page table. Other slots stay as they are.
  * Reported by kvc_check, and that sequence left, its new_len kv_len: rows and

@@ -203,7 +203,7 @@ inline int kv_check_commit(const KvLayout& L, void* const* pages, int32_t layers
   if (!p) return kv_refuse(why, AGEMM_EINVAL, "args must be non-NULL");
   int rc = kv_check_nodes(p->batch, p->max_q, p->tokens, why);
   if (rc) return rc;
-  if (layers < 0 || layers > 4096) return kv_refuse(why, AGEMM_EINVAL, "layers must be 0 to 4096");
+  if (layers < 0 || layers > 1024) return kv_refuse(why, AGEMM_EINVAL, "layers must be 0 to 1024");
   if ((int64_t)p->batch * L.Hkv > (int64_t{1} << 25)) return kv_refuse(why, AGEMM_ESHAPE, "more than 2^25 sequences' heads in a call");
   if (p->batch == 0 || (layers == 0 && !p->new_len)) return kKvNothing;
   if (layers > 0 && !pages) return kv_refuse(why, AGEMM_EINVAL, "pages must be non-NULL");

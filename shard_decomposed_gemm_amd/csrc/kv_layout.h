@@ -304,7 +304,8 @@ inline KvPlan kv_tree_plan_as(const KvForm& f, const KvLayout& L, int64_t batch,
   p.slots = p.items;
   p.places = num_cus * f.places_per_cu;
   p.least = kv_tree_least(p.rows, p.items, p.places);
-  if (p.items == 0 || batch > kKvMaxBatch || nblk <= f.blocks) return p;
+  // (So many items need no more runs, and their grid stays below 2^32 threads.)
+  if (p.items == 0 || p.items > 1 << 22 || batch > kKvMaxBatch || nblk <= f.blocks) return p;
   p.slots = p.items + p.places;
   p.most_runs = (int32_t)kv_tree_most_runs(nblk, p.least);
   p.partials = kv_tree_partials(p.items, p.most_runs, p.places);

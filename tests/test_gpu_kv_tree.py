@@ -886,6 +886,104 @@ def test_speculative_steps_in_a_graph_and_eager():
     assert lens.tolist() != [5, 10, 35]  # some drafts were accepted on the way
 
 
+def test_calls_at_once_on_streams():
+    """Two verifications whose workgroups wait for each other, two attention calls with trees, a layout and a commit in
+    flight together, each with a workspace of its own."""
+    import torch
+    Hq, Hkv, D, page, n = 8, 2, 128, 32, 20
+    pages, table, K, V = _sequences(22, Hkv, D, page, [3000, 900])
+    kv = _cache(Hq, Hkv, D, page_tokens=page, num_pages=pages.shape[0])
+    r = np.random.default_rng(5)
+    dp, dt, lens, starts = _dev(pages), _i32(table), _i32([3000, 900]), _i32([0, n, 2 * n])
+    masks = [np.concatenate([okt.masks(_parents(r, n), 1) for _ in range(2)]) for _ in range(2)]
+    dm = [_dev(x.view(np.int64)) for x in masks]
+    qs = [r.standard_normal((2 * n, Hq, D)).astype(np.float16) for _ in range(2)]
+    dq = [_dev(x) for x in qs]
+    outs = [_full((2 * n, Hq, D), "float32") for _ in range(2)]
+    ws = [kv.workspace(2, n, 3072) for _ in range(2)]
+    problems = [_verify_problem(30 + i, [30] * 12, 20011, True, "mixed", gap=1.5) for i in range(2)]
+    dev = [{k: _dev(x[k]) for k in ("token", "p", "q", "u")} | dict(parent=_i32(x["parent"]), starts=_i32(x["starts"])) for x in problems]
+    got = [(_full((360,), "int32"), _full((12,), "int32"), _full((12,), "int64")) for _ in range(2)]
+    vws = [kv.verify_workspace(12, 20011) for _ in range(2)]
+    parent, mask = _i32(_parents(r, n) * 2), _full((2 * n, 1), "int64")
+    c = _commit_problem(3, Hkv, D, page, 1, [(13, 60, [0, 2, 3, 9])])
+    other, old = _cache(Hkv, Hkv, D, page_tokens=page, num_pages=c["P"]), _dev(c["before"][0])
+    args = [_i32(c[k]) for k in ("starts", "lens", "path", "count", "table")]
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    torch.cuda.synchronize()
+    for turn in range(10):
+        for i in (0, 1):
+            d = dev[i]
+            kv.verify(d["token"], d["parent"], d["starts"], d["p"], d["u"], *got[i], max_q=30, q=d["q"], max_children=9,
+                      workspace=vws[i], stream=streams[i])
+            kv.attend(dp, dq[i], lens, dt, outs[i], q_start=starts, max_q=n, workspace=ws[i], stream=streams[2 + i], tree=dm[i])
+        kv.tree(parent, starts, lens, None, n, mask, stream=streams[4])
+        if turn == 0:
+            other.commit(old, *args, 13, stream=streams[5])
+    torch.cuda.synchronize()
+    kv.check()
+    other.check()
+    for i in (0, 1):
+        _check_verify([x.cpu().numpy() for x in got[i]], problems[i])
+        for b, L in enumerate((3000, 900)):
+            rows = slice(b * n, (b + 1) * n)
+            _check_rows(outs[i][rows].cpu().numpy().astype(np.float64), None, qs[i][rows], K[b], V[b],
+                        okt.visible(masks[i][rows], L - n, L), D ** -0.5, True)
+    np.testing.assert_array_equal(old.cpu().numpy(), _committed(c, Hkv, D, page)[0])
+
+
+def test_two_graphs_share_workspaces():
+    """Attention and verification captured into two graphs with the same workspaces, replayed in turn with eager calls in
+    between: what one leaves there does not matter to the other."""
+    import torch
+    Hq, Hkv, D, page = 8, 1, 64, 32
+    sides = []
+    ws = vws = None
+    for lens, n, vocab in (([4000, 70], 33, 5003), ([2500, 2600, 900], 9, 777)):
+        B = len(lens)
+        pages, table, _, _ = _sequences(B, Hkv, D, page, lens)
+        kv = _cache(Hq, Hkv, D, page_tokens=page, num_pages=pages.shape[0])
+        if ws is None:
+            ws, vws = kv.workspace(3, 33, 4096), kv.verify_workspace(3, 5003)
+        r = np.random.default_rng(B)
+        t = dict(dp=_dev(pages), dt=_i32(table), lens=_i32(lens), starts=_i32(_starts([n] * B)),
+                 q=_dev(r.standard_normal((B * n, Hq, D)).astype(np.float16)), out=_full((B * n, Hq, D), "float32"),
+                 mask=_dev(np.concatenate([okt.masks(_parents(r, n), 1) for _ in lens]).view(np.int64)))
+        c = _verify_problem(B, [n] * B, vocab, True, gap=1.0)
+        d = {k: _dev(c[k]) for k in ("token", "p", "q", "u")}
+        t.update(d, parent=_i32(c["parent"]), path=_full((B * n,), "int32"), count=_full((B,), "int32"), next=_full((B,), "int64"))
+
+        def step(kv=kv, t=t, n=n):
+            kv.attend(t["dp"], t["q"], t["lens"], t["dt"], t["out"], q_start=t["starts"], max_q=n, workspace=ws, tree=t["mask"])
+            kv.verify(t["token"], t["parent"], t["starts"], t["p"], t["u"], t["path"], t["count"], t["next"], max_q=n, q=t["q_"],
+                      max_children=9, workspace=vws)
+        t["q_"], t["q"] = t["q"], _dev(r.standard_normal((B * n, Hq, D)).astype(np.float16))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        step()
+        torch.cuda.synchronize()
+        _check_verify([t[k].cpu().numpy() for k in ("path", "count", "next")], c)
+        sides.append((kv, t, graph, {k: t[k].clone() for k in ("out", "path", "count", "next")}, step))
+    for turn in range(4):
+        for kv, t, graph, want, step in sides:
+            for k in want:
+                t[k].fill_(PAD)
+            graph.replay()
+            torch.cuda.synchronize()
+            for k, x in want.items():
+                assert torch.equal(t[k], x), k
+            if turn % 2:
+                step()
+            torch.cuda.synchronize()
+            kv.check()
+
+
 def test_tree_partials_of_ranks_combine():
     """Flash Decode with a tree: ranks that hold parts of the cached tokens attend without a mask, the last one with the
     tree; the combine of their partials is the attention over all."""

@@ -184,6 +184,8 @@ def test_commit_refusals_of_counts(host):
     why = ctypes.create_string_buffer(256)
     assert host.kvt_commit(2, _pointers(A), -1, _commit(), why) == agemm.EINVAL
     assert host.kvt_commit(2, None, 1, _commit(), why) == agemm.EINVAL
+    assert host.kvt_commit(2, _pointers(*(A + 16 * i for i in range(1024))), 1024, _commit(), why) == agemm.OK
+    assert host.kvt_commit(2, _pointers(A), 1025, _commit(), why) == agemm.EINVAL
     assert host.kvt_commit(1024, _pointers(A), 1, _commit(batch=(1 << 15) + 1), why) == agemm.ESHAPE
     assert host.kvt_commit(2, _pointers(A), 1, None, why) == agemm.EINVAL
 
@@ -238,6 +240,7 @@ def test_tree_plans_hold_any_lengths(host, D, cus):
         f32 = int(r.integers(2))
         p = _plan(host, Hq, Hkv, D, batch, max_q, max_kv, f32, cus)
         assert p["items"] == batch * Hkv * p["tiles"] and p["tiles"] * p["rows"] >= max_q * Hq // Hkv
+        assert p["items"] >= 1 << 23 or p["slots"] * 512 < 1 << 32
         assert p["rows"] in {64: (16, 32, 64, 128), 128: (16, 32, 128, 256) if f32 else (16, 32, 64, 128, 256), 256: (16, 128)}[D]
         if p["slots"] == p["items"]:
             assert p["ws_bytes"] == 0 or batch > 512
@@ -291,7 +294,11 @@ def test_tree_plans_at_the_ends(host):
     assert _plan(host, 64, 8, 128, 0, 5, 100, 0, 256)["items"] == 0
     p = _plan(host, 64, 8, 128, 1, 1, 1 << 40, 0, 256)
     assert p["partials"] <= 1024 and p["most_runs"] == 256
-    assert _plan(host, 1024, 1, 64, 1 << 20, 1024, 1 << 31, 1, 256)["items"] >= 1 << 20  # refused for its items
+    assert _plan(host, 1024, 1, 64, 1 << 20, 1024, 1 << 31, 1, 256)["items"] >= 1 << 23  # refused for its items
+    for max_q in (1 << 13, 1 << 16, 1 << 18, 1 << 20, 1 << 23):  # many items: one run each, in a grid that can be launched
+        for shape in ((1024, 1), (64, 8), (8, 8)):
+            p = _plan(host, *shape, 128, 512, max_q, 1 << 20, 0, 256)
+            assert p["items"] >= 1 << 23 or p["slots"] * 512 < 1 << 32
 
 
 def test_reports(host):
