@@ -590,10 +590,10 @@ template <int D, int NT, bool F32, bool TREE>
 __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void kv_attend_few_kernel(KvAttendArgs a) {
   constexpr int MT = D / 16;
   constexpr int R = 16 * NT, LD = D + 4;  // rows of an item; a row's floats in LDS, padded off the same banks
-  // From three tiles on the queries lie in LDS, for want of registers, and the
-  // waves join two tiles at a time, for want of LDS.
-  constexpr bool QL = NT > 2;
-  constexpr int PN = QL ? 2 : NT;
+  // Of many rows and channels the queries lie in LDS, for want of registers, and
+  // the waves join some tiles at a time, for want of LDS.
+  constexpr bool QL = NT * D > 256 || NT > 2;
+  constexpr int PN = !QL ? NT : D == 256 ? 1 : 2;
   __shared__ __attribute__((aligned(16))) float part[kWaves][16 * PN][LD];
   __shared__ half8v ql[QL ? NT : 1][QL ? D / 32 : 1][64];
   __shared__ TreeRow tl[QL ? R : 1];
@@ -1389,10 +1389,9 @@ hipError_t launch_d(const KvAttendArgs& a, hipStream_t s) {
     if constexpr (D == 128) e = kv_launch(kv_attend_many_kernel<D, 8, F32, TREE>, grid, 512, s, a);
   } else if (a.plan.rows == 16) {
     e = kv_launch(kv_attend_few_kernel<D, 1, F32, TREE>, grid, kWaves * 64, s, a);
-  } else if constexpr (D <= 128) {
-    e = hipErrorInvalidValue;
+  } else if constexpr (D <= 128 || TREE) {
     if (a.plan.rows == 32) e = kv_launch(kv_attend_few_kernel<D, 2, F32, TREE>, grid, kWaves * 64, s, a);
-    if constexpr (TREE && !(D == 128 && F32))
+    if constexpr (TREE && D <= 128 && !(D == 128 && F32))
       if (a.plan.rows == 64) e = kv_launch(kv_attend_few_kernel<D, 4, F32, true>, grid, kWaves * 64, s, a);
   }
   if (a.plan.ws_bytes > 0 && e == hipSuccess)

@@ -245,7 +245,7 @@ KV_HD inline int kv_tree_longer(const KvPlan& p, int c, int runs) {
 // former start fast and need no barrier, and the more rows unpack a block once
 // the better; the latter unpack it once for four or eight waves. Which is faster
 // follows from the work of a place (a workgroup that runs at once with others), by
-// a model fitted to 560 shapes with 8 kv heads (1 to 32 sequences of 200 to 32000
+// a model fitted to 700 shapes with 8 kv heads (1 to 32 sequences of 200 to 32000
 // tokens, 24 to 512 rows a kv head):
 //   us = first + round max(1, items / places) + (block + full F) B + J (join + runs N / places)
 // with B the blocks of a place, F the part of a tile's rows that exist, J whether
@@ -258,6 +258,10 @@ KV_HD inline int kv_tree_longer(const KvPlan& p, int c, int runs) {
 //   8 of 16000,                  104          150    114   95.2    102    107
 //   32 of 2000,                  200          131    145    125   89.1   80.0
 //   8 of 16000,                  384                 324           311    261
+// and of D 256, tiles of 16, 32 and 128:
+//   8 of 500,                    104         23.3   17.5          39.2
+//   8 of 8000,                   104          152    105           136
+//   32 of 500,                   200          140    106          83.0
 // A binary32 output of D 128 does not fit 64 rows' registers (8 of 16000, 64 rows:
 // 85.9 us spilling, 76.0 with 32).
 struct KvForm {
@@ -270,9 +274,10 @@ inline int kv_tree_forms(int D, const KvForm** forms) {
   static const KvForm d128[] = {{16, 2, 64, 1.0, 4.6, .249, 0, .8, 12.8}, {32, 1, 32, 2.1, 6.3, .208, 0, 4.2, 2.7},
                                 {64, 1, 32, 1.1, 9.7, .318, 0, 2.9, 5.6}, {128, 2, 32, 0, 4.8, .868, .342, 5.7, 19.6},
                                 {256, 1, 32, 0, 8.5, .519, .555, 4.4, 15.6}};
-  static const KvForm d256[] = {{16, 1, 64, 3.1, 6.2, .264, 0, 3.6, 6.4}, {128, 1, 32, 0, 13.1, 1.55, .125, 2.9, 19.0}};
+  static const KvForm d256[] = {{16, 1, 64, 2.8, 6.1, .270, 0, 5.1, 4.0}, {32, 1, 32, 2.1, 8.9, .359, 0, 3.0, 6.2},
+                                {128, 1, 32, 0, 12.6, 1.51, .186, 3.7, 16.3}};
   *forms = D == 64 ? d64 : D == 128 ? d128 : d256;
-  return D == 64 ? 4 : D == 128 ? 5 : 2;
+  return D == 64 ? 4 : D == 128 ? 5 : 3;
 }
 // The shortest run: four blocks a wave make up for what a run costs beside its
 // blocks; a tile for many rows has large partials, and short runs only where few

@@ -297,8 +297,10 @@ FORMS = [
     (16, 4, 128, 64, _batch(2, 32, 4000), None),
     (16, 8, 128, 64, _batch(16, 60, 200), None),
     (8, 8, 128, 64, _batch(16, 40, 2100), None),
-    (8, 4, 256, 32, _batch(32, 25, 64), None),
-    (8, 4, 256, 64, _batch(32, 60, 1100), 1100),
+    (32, 8, 256, 32, _batch(12, 25, 64), None),
+    (32, 8, 256, 64, _batch(32, 25, 1100), 1100),
+    (16, 8, 256, 32, _batch(12, 25, 64), None),
+    (4, 4, 256, 64, _batch(12, 20, 4000), None),
     (1, 1, 256, 32, [(1, 64)], None),
     (1, 1, 256, 64, [(1, 2100)], None),
     (8, 1, 256, 64, _batch(12, 5, 2100), None),

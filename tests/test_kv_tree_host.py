@@ -241,7 +241,7 @@ def test_tree_plans_hold_any_lengths(host, D, cus):
         p = _plan(host, Hq, Hkv, D, batch, max_q, max_kv, f32, cus)
         assert p["items"] == batch * Hkv * p["tiles"] and p["tiles"] * p["rows"] >= max_q * Hq // Hkv
         assert p["items"] >= 1 << 23 or p["slots"] * 512 < 1 << 32
-        assert p["rows"] in {64: (16, 32, 64, 128), 128: (16, 32, 128, 256) if f32 else (16, 32, 64, 128, 256), 256: (16, 128)}[D]
+        assert p["rows"] in {64: (16, 32, 64, 128), 128: (16, 32, 128, 256) if f32 else (16, 32, 64, 128, 256), 256: (16, 32, 128)}[D]
         if p["slots"] == p["items"]:
             assert p["ws_bytes"] == 0 or batch > 512
             continue
@@ -284,7 +284,7 @@ def test_gpu_tests_reach_every_form(host):
         for f32 in (0, 1):
             p = _plan(host, Hq, Hkv, D, len(shape), max(n for n, _ in shape), max_kv or width, f32, 256)
             seen.add((D, p["rows"], p["slots"] > p["items"], p["join_rows"] > 0 if p["slots"] > p["items"] else None))
-    several = {(D, n, True) for D, rows in ((64, (16, 32, 64, 128)), (128, (16, 32, 64, 128, 256)), (256, (16, 128))) for n in rows}
+    several = {(D, n, True) for D, rows in ((64, (16, 32, 64, 128)), (128, (16, 32, 64, 128, 256)), (256, (16, 32, 128))) for n in rows}
     one = {(D, n, False) for D, n, _ in several} - {(128, 32, False)}
     assert {x[:3] for x in seen} >= one | several - {(128, 128, True)}  # one run of 32, several of 128: only larger calls
     assert {x[3] for x in seen} == {None, False, True}
