@@ -530,6 +530,12 @@ __device__ inline void store_out(void* out, int64_t at, const float (&v)[N]) {
 // one after the other) and the waves' join (3 us). A ragged batch (64 sequences
 // up to 8192 tokens, 36 us for 18 of bytes) waits for its last runs: vector units
 // are busy 43 % of the cycles, matrix units 7 %.
+//
+// With a tree an item is a tile of 16 NT rows of a sequence's head, and any number
+// of rows comes here while the call is small. Unpacking a block is then shared by
+// all of the tile's rows; softmax is not. A block takes a workgroup of D 128, as
+// fitted to measured times, 0.25 us (16 rows, two workgroups a CU), 0.21 (32, one)
+// or 0.32 (64, one): the taller tile does more rows for less.
 constexpr int kWaves = kKvWaves;
 
 template <int D>
@@ -889,6 +895,9 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
 // vector units 50 % of the cycles, at 1.9 GHz of 2.4: power seems to hold the clock.
 // Binary32 out, which has twice the value products: 1394 us. D 64: 708 (binary32
 // 883), D 256 with half the heads: 1552 (1850), one block a tile there.
+// With a tree: 16 x 64 nodes of 64 heads (8 kv heads, D 128) on 8192 tokens in 292
+// us with the join, 0.93 PFLOP/s; 48 nodes of 96 heads on 131072, binary32 out,
+// 491 to 502, of 271 for the products and 406 with the second part of the weights.
 template <int D, int W, bool F32, bool TREE>
 __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel(KvAttendArgs a) {
   constexpr int KB = W * 64 / D;   // blocks of a tile
@@ -1179,7 +1188,7 @@ __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel
 // thread adds up four channels of a row over every S-th run, in order, and the
 // S sums of a row meet in LDS. One row a workgroup (S = 2048 / D) where the call
 // has few, so that many runs do not queue; a full workgroup of rows otherwise.
-// Latency-bound: 4.2 to 7 us, of which the launch is 2; a join by the last
+// Latency-bound: 4 to 8 us, of which the launch is 2; a join by the last
 // workgroup of an item instead would need fences and counters to be cleared.
 constexpr int kJoinThreads = 512;
 

@@ -902,7 +902,7 @@ def test_calls_at_once_on_streams():
     qs = [r.standard_normal((2 * n, Hq, D)).astype(np.float16) for _ in range(2)]
     dq = [_dev(x) for x in qs]
     outs = [_full((2 * n, Hq, D), "float32") for _ in range(2)]
-    ws = [kv.workspace(2, n, 3072) for _ in range(2)]
+    ws = [kv.workspace(2, n, 4096) for _ in range(2)]
     problems = [_verify_problem(30 + i, [30] * 12, 20011, True, "mixed", gap=1.5) for i in range(2)]
     dev = [{k: _dev(x[k]) for k in ("token", "p", "q", "u")} | dict(parent=_i32(x["parent"]), starts=_i32(x["starts"])) for x in problems]
     got = [(_full((360,), "int32"), _full((12,), "int32"), _full((12,), "int64")) for _ in range(2)]
