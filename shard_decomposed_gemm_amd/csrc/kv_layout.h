@@ -245,7 +245,7 @@ KV_HD inline int kv_tree_longer(const KvPlan& p, int c, int runs) {
 // former start fast and need no barrier, and the more rows unpack a block once
 // the better; the latter unpack it once for four or eight waves. Which is faster
 // follows from the work of a place (a workgroup that runs at once with others), by
-// a model fitted to 700 shapes with 8 kv heads (1 to 32 sequences of 200 to 32000
+// a model fitted to measured shapes with 8 kv heads (1 to 32 sequences of 200 to 32000
 // tokens, 24 to 512 rows a kv head):
 //   us = first + round max(1, items / places) + (block + full F) B + J (join + runs N / places)
 // with B the blocks of a place, F the part of a tile's rows that exist, J whether
