@@ -254,15 +254,17 @@ typedef struct {
  * distributed as the target's are. At a node, from node 0 on, its children c are
  * tried in their order. With x = token[c], and for the first child w = p, d = q:
  * c is accepted if u[c] d(x) < w(x), and the walk goes on from it; else w becomes
- * max(0, w - d), normalised, and d loses x and is normalised (a whole row of p or
- * q counts as a sum of 1). Without q, d is 1 at x and 0 elsewhere for each child. Where no child is accepted (or none is
+ * max(0, w - d), normalised, and d loses x and is normalised, by the sum of what is
+ * left of the row (only a whole row of p or q counts as a sum of 1). Without q, d is
+ * 1 at x and 0 elsewhere for each child. Where no child is accepted (or none is
  * there) the walk ends, and next is the smallest token t with
  *   sum_{s <= t} w(s) > u[node 0] sum_s w(s).
  * A child whose token an earlier one of the same parent had is passed over, and so
- * are those behind children that had all of d or left w 0 everywhere; next is
- * drawn from p then.
+ * are those behind children that left w 0 everywhere (next is drawn from p then) or
+ * had all of d: 2^-57 of it a token of the vocabulary counts as nothing.
  * In 64 bits; the weights w of the sums as multiples of 2^-50, whose sums are
- * exact below 8 in any order: equal calls give equal results however they are
+ * exact below 8 in any order, and d's in two parts, as a multiple of 2^-50 and
+ * the rest as one of 2^-76: equal calls give equal results however they are
  * split. Entries of p, q outside 0..1 count as the nearer end, NaN as 0; so does u,
  * its upper end the largest number below 1.
  * A sequence without rows has count 0 and next -1. Reported by kvc_check: a

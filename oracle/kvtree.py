@@ -83,8 +83,10 @@ def verify(token, parent, p, q, u):
                 draft = np.zeros(vocab)
                 draft[x] = 1.0
             else:
-                mass = 1.0 - sum(unit(q[cur])[t] for t in tried)
-                if not mass > 0:
+                mass = 1.0  # a whole row counts as 1
+                if tried:
+                    mass = d.sum()
+                if not mass > vocab * 2.0 ** -57:
                     continue
                 draft = d / mass
             tried.append(x)

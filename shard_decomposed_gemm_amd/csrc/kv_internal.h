@@ -81,13 +81,14 @@ struct KvTreeArgs {
   uint64_t* err;  // kv_report.h
 };
 
-// How far a sequence's verification has come (kv_verify.hip says what A, S and Z are).
+// How far a sequence's verification has come (kv_verify.hip says what A, Z and D are).
 struct KvWalk {
-  double A, S, Z;
+  double A, Z, D;
+  double coarse, fine;     // D in two parts; as long as the row's sum is not known, less that
   int32_t node, last;      // where it is, the child tried last
   int32_t count, rejects;  // accepted nodes, tokens rejected at the last of them (without q)
-  int32_t pending, wants;  // Z is out of date; the walk needs it to go on (else it has ended)
-  int32_t done, unused;
+  int32_t pending, wants;  // Z and D are out of date; the walk needs it to go on (else it has ended)
+  int32_t done, known;     // known: q's sum of the row is in D's parts
 };
 // A line of its own: workgroups of all XCDs count in it.
 struct KvVerifyState {
@@ -111,7 +112,7 @@ struct KvVerifyArgs {
   int64_t* next;
   KvVerifyPlan plan;
   KvVerifyState* states;  // batch
-  double* sums;           // batch x segments of all parts
+  double* sums;           // batch x kKvSums x segments of all parts
   int64_t patience;       // ticks of the wall clock that a workgroup of the rounds waits for the others
   uint64_t* err;  // kv_report.h
 };

@@ -406,12 +406,14 @@ inline KvVerifyPlan kv_verify_plan(int64_t batch, int64_t vocab, bool drawn, int
   p.rounds = drawn && max_children > 1;
   return p;
 }
-inline int64_t kv_verify_bytes(const KvVerifyPlan& p, int64_t batch) { return batch * ((int64_t)p.parts * 32 + kKvStateBytes); }
+constexpr int kKvSums = 3;  // of a segment, a quarter of a part: the weights, and q in two parts
+constexpr int kKvPartBytes = 4 * kKvSums * 8;
+inline int64_t kv_verify_bytes(const KvVerifyPlan& p, int64_t batch) { return batch * ((int64_t)p.parts * kKvPartBytes + kKvStateBytes); }
 // Bytes for every verification of up to `batch` sequences and `vocab` tokens.
 inline int64_t kv_verify_bound(int64_t batch, int64_t vocab, int num_cus) {
   const int64_t most = (vocab + 2047) / 2048 < kKvParts ? (vocab + 2047) / 2048 : kKvParts, all = batch * most;
   const int64_t some = batch * ((vocab + 16383) / 16384 + 1) + 4 * num_cus;
-  return (some < all ? some : all) * 32 + batch * kKvStateBytes;
+  return (some < all ? some : all) * kKvPartBytes + batch * kKvStateBytes;
 }
 
 }  // namespace agemm

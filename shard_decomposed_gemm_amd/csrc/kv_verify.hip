@@ -3,16 +3,26 @@
 // At a node, after j rejected children of the draft q without replacement, the
 // weights are w_j = max(0, w_{j-1} - c_j q_j) with q_j what is left of q,
 // normalised, and c_j = sum w_{j-1}. As every term takes a multiple of q off, all
-// of it is one number: w = max(0, p - A q) with A = sum_j Z_{j-1} / (1 - S_{j-1}),
-// Z the sum of w and S the q of the rejected tokens. (A rejected token x has
-// w(x) = 0 from then on: u q_j(x) Z >= w(x) with u < 1 makes the difference
+// of it is one number: w = max(0, p - A q) with A = sum_j Z_{j-1} / D_{j-1},
+// Z the sum of w and D that of q without the rejected tokens. (A rejected token x
+// has w(x) = 0 from then on: u q_j(x) Z >= w(x) with u < 1 makes the difference
 // negative.) So a child is held against three numbers, and only another child
-// after a rejection needs a pass over the vocabulary, for Z; without q not even
-// that: Z = 1 - the p of the rejected ones.
+// after a rejection needs a pass over the vocabulary, for Z and D; without q not
+// even that: Z = 1 - the p of the rejected ones.
 //
 // Weights are taken to multiples of 2^-50 (by adding and taking off 4, whose
 // neighbours lie that far apart), so that sums in binary64 are exact up to 8 and
 // do not depend on how the vocabulary is split.
+//
+// D divides, and a draft sure of its first token leaves little of it: 1 less the
+// rejected q would be off by the binary32 roundings of the whole row (with 2^-23
+// left, by a third of it), and 2^-50 is coarse for it too. So q is summed, as a
+// multiple of 2^-50 and what that is off by as one of 2^-76, exactly both (of up to
+// 2^28 numbers, the latter are below 2^-23 together), once a row, and the rejected
+// tokens are taken off in the same two parts. D is off by 2^-77 a token then; below 2^-57 a
+// token, where that might be a millionth of it, it counts as nothing. (To pass
+// over the drafts that follow leaves the distribution as it is: the rest is drawn
+// from w.)
 //
 // Where no sum but the last is expected, the workgroups of a row's parts each walk
 // by themselves and sum, and a second kernel draws. Else one workgroup a sequence
@@ -61,6 +71,16 @@ __device__ inline double weight(double A, float p, float q) {
   w = w > 0.0 ? w : 0.0;
   return (w + kGrid) - kGrid;
 }
+
+struct Parts {
+  double coarse, fine;
+};
+__device__ inline Parts parts_of(float q) {
+  constexpr double kFine = 0x1.8p-24;  // its neighbours are 2^-76 apart, on both sides
+  const double x = unit(q), coarse = (x + kGrid) - kGrid;
+  return {coarse, ((x - coarse) + kFine) - kFine};
+}
+constexpr double kLeast = 0x1p-57;  // of what is left of q, times the vocabulary
 
 struct Rows {
   int64_t row0;
@@ -126,7 +146,7 @@ __device__ inline void go_on(Shared& s, KvWalk w, int n, int lane) {
     const int l = c & 63, x = __builtin_amdgcn_readlane(token, l);
     bool again = x < 0 || __any(lane < l && parent == w.node && token == x);
     for (int i = (w.node & ~63) + lane; i < base && !again; i += 64) again = __any(s.parent[i] == w.node && s.token[i] == x);
-    if (again || (DRAWN && !(w.S < 1.0)) || (!w.pending && !(w.Z > 0.0))) {
+    if (again || (!w.pending && !(w.Z > 0.0 && w.D > 0.0))) {
       w.last = c;
       continue;
     }
@@ -139,10 +159,12 @@ __device__ inline void go_on(Shared& s, KvWalk w, int n, int lane) {
     bool take;
     if constexpr (DRAWN) {
       const double q = number_of(nq, l), left = __builtin_fma(-w.A, q, p);
-      take = u * q * w.Z < (left > 0.0 ? left : 0.0) * (1.0 - w.S);
+      take = u * q * w.Z < (left > 0.0 ? left : 0.0) * w.D;
       if (!take) {
-        w.A += w.Z / (1.0 - w.S);
-        w.S += q;
+        const Parts x = parts_of((float)q);
+        w.A += w.Z / w.D;
+        w.coarse -= x.coarse;
+        w.fine -= x.fine;
         w.pending = 1;
       }
     } else {
@@ -157,9 +179,9 @@ __device__ inline void go_on(Shared& s, KvWalk w, int n, int lane) {
       if (lane == 0) s.path[w.count] = c;
       ++w.count;
       w.node = c;
-      w.rejects = w.pending = 0;
-      w.A = w.S = 0.0;
-      w.Z = 1.0;
+      w.rejects = w.pending = w.known = 0;
+      w.A = w.coarse = w.fine = 0.0;
+      w.Z = w.D = 1.0;
     }
   }
   if (lane == 0) s.walk = __builtin_bit_cast(KvWalkWords, w);
@@ -208,7 +230,7 @@ __device__ inline bool begin(const KvVerifyArgs& a, int b, Shared& s, bool keeps
   load_tree<DRAWN>(a, r, s, keeps);
   if (tid == 0) s.path[0] = 0;
   __syncthreads();
-  if (tid < 64) go_on<DRAWN>(s, KvWalk{0.0, 0.0, 1.0, 0, 0, 1, 0, 0, 0, 0, 0}, r.n, tid);
+  if (tid < 64) go_on<DRAWN>(s, KvWalk{0.0, 1.0, 1.0, 0.0, 0.0, 0, 0, 1, 0, 0, 0, 0, 0}, r.n, tid);
   __syncthreads();
   if (keeps) {
     const KvWalk w = __builtin_bit_cast(KvWalk, s.walk);
@@ -220,18 +242,33 @@ __device__ inline bool begin(const KvVerifyArgs& a, int b, Shared& s, bool keeps
   return true;
 }
 
-// A wave's sum of the weights of tokens t0 .. t1 - 1 of a row, and of the lanes' `sum`.
-template <bool DRAWN>
-__device__ inline double sum_segment(const float* p, const float* q, double A, int t0, int t1, int lane, double sum) {
+// A wave's sums of tokens t0 .. t1 - 1 of a row: of the weights and the lanes' `sum`; with REST of q too.
+struct Sums {
+  double x[kKvSums];
+  __device__ double of(int k) const { return k == 0 ? x[0] : k == 1 ? x[1] : x[2]; }
+};
+template <bool DRAWN, bool REST>
+__device__ inline Sums sum_segment(const float* p, const float* q, double A, int t0, int t1, int lane, double sum) {
+  Sums s = {{sum, 0.0, 0.0}};
+  auto add = [&](float x, float y) {
+    s.x[0] += weight<DRAWN>(A, x, y);
+    if constexpr (REST) {
+      const Parts z = parts_of(y);
+      s.x[1] += z.coarse;
+      s.x[2] += z.fine;
+    }
+  };
   int t = t0 + 4 * lane;
 #pragma unroll 4
   for (; t + 4 <= t1; t += 256) {
     const float4v x = reinterpret_cast<const Quad*>(p + t)->x, y = DRAWN ? reinterpret_cast<const Quad*>(q + t)->x : x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum += weight<DRAWN>(A, x[i], y[i]);
+    for (int i = 0; i < 4; ++i) add(x[i], y[i]);
   }
-  for (; t < t1; ++t) sum += weight<DRAWN>(A, p[t], q[t]);
-  return wave_sum(sum);
+  for (; t < t1; ++t) add(p[t], q[t]);
+#pragma unroll
+  for (int k = 0; k < (REST ? kKvSums : 1); ++k) s.x[k] = wave_sum(s.x[k]);
+  return s;
 }
 
 __device__ inline double load_sum(const double* p) {
@@ -255,25 +292,44 @@ struct Row {
     const int64_t t = (int64_t)i * segment;
     return t < vocab ? (int)t : vocab;
   }
-  __device__ double sum(int i, int lane, double start = 0.0) const { return sum_segment<DRAWN>(p, q, A, first(i), first(i + 1), lane, start); }
+  // `rest`: of q too (what the walk wants to go on)
+  __device__ Sums sum(int i, int lane, bool rest, double start = 0.0) const {
+    if constexpr (DRAWN)
+      if (rest) return sum_segment<true, true>(p, q, A, first(i), first(i + 1), lane, start);
+    return sum_segment<DRAWN, false>(p, q, A, first(i), first(i + 1), lane, start);
+  }
 };
 
 struct Meeting {
-  double sums[kKvParts * kSegments];  // of the segments of all parts
-  double waves[kSegments];
+  double sums[kKvSums][kKvParts * kSegments];  // of the segments of all parts
+  double waves[kKvSums][kSegments];
   int found, told;
 };
-__device__ inline double total_of(const Meeting& m, int segments) {  // the same in all waves
+__device__ inline double total_of(const Meeting& m, int segments, int k = 0) {  // the same in all waves
   double x = 0.0;
-  for (int i = threadIdx.x & 63; i < segments; i += 64) x += m.sums[i];
+  for (int i = threadIdx.x & 63; i < segments; i += 64) x += m.sums[k][i];
   return wave_sum(x);
 }
+// The walk wants q's sum: once a row, as the rejected tokens' q comes off it.
+__device__ inline bool wants_rest(const KvWalk& w) { return w.wants && !w.known; }
+// The sums that the walk wanted are there.
+__device__ inline void has_sums(KvWalk& w, const Meeting& m, int segments, int vocab) {
+  w.Z = total_of(m, segments);
+  if (!w.known) {
+    w.coarse += total_of(m, segments, 1);
+    w.fine += total_of(m, segments, 2);
+    w.known = 1;
+  }
+  w.D = w.coarse + w.fine;
+  if (!(w.D > vocab * kLeast)) w.D = 0.0;
+  w.pending = 0;
+}
 template <bool DRAWN>
-__device__ inline void sum_all(Meeting& m, const Row<DRAWN>& row, int segments) {
+__device__ inline void sum_all(Meeting& m, const Row<DRAWN>& row, int segments, bool rest) {
   const int lane = threadIdx.x & 63;
   for (int i = threadIdx.x >> 6; i < segments; i += kSegments) {
-    const double x = row.sum(i, lane);
-    if (lane == 0) m.sums[i] = x;
+    const Sums s = row.sum(i, lane, rest);
+    if (lane < (rest ? kKvSums : 1)) m.sums[lane][i] = s.of(lane);
   }
   __syncthreads();
 }
@@ -292,7 +348,7 @@ __device__ inline void draw(const KvVerifyArgs& a, int b, Shared& s, Meeting& m,
     rejects = 0;
     __syncthreads();
     row = Row<DRAWN>(a, row0, w);
-    sum_all(m, row, segments);
+    sum_all(m, row, segments, false);
     all = total_of(m, segments);
   }
   constexpr int kNone = 0x7fffffff;
@@ -307,7 +363,7 @@ __device__ inline void draw(const KvVerifyArgs& a, int b, Shared& s, Meeting& m,
       double own = 0.0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = 4 * lane + i < segments ? m.sums[4 * lane + i] : 0.0;
+        v[i] = 4 * lane + i < segments ? m.sums[0][4 * lane + i] : 0.0;
         own += v[i];
       }
       double run = sum_up_to(own) - own, before = 0.0;  // exact where all sums are
@@ -327,8 +383,8 @@ __device__ inline void draw(const KvVerifyArgs& a, int b, Shared& s, Meeting& m,
         below = lane_of(before, l);
       } else {  // only by rounding, where sums are not exact: the last one with a weight
         for (int i = 0; i < segments; ++i)
-          if (m.sums[i] > 0.0) at = i;
-        for (int i = 0; i < at; ++i) below += m.sums[i];
+          if (m.sums[0][i] > 0.0) at = i;
+        for (int i = 0; i < at; ++i) below += m.sums[0][i];
       }
     }
     // Then the first token. Rejected ones of the segment are left out.
@@ -377,14 +433,14 @@ __device__ inline void draw(const KvVerifyArgs& a, int b, Shared& s, Meeting& m,
         own += v[i];
       }
       const double upto = sum_up_to(own);
-      if (lane == 63) m.waves[wave] = upto;
+      if (lane == 63) m.waves[0][wave] = upto;
       if (tid == 0) m.found = kNone;
       __syncthreads();
       double run = below + (upto - own);
 #pragma unroll
       for (int i = 0; i < kSegments; ++i) {
-        if (i < wave) run += m.waves[i];
-        below += m.waves[i];
+        if (i < wave) run += m.waves[0][i];
+        below += m.waves[0][i];
       }
       int hit = kNone;
 #pragma unroll
@@ -454,27 +510,36 @@ __global__ __launch_bounds__(kThreads) void kv_verify_rounds_kernel(KvVerifyArgs
   const int n = a.q_start[b + 1] - (int)row0;
   const float u0 = a.u[row0];
   load_tree<DRAWN>(a, Rows{row0, n, true}, s, false);
-  double* sums = a.sums + (int64_t)b * segments;
+  double* sums = a.sums + (int64_t)b * kKvSums * segments;
   for (uint32_t turn = 1;; ++turn) {
     const Row<DRAWN> row(a, row0, w);
-    const double mine = row.sum(part * kSegments + wave, lane);
-    if (lane == 0) m.waves[wave] = mine;
+    const Sums mine = row.sum(part * kSegments + wave, lane, wants_rest(w));
+    const int kinds = wants_rest(w) ? kKvSums : 1;
+    if (lane < kinds) m.waves[lane][wave] = mine.of(lane);
     __syncthreads();
     if (wave == 0) {
-      if (lane < kSegments) store_sum(sums + part * kSegments + lane, m.waves[lane]);
+      const int k = lane / kSegments, i = lane % kSegments;
+      if (k < kinds) store_sum(sums + k * segments + part * kSegments + i, m.waves[k][i]);
       stores_are_there();
       if (lane == 0) m.found = __hip_atomic_fetch_add(&state.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == a.plan.parts * turn;
     }
     __syncthreads();
     if (m.found) {  // the last one
-      if (tid < segments) m.sums[tid] = load_sum(sums + tid);
+      if (tid < segments) {
+        double x[kKvSums];
+#pragma unroll
+        for (int k = 0; k < kKvSums; ++k)  // all on their way at once
+          if (k < kinds) x[k] = load_sum(sums + k * segments + tid);
+#pragma unroll
+        for (int k = 0; k < kKvSums; ++k)
+          if (k < kinds) m.sums[k][tid] = x[k];
+      }
       __syncthreads();
       if (!w.wants) {
         draw<DRAWN>(a, b, s, m, w, row, row0, n, u0, true);
         return;
       }
-      w.Z = total_of(m, segments);
-      w.pending = 0;
+      has_sums(w, m, segments, a.vocab);
       if (wave == 0) {
         go_on<DRAWN>(s, w, n, lane);
         if (lane < kWords)
@@ -524,8 +589,9 @@ __global__ __launch_bounds__(kThreads) void kv_verify_sum_kernel(KvVerifyArgs a)
       const int node = s.path[w.count + k], t = s.token[node];
       if (t >= row.first(i) && t < row.first(i + 1)) start -= weight<false>(0.0, s.p[node], 0.f);
     }
-  const double mine = row.sum(i, lane, start);
-  if (lane == 0) a.sums[(int64_t)b * a.plan.parts * kSegments + i] = mine;
+  const Sums mine = row.sum(i, lane, wants_rest(w), start);
+  const int segments = a.plan.parts * kSegments;
+  if (lane < (wants_rest(w) ? kKvSums : 1)) a.sums[((int64_t)b * kKvSums + lane) * segments + i] = mine.of(lane);
 }
 // SUMMED: the sums that the walk wants are there; else only what the rounds left is
 // to do. Latency-bound: 3.8 us for a chain, 5.8 for 64, 4.6 with nothing left.
@@ -538,7 +604,8 @@ __global__ __launch_bounds__(kThreads) void kv_verify_draw_kernel(KvVerifyArgs a
   const Rows r = rows_of(a, b);
   const int64_t row0 = r.row0;
   const int n = r.n;
-  if (SUMMED && tid < segments) m.sums[tid] = a.sums[(int64_t)b * segments + tid];
+  const double* sums = a.sums + (int64_t)b * kKvSums * segments + tid;
+  if (SUMMED && tid < segments) m.sums[0][tid] = *sums;
   int known[kKvNodes / kThreads];
   if constexpr (!DRAWN) {
 #pragma unroll
@@ -549,6 +616,8 @@ __global__ __launch_bounds__(kThreads) void kv_verify_draw_kernel(KvVerifyArgs a
   Row<DRAWN> row(a, row0, w);
   const float u0 = a.u[row0];
   const bool tree = !SUMMED || w.wants;
+  if (SUMMED && wants_rest(w) && tid < segments)
+    for (int k = 1; k < kKvSums; ++k) m.sums[k][tid] = sums[k * segments];
   if (tree) {
     load_tree<DRAWN>(a, Rows{row0, n, true}, s, false);
   } else if constexpr (!DRAWN) {
@@ -559,16 +628,15 @@ __global__ __launch_bounds__(kThreads) void kv_verify_draw_kernel(KvVerifyArgs a
     }
   }
   __syncthreads();
-  if (!SUMMED) sum_all(m, row, segments);
+  if (!SUMMED) sum_all(m, row, segments, wants_rest(w));
   while (w.wants) {
-    w.Z = total_of(m, segments);
-    w.pending = 0;
+    has_sums(w, m, segments, a.vocab);
     __syncthreads();
     if (tid < 64) go_on<DRAWN>(s, w, n, tid);
     __syncthreads();
     w = __builtin_bit_cast(KvWalk, s.walk);
     row = Row<DRAWN>(a, row0, w);
-    sum_all(m, row, segments);
+    sum_all(m, row, segments, wants_rest(w));
   }
   draw<DRAWN>(a, b, s, m, w, row, row0, n, u0, tree);
 }
