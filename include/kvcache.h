@@ -168,7 +168,8 @@ int kvc_attend(kvc_ctx* ctx, const void* pages, const kvc_attend_args* args, voi
 /* Workspace that holds every kvc_attend and kvc_attend_tree call of up to `batch` sequences, max_q
  * queries and max_kv tokens (any out type): one made for a server's largest
  * batch, chunk and length serves its smaller calls too, which may need more
- * than the largest one does. */
+ * than the largest one does. (It is the larger of what calls without and with
+ * trees need, at most some two times the former.) */
 int kvc_attend_workspace(const kvc_ctx* ctx, int32_t batch, int32_t max_q, int64_t max_kv, int64_t* bytes);
 
 /* A step with drafted tokens. The tokens of a sequence's step form a tree of up

@@ -286,13 +286,16 @@ inline int kv_tree_forms(int D, const KvForm** forms) {
 // and 37.4 in one run).
 inline int kv_tree_least(int rows, int64_t items, int64_t places) { return rows < 128 ? 32 : items * 8 <= places ? 8 : 16; }
 
-// Runs of an item at most, and partials that items of several runs leave.
+// Runs of an item at most, and partials that items of several runs leave: such an
+// item has more than c blocks, so that there are fewer than U / c <= places of them,
+// and their runs, each less than its blocks / c + 1, are fewer than twice that.
 inline int64_t kv_tree_most_runs(int64_t nblk, int64_t least) {
   const int64_t runs = (nblk + least - 1) / least;
   return runs < kKvMaxSplits ? runs : kKvMaxSplits;
 }
 inline int64_t kv_tree_partials(int64_t items, int64_t runs, int64_t places) {
-  return items < 2 * places && items * runs < 2 * places ? items * runs : 2 * places;
+  const int64_t most = places + (items < places ? items : places);
+  return items < most && items * runs < most ? items * runs : most;
 }
 
 inline KvPlan kv_tree_plan_as(const KvForm& f, const KvLayout& L, int64_t batch, int64_t max_q, int64_t max_kv, int num_cus) {
@@ -342,7 +345,7 @@ inline KvPlan kv_tree_plan(const KvLayout& L, int64_t batch, int64_t max_q, int6
   double least = 0;
   for (int i = 0; i < n; ++i) {
     if (forms[i].rows >= 128 && rows <= 32) break;  // their partials would be the most of a decoder's workspace
-    if (forms[i].rows == 64 && L.D == 128 && out_f32) continue;
+    if (forms[i].rows == 64 && (rows <= 32 || (L.D == 128 && out_f32))) continue;
     const KvPlan p = kv_tree_plan_as(forms[i], L, batch, max_q, max_kv, num_cus);
     const double us = kv_tree_us(forms[i], p, rows, nblk);
     if (i == 0 || us < least) best = p, least = us;
@@ -358,7 +361,7 @@ inline int64_t kv_tree_bound(const KvLayout& L, int64_t batch, int64_t max_q, in
   for (int i = 0; i < n; ++i) {
     const KvForm& f = forms[i];
     if (f.rows >= 128 && rows <= 32) break;
-    if (nblk <= f.blocks) continue;
+    if (nblk <= f.blocks || (f.rows == 64 && rows <= 32)) continue;
     const int64_t some = batch < kKvMaxBatch ? batch : kKvMaxBatch, places = (int64_t)num_cus * f.places_per_cu;
     const int64_t items = some * L.Hkv * ((rows + f.rows - 1) / f.rows);
     const int64_t need = kv_tree_partials(items, kv_tree_most_runs(nblk, f.rows < 128 ? 32 : 8), places) * f.rows * (L.D + 2) * 4 + 16 +
