@@ -222,9 +222,9 @@ int kvc_tree(kvc_ctx* ctx, const kvc_tree_args* args, void* stream);
 /* kvc_attend (causal = 1) with a tree: query i of a sequence sees the first q_off
  * of its cached tokens, and token q_off + j where bit j of row i of `mask` is set
  * (no token past kv_len; q_off NULL stands for kv_len - its queries). mask: T x
- * mask_words (1 .. 16), contiguous, device, as kvc_tree leaves it. The queries
- * need not be all of the tree's nodes: with q_off given, those of its last level
- * attend to what is cached of the others. Everything else as in kvc_attend; the
+ * mask_words (1 .. 16, and max_q up to 64 mask_words, as in kvc_tree), contiguous,
+ * device, as kvc_tree leaves it. The queries need not be all of the tree's nodes:
+ * with q_off given, those of its last level attend to what is cached of the others. Everything else as in kvc_attend; the
  * workspace too (kvc_attend_workspace). */
 int kvc_attend_tree(kvc_ctx* ctx, const void* pages, const kvc_attend_args* args, const uint64_t* mask,
                     int32_t mask_words, void* workspace, int64_t workspace_bytes, void* stream);

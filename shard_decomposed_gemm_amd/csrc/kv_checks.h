@@ -137,6 +137,7 @@ constexpr int64_t kKvMaxSequences = int64_t{1} << 20;  // of a call with trees: 
 inline int kv_check_mask(const kvc_attend_args* p, const uint64_t* mask, int32_t words, char* why) {
   if (!p) return kv_refuse(why, AGEMM_EINVAL, "args must be non-NULL");
   if (words < 1 || words > kKvMaskWords) return kv_refuse(why, AGEMM_EINVAL, "mask_words must be 1 to %d", kKvMaskWords);
+  if (p->max_q > 64 * words) return kv_refuse(why, AGEMM_EINVAL, "mask_words must hold max_q nodes");
   if (p->causal != 1) return kv_refuse(why, AGEMM_EINVAL, "causal must be 1 with a tree");
   if (p->batch > 0 && p->tokens > 0 && (!mask || !kv_natural(mask)))
     return kv_refuse(why, AGEMM_EINVAL, "mask must be non-NULL and aligned to its elements");
