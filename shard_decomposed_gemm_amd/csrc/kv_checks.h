@@ -223,6 +223,50 @@ inline int kv_check_commit(const KvLayout& L, void* const* pages, int32_t layers
   return AGEMM_OK;
 }
 
+// Arrays that kernels write while others read: `bytes` from `at` on, NULL for none.
+struct KvArray {
+  const char* name;
+  const void* at;
+  int64_t bytes;
+};
+// The first `outputs` arrays lie apart from the others and each other.
+inline int kv_check_apart(std::initializer_list<KvArray> arrays, int outputs, char* why) {
+  const KvArray* x = arrays.begin();
+  for (int i = 0; i < outputs; ++i)
+    for (int j = i + 1; j < (int)arrays.size(); ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(x[i].at), b = reinterpret_cast<uintptr_t>(x[j].at);
+      if (a && b && (a < b ? (int64_t)(b - a) < x[i].bytes : (int64_t)(a - b) < x[j].bytes) && x[i].bytes > 0 && x[j].bytes > 0)
+        return kv_refuse(why, AGEMM_EINVAL, "%s and %s must lie apart", x[i].name, x[j].name);
+    }
+  return AGEMM_OK;
+}
+inline int64_t kv_rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? ((rows - 1) * stride + width) * 4 : 0; }
+
+// Of calls that the checks above let pass.
+inline int kv_check_tree_apart(const kvc_tree_args* p, char* why) {
+  const int64_t T = p->tokens, B = p->batch;
+  return kv_check_apart({{"mask", p->mask, T * p->mask_words * 8}, {"positions", p->positions, T * 8}, {"slots", p->slots, T * 8},
+                         {"total_len", p->total_len, B * 4}, {"q_start", p->q_start, (B + 1) * 4}, {"kv_len", p->kv_len, B * 4},
+                         {"parent", p->parent, T * 4},
+                         {"page_table", p->slots ? p->page_table : nullptr, kv_rows_bytes(B, p->table_stride, p->table_width)}},
+                        4, why);
+}
+inline int kv_check_verify_apart(const kvc_verify_args* p, const void* workspace, int64_t need, char* why) {
+  const int64_t T = p->tokens, B = p->batch;
+  return kv_check_apart({{"workspace", workspace, need}, {"path", p->path, T * 4}, {"count", p->count, B * 4}, {"next", p->next, B * 8},
+                         {"q_start", p->q_start, (B + 1) * 4}, {"parent", p->parent, T * 4}, {"token", p->token, T * 8},
+                         {"u", p->u, T * 4}, {"p", p->p, kv_rows_bytes(T, p->p_stride, p->vocab)},
+                         {"q", p->q, kv_rows_bytes(T, p->q_stride, p->vocab)}},
+                        4, why);
+}
+inline int kv_check_commit_apart(const kvc_commit_args* p, char* why) {
+  const int64_t T = p->tokens, B = p->batch;
+  return kv_check_apart({{"new_len", p->new_len, B * 4}, {"q_start", p->q_start, (B + 1) * 4}, {"kv_len", p->kv_len, B * 4},
+                         {"path", p->path, T * 4}, {"count", p->count, B * 4},
+                         {"page_table", p->page_table, kv_rows_bytes(B, p->table_stride, p->table_width)}},
+                        1, why);
+}
+
 inline int kv_check_read(const void* pages, int64_t tokens, const int64_t* slots, const void* k_out, const void* v_out,
                          char* why) {
   if (tokens < 0) return kv_refuse(why, AGEMM_EINVAL, "tokens must not be negative");

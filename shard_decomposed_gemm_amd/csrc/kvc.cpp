@@ -230,7 +230,8 @@ int kvc_attend_tree(kvc_ctx* ctx, const void* pages, const kvc_attend_args* p, c
 int kvc_tree(kvc_ctx* ctx, const kvc_tree_args* p, void* stream) {
   if (!ctx) return AGEMM_EINVAL;
   char why[kKvWhy];
-  const int rc = kv_check_tree(p, why);
+  int rc = kv_check_tree(p, why);
+  if (!rc) rc = kv_check_tree_apart(p, why);
   if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);
 
   KvTreeArgs a{};
@@ -270,7 +271,8 @@ int kvc_verify(kvc_ctx* ctx, const kvc_verify_args* p, void* workspace, int64_t 
     plan = kv_verify_plan(p->batch, p->vocab, p->q != nullptr, p->max_children, ctx->num_cus);
   char why[kKvWhy];
   const int64_t need = p ? kv_verify_bytes(plan, p->batch) : 0;
-  const int rc = kv_check_verify(p, need, workspace, workspace_bytes, why);
+  int rc = kv_check_verify(p, need, workspace, workspace_bytes, why);
+  if (!rc) rc = kv_check_verify_apart(p, workspace, need, why);
   if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);
 
   KvVerifyArgs a{};
@@ -304,7 +306,8 @@ int kvc_verify(kvc_ctx* ctx, const kvc_verify_args* p, void* workspace, int64_t 
 int kvc_commit(kvc_ctx* ctx, void* const* pages, int32_t layers, const kvc_commit_args* p, void* stream) {
   if (!ctx) return AGEMM_EINVAL;
   char why[kKvWhy];
-  const int rc = kv_check_commit(ctx->L, pages, layers, p, why);
+  int rc = kv_check_commit(ctx->L, pages, layers, p, why);
+  if (!rc) rc = kv_check_commit_apart(p, why);
   if (rc) return rc == kKvNothing ? AGEMM_OK : fail(ctx, rc, "%s", why);
 
   KvCommitArgs a{};
