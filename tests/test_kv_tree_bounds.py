@@ -63,3 +63,27 @@ def test_partials_hold_items_just_longer_than_their_runs(host, D, cus):  # noqa:
             blocks[some] = r.integers(0, chunk + 1, int(some.sum()))
             blocks[~some] += chunk * r.integers(0, 4)
     assert full > 0.75
+
+
+def test_gpu_tests_reach_every_form_and_join(host):  # noqa: F811
+    """Every (D, rows of a tile, several runs, joined by waves, output type) that some 20000 random calls are planned as."""
+    from tests import test_gpu_kv_tree as one
+    from tests import test_gpu_kv_tree_forms as more
+
+    def form(Hq, Hkv, D, batch, max_q, max_kv, f32):
+        p = _plan(host, Hq, Hkv, D, batch, max_q, max_kv, f32, 256)
+        several = p["slots"] > p["items"]
+        return D, p["rows"], several, several and p["join_rows"] > 0, f32
+    reached = set()
+    for Hq, Hkv, D, page, shape, max_kv in one.FORMS + more.FORMS:
+        width = max(1, max(-(-n // page) for _, n in shape)) * page
+        for f32 in (0, 1):
+            reached.add(form(Hq, Hkv, D, len(shape), max(n for n, _ in shape), max_kv or width, f32))
+    r, missing = np.random.default_rng(0), {}
+    heads = [(64, 8), (96, 8), (8, 8), (1, 1), (12, 4), (32, 4), (16, 2), (40, 8), (24, 2), (32, 8), (16, 1), (64, 64)]
+    for _ in range(20000):
+        Hq, Hkv = heads[r.integers(len(heads))]
+        shape = (Hq, Hkv, (64, 128, 256)[r.integers(3)], *(int(np.exp(r.uniform(0, np.log(top)))) for top in (200, 100, 9000)), int(r.integers(2)))
+        if form(*shape) not in reached:
+            missing[form(*shape)] = shape
+    assert not missing
