@@ -390,8 +390,8 @@ struct KvVerifyPlan {
 constexpr int kKvParts = 64;   // at most
 constexpr int kKvStateBytes = 128;  // of a sequence: how far it has come, parts that are summed
 inline int64_t kv_verify_parts(int64_t batch, int64_t vocab, int num_cus) {
-  // Four workgroups a CU, of 2048 tokens at the least and 16384 at the most (the
-  // draw looks through a quarter of a part).
+  // Four workgroups a CU, of 2048 tokens at the least and, as far as 64 parts hold
+  // the vocabulary so, 16384 at the most (the draw looks through a quarter of a part).
   int64_t parts = (4 * num_cus + batch - 1) / (batch > 0 ? batch : 1), most = (vocab + 2047) / 2048;
   const int64_t least = (vocab + 16383) / 16384;
   parts = parts > least ? parts : least;

@@ -116,7 +116,9 @@ int kvc_create(kvc_ctx** out, int Hq, int Hkv, int D, int page_tokens, int64_t n
   if (e == hipSuccess) e = hipDeviceGetAttribute(&c->num_cus, hipDeviceAttributeMultiprocessorCount, c->device);
   int khz = 0;
   if (e == hipSuccess) e = hipDeviceGetAttribute(&khz, hipDeviceAttributeWallClockRate, c->device);
-  // Some ten times what a round takes. AGEMM_VERIFY_WAIT_US: a testing hook (0: no wait, the last kernel does it all).
+  // Some forty times what a round takes with parts of 2048 tokens. What a workgroup waits for is by how much the others end
+  // later, not a round: those of parts of 2^20 tokens (600 us) still go on by themselves. AGEMM_VERIFY_WAIT_US: a testing
+  // hook (0: no wait, the last kernel does it all).
   const char* wait = std::getenv("AGEMM_VERIFY_WAIT_US");
   const long us = wait ? std::strtol(wait, nullptr, 10) : 200;
   c->patience = (int64_t)(us < 0 ? 0 : us < 100000 ? us : 100000) * khz / 1000;
