@@ -43,8 +43,9 @@
  * context's device whichever is current. No call but kvc_create allocates,
  * and none synchronises, so all of them can be captured into a graph.
  * Calls of one context may run at the same time on several streams, as long
- * as each kvc_attend in flight has a workspace of its own, and no call reads
- * slots that another one writes. (The error text of kvc_last_error is per
+ * as each kvc_attend, kvc_attend_tree and kvc_verify in flight has a workspace of
+ * its own (two that share one mix their partials, sums and counters), and no call
+ * reads slots that another one writes. (The error text of kvc_last_error is per
  * context: use one context per host thread.)
  *
  * What only the device can see - page ids, lengths, positions, slots, values
@@ -186,7 +187,10 @@ int kvc_attend_workspace(const kvc_ctx* ctx, int32_t batch, int32_t max_q, int64
  *   kvc_commit       the path's keys and values go to places kv_len, kv_len + 1,
  *                    ..., in all layers; the lengths that the next step starts with.
  * Nothing of it needs the host, so a step can be captured into a graph. Up to
- * 2^20 sequences and 2^23 rows a call. */
+ * 2^20 sequences and 2^23 rows a call. q_start must ascend: where it descends, the
+ * sequence with a negative number of rows is reported, and what the outputs hold in
+ * rows that two sequences name, before q_start[0] and from q_start[batch] on is not
+ * said. */
 
 /* Arguments of kvc_tree. */
 typedef struct {
@@ -245,7 +249,10 @@ typedef struct {
   int64_t vocab;               /* 1 .. 2^28 */
   const float* u;              /* T, device: random numbers in [0, 1), one for each draft; node 0's is for the
                                   token at the end */
-  int32_t max_children;        /* the most children of one node to expect, >= 1: it only chooses how work is split */
+  int32_t max_children;        /* the most children of one node to expect, >= 1: it only chooses how work is split.
+                                  With q, 1 is for chains: trees get the same results, but one workgroup a sequence
+                                  for every sum (16 trees of 25 on 131072 tokens 147 to 476 us, 30 to 63 with what
+                                  they have) */
   int32_t* path;               /* T: the accepted nodes, node 0 first, then -1 */
   int32_t* count;              /* batch: their number */
   int64_t* next;               /* batch: the token that follows them */
@@ -264,9 +271,9 @@ typedef struct {
  * are those behind children that left w 0 everywhere (next is drawn from p then) or
  * had all of d: 2^-57 of it a token of the vocabulary counts as nothing.
  * In 64 bits; the weights w of the sums as multiples of 2^-50, whose sums are
- * exact below 8 in any order, and d's in two parts, as a multiple of 2^-50 and
- * the rest as one of 2^-76: equal calls give equal results however they are
- * split. Entries of p, q outside 0..1 count as the nearer end, NaN as 0; so does u,
+ * exact below 8 in any order (a token whose weight is 2^-51 or less has none, and
+ * is never drawn), and d's in two parts, as a multiple of 2^-50 and the rest as one
+ * of 2^-76: equal calls give equal results however they are split. Entries of p, q outside 0..1 count as the nearer end, NaN as 0; so does u,
  * its upper end the largest number below 1.
  * path, count, next and the workspace must lie apart from the inputs and each other.
  * A sequence without rows has count 0 and next -1. Reported by kvc_check: a
