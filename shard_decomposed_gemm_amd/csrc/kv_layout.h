@@ -246,12 +246,15 @@ KV_HD inline int kv_tree_longer(const KvPlan& p, int c, int runs) {
 // the better; the latter unpack it once for four or eight waves. Which is faster
 // follows from the work of a place (a workgroup that runs at once with others), by
 // a model fitted to measured shapes with 8 kv heads (1 to 32 sequences of 200 to 32000
-// tokens, 24 to 512 rows a kv head):
+// tokens, equally long, 24 to 512 rows a kv head, binary16 outputs):
 //   us = first + round max(1, items / places) + (block + full F) B + J (join + runs N / places)
 // with B the blocks of a place, F the part of a tile's rows that exist, J whether
 // items of several runs are joined, N the runs. Its choice takes 1.03 times the
-// best form's time on average (1.4 at worst). In us, of D 128, tiles of 16, 32,
-// 64, 128 and 256 rows:
+// best form's time on average (1.4 at worst). Outside that range, on 23 shapes of 1
+// to 20 kv heads, 60 to 8192 tokens and both outputs, 1.04 times (at worst 1.32: 24
+// trees of 25 on 4099 tokens, 32 heads on 4, D 64, 70 us in tiles of 128 rows, 54 in
+// tiles of 32; and 1.22: 4 of 16 on 4000, 16 on 1, D 128, binary32 out, 20 for 16).
+// In us, of D 128, tiles of 16, 32, 64, 128 and 256 rows:
 //   8 sequences of 500 tokens,    64 rows     9.8   12.2   16.0   19.5   17.4
 //   8 of 16000,                   64         87.7   70.1   61.4   88.7   99.0
 //   32 of 2000,                   64         47.7   48.2   37.7   53.1   55.3

@@ -486,9 +486,9 @@ __global__ __launch_bounds__(kThreads) void kv_verify_begin_kernel(KvVerifyArgs 
   begin<DRAWN>(a, blockIdx.x, s, true, row0);
 }
 
-// The rounds: 16 trees of 25 drawn nodes on 131072 tokens take 31 us a call where
-// no tree wants more than four sums and 60 where one wants ten, 4.7 a turn, nearly
-// all of it latency. What workgroups tell each other goes past the caches of their XCDs
+// The rounds: 16 trees of 25 drawn nodes on 131072 tokens take 33 to 37 us a call
+// where no tree wants more than four sums and 63 where one wants ten, 5.0 a turn, nearly
+// all of it latency (q's sum once a row is some 0.2 of it). What workgroups tell each other goes past the caches of their XCDs
 // (relaxed accesses at the device's scope), and is there before the counter or
 // turn that announces it: one wave stores and waits, which a release (the
 // write-back of all of the cache, 20 us a call of 1024 workgroups) would do too.
@@ -572,8 +572,8 @@ __global__ __launch_bounds__(kThreads) void kv_verify_rounds_kernel(KvVerifyArgs
 // Where the walk is expected to need no sum but the last: every part walks for
 // itself and sums, and a second kernel draws. (With a kernel that begins, and the
 // last part's workgroup drawing, 64 chains of 6 take 26 us, not 20.) Those chains,
-// on 131072 tokens, take 14.4 us here, the rows at 4.7 TB/s with the walk that
-// comes first; one chain on 32768 4.5, latency.
+// on 131072 tokens, take 13.8 us here, the rows at 4.9 TB/s with the walk that
+// comes first; one chain on 32768 4.6, latency.
 template <bool DRAWN>
 __global__ __launch_bounds__(kThreads) void kv_verify_sum_kernel(KvVerifyArgs a) {
   __shared__ Shared s;
@@ -594,7 +594,7 @@ __global__ __launch_bounds__(kThreads) void kv_verify_sum_kernel(KvVerifyArgs a)
   if (lane < (wants_rest(w) ? kKvSums : 1)) a.sums[((int64_t)b * kKvSums + lane) * segments + i] = mine.of(lane);
 }
 // SUMMED: the sums that the walk wants are there; else only what the rounds left is
-// to do. Latency-bound: 3.8 us for a chain, 5.8 for 64, 4.6 with nothing left.
+// to do. Latency-bound: 4.0 us for a chain, 6.2 for 64, 4.6 with nothing left.
 template <bool DRAWN, bool SUMMED>
 __global__ __launch_bounds__(kThreads) void kv_verify_draw_kernel(KvVerifyArgs a) {
   __shared__ Shared s;
