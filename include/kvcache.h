@@ -275,7 +275,8 @@ typedef struct {
  * is never drawn), and d's in two parts, as a multiple of 2^-50 and the rest as one
  * of 2^-76: equal calls give equal results however they are split. Entries of p, q outside 0..1 count as the nearer end, NaN as 0; so does u,
  * its upper end the largest number below 1.
- * path, count, next and the workspace must lie apart from the inputs and each other.
+ * path, count, next and the workspace must lie apart from the inputs (what lies
+ * between their rows counts as theirs) and each other.
  * A sequence without rows has count 0 and next -1. Reported by kvc_check: a
  * parent as in kvc_tree (of node 0, anything but -1), a drafted token outside the
  * vocabulary (passed over), a row of p without any weight (next -1), and rows as

@@ -240,7 +240,12 @@ inline int kv_check_apart(std::initializer_list<KvArray> arrays, int outputs, ch
     }
   return AGEMM_OK;
 }
-inline int64_t kv_rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? ((rows - 1) * stride + width) * 4 : 0; }
+// Of 4-byte elements, first to last, what lies between rows with them; 2^62 for more than that.
+inline int64_t kv_rows_bytes(int64_t rows, int64_t stride, int64_t width) {
+  if (rows < 1) return 0;
+  const __int128 bytes = ((__int128)(rows - 1) * stride + width) * 4;
+  return bytes < (int64_t{1} << 62) ? (int64_t)bytes : int64_t{1} << 62;
+}
 
 // Of calls that the checks above let pass.
 inline int kv_check_tree_apart(const kvc_tree_args* p, char* why) {

@@ -93,3 +93,13 @@ def test_workspace_of_a_verification_lies_apart(apart):
 def test_empty_arrays_lie_apart(apart):
     assert _apart(apart, "tree", {**TREE, "tokens": 0, **{k: A for k in ("mask", "positions", "slots", "parent")}}) == agemm.OK
     assert _apart(apart, "verify", {**VERIFY, "tokens": 0, "path": VERIFY["u"]}) == agemm.OK
+
+
+def test_extents_of_the_widest_strides_do_not_overflow(apart):
+    """Rows 2^40 elements apart, 2^23 of them: past 2^63 bytes."""
+    at = 1 << 45
+    far = {**VERIFY, "tokens": 1 << 23, "p_stride": 1 << 40, "q": None, **{k: at - (i + 1 << 26) for i, k in enumerate(
+        ("path", "count", "next", "q_start", "parent", "token", "u"))}, "p": at}
+    assert _apart(apart, "verify", far) == agemm.OK
+    assert _apart(apart, "verify", {**far, "next": at + (1 << 50)}) == agemm.EINVAL
+    assert _apart(apart, "verify", {**far, "p_stride": 0, "next": at + (1 << 50)}) == agemm.OK
