@@ -19,10 +19,10 @@
 // left, by a third of it), and 2^-50 is coarse for it too. So q is summed, as a
 // multiple of 2^-50 and what that is off by as one of 2^-76, exactly both (of up to
 // 2^28 numbers, the latter are below 2^-23 together), once a row, and the rejected
-// tokens are taken off in the same two parts. D is off by 2^-77 a token then; below 2^-57 a
-// token, where that might be a millionth of it, it counts as nothing. (To pass
-// over the drafts that follow leaves the distribution as it is: the rest is drawn
-// from w.)
+// tokens are taken off in the same two parts. D is off by 2^-77 a token then; below
+// 2^-57 a token, where that might be a millionth of it, it counts as nothing. (To
+// pass over the drafts that follow leaves the distribution as it is: the rest is
+// drawn from w.)
 //
 // Where no sum but the last is expected, the workgroups of a row's parts each walk
 // by themselves and sum, and a second kernel draws. Else one workgroup a sequence
@@ -487,11 +487,12 @@ __global__ __launch_bounds__(kThreads) void kv_verify_begin_kernel(KvVerifyArgs 
 }
 
 // The rounds: 16 trees of 25 drawn nodes on 131072 tokens take 33 to 37 us a call
-// where no tree wants more than four sums and 63 where one wants ten, 5.0 a turn, nearly
-// all of it latency (q's sum once a row is some 0.2 of it). What workgroups tell each other goes past the caches of their XCDs
-// (relaxed accesses at the device's scope), and is there before the counter or
-// turn that announces it: one wave stores and waits, which a release (the
-// write-back of all of the cache, 20 us a call of 1024 workgroups) would do too.
+// where no tree wants more than four sums and 63 where one wants ten, 5.0 a turn,
+// nearly all of it latency (without q's sums a call takes 1.4 to 2.1 less). What
+// workgroups tell each other goes past the caches of their XCDs (relaxed accesses at
+// the device's scope), and is there before the counter or turn that announces it: one
+// wave stores and waits, which a release (the write-back of all of the cache, 20 us a
+// call of 1024 workgroups) would do too.
 __device__ inline void stores_are_there() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0);
