@@ -895,8 +895,8 @@ __global__ __launch_bounds__(kWaves * 64, NT * D > 128 || NT > 1 ? 2 : 4) void k
 // vector units 50 % of the cycles, at 1.9 GHz of 2.4: power seems to hold the clock.
 // Binary32 out, which has twice the value products: 1394 us. D 64: 708 (binary32
 // 883), D 256 with half the heads: 1552 (1850), one block a tile there.
-// With a tree: 16 x 64 nodes of 64 heads (8 kv heads, D 128) on 8192 tokens in 292
-// to 299 us with the join, 0.91 to 0.93 PFLOP/s; 48 nodes of 96 heads on 131072, binary32 out,
+// With a tree: 16 x 64 nodes of 64 heads (8 kv heads, D 128) on 8192 tokens in 285
+// to 299 us with the join, 0.91 to 0.96 PFLOP/s; 48 nodes of 96 heads on 131072, binary32 out,
 // 491 to 508, of 271 for the products and 406 with the second part of the weights.
 template <int D, int W, bool F32, bool TREE>
 __global__ __launch_bounds__(W * 64, D > 128 ? 1 : 2) void kv_attend_many_kernel(KvAttendArgs a) {
